@@ -532,6 +532,99 @@ int mq_read_floor(const void *src, size_t bytes, void *stream);
  * the dispatch plan sizes its grid from it. */
 int mq_device_sms(void);
 
+/* ------------------------------------------------------------------------
+ * The rest of a decode step (device; no counterpart on the pages, which stop
+ * at the GEMVs): what lies between the q/k/v GEMVs and the o GEMV, and behind
+ * the output head.
+ *
+ * Paged KV cache.  The caller owns two arrays of pages, one for keys and one
+ * for values.  A page holds page_size consecutive tokens of one sequence for
+ * all kv heads; its bytes are head-major:
+ *   F16, BF16: [n_kv_heads][page_size][head_dim] values;
+ *   Q8: per head [page_size][head_dim] int8 codes, then
+ *       [page_size][head_dim / 32] fp16 scales: value = scale * code, one
+ *       block per 32 values, quantized as the q8 producers do.
+ * mq_kv_page_bytes: bytes of one page (0 on a bad type or shape).
+ * page_stride: bytes from one page to the next, the same in k and v (0: the
+ *   pages lie back to back); a multiple of 16 and at least a page.
+ * Shapes: head_dim 64, 96, 128 or 256; page_size a multiple of 16; n_pages
+ *   and n_kv_heads >= 1.
+ *
+ * Page tables.  pages[s * pages_stride + i] is the page of tokens
+ * [i * page_size, (i + 1) * page_size) of sequence s, 0 <= s < n_seqs,
+ * 0 <= i < pages_stride.  Row t of a call belongs to sequence seq[t], or to
+ * sequence t where seq is NULL.  Entries behind a sequence's last page are
+ * never read.  Tables, positions and lengths are device memory, 4-byte
+ * aligned, read by the kernel: a captured graph replays with their new values.
+ *
+ * Values on the device cannot be checked before the launch.  A row whose
+ * sequence, position, length or page is out of range does no access there:
+ * its f32 output becomes NaN, its cache write is left out, and 1 is OR-ed into
+ * *status (device int32, may be NULL; the caller clears it).
+ * ------------------------------------------------------------------------ */
+#define MQ_KV_F16 1
+#define MQ_KV_BF16 2
+#define MQ_KV_Q8 3
+
+typedef struct {
+    int type;              /* MQ_KV_F16, MQ_KV_BF16 or MQ_KV_Q8            */
+    int n_pages, page_size, n_kv_heads, head_dim;
+    void *k, *v;           /* the pages (device, 16-byte aligned)          */
+    long long page_stride; /* bytes between pages; 0: back to back         */
+} mq_kv_cache;
+
+size_t mq_kv_page_bytes(int type, int n_kv_heads, int page_size, int head_dim);
+
+/* ------------------------------------------------------------------------
+ * Rotation and append (device): nt rows of queries, keys and values, as the
+ * q/k/v GEMVs write them, to rotated queries (f32) and cache entries, in one
+ * launch.  For each head of a row:
+ *   x += bias                               (q_bias, k_bias, v_bias, may be NULL)
+ *   x = x / sqrt(mean(x^2) + eps) * gain    (q_gain, k_gain: head_dim f32, may be NULL)
+ *   rotate the first rope_dims values       (queries and keys)
+ *   queries -> q_out; keys and values -> the page of position positions[t],
+ *   rounded once (to nearest even).
+ * Rotation by angle phi_i = position * freq_i, 0 <= i < rope_dims / 2:
+ *   (a, b) -> (a cos phi - b sin phi, b cos phi + a sin phi) with (a, b) =
+ *   MQ_ROPE_HALF:  x[i], x[i + rope_dims / 2];
+ *   MQ_ROPE_PAIRS: x[2 i], x[2 i + 1].
+ * The angle is kept modulo one turn in 64-bit fixed point, so far positions
+ * lose nothing.  rope_table (device, 8-byte aligned) holds the rope_dims / 2
+ * steps that mq_rope_table (host) makes of freqs (radians per position).
+ * rope_dims: 0 (no rotation, rope_table may be NULL) to head_dim, a multiple
+ * of 8, of 16 where head_dim is 256.
+ * Rows with a negative position are padding: nothing of them is written.  Two
+ * rows of one call must not name the same sequence and position.  q_out may
+ * be q (the same rows); the other arrays must not overlap it.
+ * Strides are in values between rows, multiples of 4; q, k, v, q_out, biases
+ * and gains 16-byte aligned.  n_heads is a multiple of n_kv_heads; the entry
+ * takes any such ratio.
+ * Errors: MQ_ERR_NULL, MQ_ERR_SHAPE, MQ_ERR_ALIGN, MQ_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+#define MQ_ROPE_HALF 0
+#define MQ_ROPE_PAIRS 1
+
+typedef struct {
+    int nt, n_heads;                       /* rows; query heads            */
+    int rope_dims, rope_style;
+    float eps;
+    const float *q, *k, *v;                /* rows of n_heads / n_kv_heads heads */
+    long long q_stride, k_stride, v_stride;
+    float *q_out;
+    long long q_out_stride;
+    const float *q_bias, *k_bias, *v_bias; /* heads * head_dim, or NULL    */
+    const float *q_gain, *k_gain;          /* head_dim, or NULL            */
+    const uint64_t *rope_table;
+    const int *positions;                  /* [nt]                         */
+    const int *seq;                        /* [nt], or NULL                */
+    const int *pages;                      /* [n_seqs][pages_stride]       */
+    int n_seqs, pages_stride;
+    int *status;                           /* or NULL                      */
+} mq_rope_append_args;
+
+int mq_rope_table(const double *freqs, int n, uint64_t *table);
+int mq_rope_append(const mq_kv_cache *kv, const mq_rope_append_args *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

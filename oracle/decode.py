@@ -1,0 +1,110 @@
+"""Plain 64-bit numpy references of the operators around the GEMVs of a decode
+step: rotation and paged append, attention over a paged cache, the draw of a
+token.  TEST INFRASTRUCTURE ONLY, like the rest of this package; it imports
+nothing from the library and works on dense per-sequence arrays and on cache
+pages in the layouts that include/mq.h states.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+
+# ------------------------------------------------------------------ cache pages
+def unpack_pages(raw: np.ndarray, kv: str, ps: int, d: int) -> np.ndarray:
+    """Pages as stored -> [n_pages, heads, ps, d] float64.  raw: float16 values
+    (f16), uint16 bits (bf16) or uint8 bytes (q8: codes, then fp16 scales)."""
+    if kv == "f16":
+        return raw.astype(np.float64)
+    if kv == "bf16":
+        return (raw.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    n, h = raw.shape[:2]
+    codes = np.ascontiguousarray(raw[..., : ps * d]).view(np.int8).reshape(n, h, ps, d // 32, 32)
+    scale = np.ascontiguousarray(raw[..., ps * d:]).view(np.float16).reshape(n, h, ps, d // 32, 1)
+    return (codes.astype(np.float64) * scale.astype(np.float64)).reshape(n, h, ps, d)
+
+
+def gather(pages: np.ndarray, table_row, n: int) -> np.ndarray:
+    """The first n cached tokens of a sequence: [heads, n, d]."""
+    ps = pages.shape[2]
+    out = np.empty((pages.shape[1], n, pages.shape[3]))
+    for j in range(n):
+        out[:, j] = pages[table_row[j // ps], :, j % ps]
+    return out
+
+
+# ------------------------------------------------------------------ rotation and append
+def heads_of(x, bias, gain, eps, d):
+    """[nt, heads * d] -> [nt, heads, d] after bias and norm, and the same of
+    the magnitudes (|x| + |bias| in x's place), which bound the roundings."""
+    x = x.astype(np.float64)
+    mag = np.abs(x)
+    if bias is not None:
+        x, mag = x + bias.astype(np.float64), mag + np.abs(bias.astype(np.float64))
+    x, mag = x.reshape(len(x), -1, d), mag.reshape(len(x), -1, d)
+    if gain is not None:
+        s = gain.astype(np.float64) / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+        x, mag = x * s, mag * np.abs(s)
+    return x, mag
+
+
+def rotate(x, mag, pos, freqs, style):
+    """Rotated heads, and |a| + |b| of each value's pair (its own magnitude
+    where it is not rotated)."""
+    r = 2 * len(freqs)
+    phi = np.outer(np.asarray(pos, np.float64), np.asarray(freqs, np.float64))[:, None, :]
+    i = np.arange(r // 2)
+    ia, ib = (i, i + r // 2) if style == "half" else (2 * i, 2 * i + 1)
+    out, m = x.copy(), mag.copy()
+    out[..., ia] = x[..., ia] * np.cos(phi) - x[..., ib] * np.sin(phi)
+    out[..., ib] = x[..., ib] * np.cos(phi) + x[..., ia] * np.sin(phi)
+    m[..., ia] = m[..., ib] = mag[..., ia] + mag[..., ib]
+    return out, m
+
+
+# ------------------------------------------------------------------ attention
+def attention(q, k, v, scale, softcap=0.0, window=0):
+    """One query row [heads, d] over k, v [kv heads, n, d] (float64)."""
+    hq, d = q.shape
+    hkv, n, _ = k.shape
+    first = max(0, n - window) if window else 0
+    if n - first == 0:
+        return np.zeros((hq, d))
+    qg = q.astype(np.float64).reshape(hkv, hq // hkv, d)
+    s = np.einsum("hgd,hnd->hgn", qg, k[:, first:]) * scale
+    if softcap:
+        s = softcap * np.tanh(s / softcap)
+    e = np.exp(s - s.max(-1, keepdims=True))
+    return (np.einsum("hgn,hnd->hgd", e, v[:, first:]) / e.sum(-1, keepdims=True)).reshape(hq, d)
+
+
+# ------------------------------------------------------------------ sampling
+def sample(logits, u, t=1.0, k=0, p=1.0, m=0.0):
+    """(token, probability among the kept, kept mask, distance of the draw
+    from the nearest border of the token's interval).  NaN counts as -inf."""
+    x = np.where(np.isnan(logits), -np.inf, logits.astype(np.float64))
+    if x.max() == -np.inf:
+        return -1, 0.0, np.zeros(len(x), bool), np.inf
+    order = np.argsort(-x, kind="stable")
+    top = x[order[0]]
+    if t <= 0:
+        n, w = 1, np.ones(1)
+    else:
+        with np.errstate(invalid="ignore"):
+            z = np.where(x[order] == top, 0.0, (x[order] - top) / t)
+        w = np.exp(z)
+        n = len(x) if k <= 0 else min(k, len(x))
+        if p < 1:
+            c = np.cumsum(w[:n])
+            n = min(n, 1 + int(np.searchsorted(c, p * c[-1], "left")))
+        n = max(1, min(n, int((w >= m).sum())))
+        while n > 1 and w[n - 1] == 0.0:
+            n -= 1
+    kept = np.zeros(len(x), bool)
+    kept[order[:n]] = True
+    weight = np.zeros(len(x))
+    weight[order[:n]] = w[:n]
+    c = np.cumsum(weight)
+    at = int(np.searchsorted(c, u * c[-1], "right"))
+    at = min(at, int(np.flatnonzero(kept)[-1]))
+    lo = c[at] - weight[at]
+    return at, weight[at] / c[-1], kept, min(u * c[-1] - lo, c[at] - u * c[-1]) / c[-1]

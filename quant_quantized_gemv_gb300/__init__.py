@@ -35,6 +35,7 @@ EXPORTS = [
     "mq_gemv_q6k_q8_plan", "mq_gemv_q4k_q8_plan", "mq_gemv_workspace_bytes_for",
     "mq_check_coverage", "mq_gemv_plan_for", "mq_set_pdl", "mq_gemv_q6k_q8_noalloc",
     "mq_gemv_group_workspace_bytes", "mq_gemv_group_q8", "mq_gemv_group_q8_plan",
+    "mq_kv_page_bytes", "mq_rope_table", "mq_rope_append",
     "mq_gemv_q6k_q8_subdots",
     "mq_gemv_q4k_q8_subdots", "mq_device_sms",
     "mq_quantize_q8_batch", "mq_rmsnorm_quant_q8_batch", "mq_swiglu_quant_q8_batch",
@@ -142,6 +143,9 @@ def lib():
         "mq_device_address": ([P, ctypes.POINTER(ctypes.c_void_p)], I),
         "mq_repack_device": ([I, P, P, I, I, P], I),
         "mq_gemv_group_q8_coverage": ([P, I, P, I, I, I, I, P, S, P, P], I),
+        "mq_kv_page_bytes": ([I, I, I, I], S),
+        "mq_rope_table": ([P, I, P], I),
+        "mq_rope_append": ([P, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -709,3 +713,161 @@ def mq_gemv_q4k_q8_subdots(Wp, q8, rows: int, cols: int, stream=None):
 
 def mq_gemv_q5k_q8_subdots(Wp, q8, rows: int, cols: int, stream=None):
     return _subdots("mq_gemv_q5k_q8_subdots", 8, Wp, q8, rows, cols, stream)
+
+
+# ------------------------------------------------------------------ around the GEMVs of a decode step
+KV_TYPES = {"f16": 1, "bf16": 2, "q8": 3}
+ROPE_STYLES = {"half": 0, "pairs": 1}
+
+
+class _KVStruct(ctypes.Structure):
+    """mq_kv_cache of include/mq.h"""
+    _fields_ = ([("type", ctypes.c_int)]
+                + [(n, ctypes.c_int) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim")]
+                + [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_longlong)])
+
+
+class _RopeAppendStruct(ctypes.Structure):
+    """mq_rope_append_args of include/mq.h"""
+    _fields_ = ([(n, ctypes.c_int) for n in ("nt", "n_heads", "rope_dims", "rope_style")]
+                + [("eps", ctypes.c_float)]
+                + [(n, ctypes.c_void_p) for n in ("q", "k", "v")]
+                + [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "v_stride")]
+                + [("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("q_bias", "k_bias", "v_bias", "q_gain", "k_gain",
+                                                  "rope_table", "positions", "seq", "pages")]
+                + [("n_seqs", ctypes.c_int), ("pages_stride", ctypes.c_int), ("status", ctypes.c_void_p)])
+
+
+def mq_kv_page_bytes(kv_type: str, n_kv_heads: int, page_size: int, head_dim: int) -> int:
+    """Bytes of one cache page (0 on a bad shape)."""
+    return lib().mq_kv_page_bytes(KV_TYPES[kv_type], n_kv_heads, page_size, head_dim)
+
+
+class MQKVCache:
+    """A paged key-value cache: the pages of one layer and their description.
+
+    kv_type: "f16", "bf16" or "q8".  k, v: the pages, [n_pages, n_kv_heads,
+    page_size, head_dim] in that type, or uint8 [n_pages, n_kv_heads, bytes of
+    a head] for q8 (the codes, then the fp16 scales); a stride between pages
+    is allowed (k and v may lie in one array).  Made zero-filled when not given.
+    The object holds the tensors."""
+
+    def __init__(self, kv_type: str, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
+                 k=None, v=None, device=None):
+        import torch
+        if kv_type not in KV_TYPES:
+            raise ValueError(f"unknown cache type {kv_type!r}")
+        page = mq_kv_page_bytes(kv_type, n_kv_heads, page_size, head_dim)
+        if page == 0 or n_pages < 1:
+            raise MQError(MQ_ERR_SHAPE, "MQKVCache")
+        if kv_type == "q8":
+            dtype, shape = torch.uint8, (n_pages, n_kv_heads, page // n_kv_heads)
+        else:
+            dtype = torch.float16 if kv_type == "f16" else torch.bfloat16
+            shape = (n_pages, n_kv_heads, page_size, head_dim)
+        if (k is None) != (v is None):
+            raise ValueError("give both k and v, or neither")
+        if k is None:
+            k, v = (torch.zeros(shape, dtype=dtype, device=device or "cuda") for _ in range(2))
+        for t in (k, v):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError("expected a CUDA tensor (the library has no CPU path)")
+            if t.dtype != dtype or tuple(t.shape) != shape:
+                raise TypeError(f"expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+            if not t[0].is_contiguous():
+                raise ValueError("a page must be contiguous")
+        if k.device != v.device or (n_pages > 1 and k.stride(0) != v.stride(0)):
+            raise ValueError("k and v must lie on one device with the same page stride")
+        self.kv_type, self.k, self.v = kv_type, k, v
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
+        self.device_index = k.get_device()
+        stride = k.stride(0) * k.element_size() if n_pages > 1 else 0
+        self._struct = _KVStruct(KV_TYPES[kv_type], n_pages, page_size, n_kv_heads, head_dim,
+                                 k.data_ptr(), v.data_ptr(), stride)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _on_current(index: int):
+    """The calls below run on the current device; its index, if it is `index`."""
+    import torch
+    if torch.cuda.current_device() != index:
+        raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
+    return index
+
+
+def _raw_stream(stream, index: int) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _rows(t, nt, cols, dtype, index, what):
+    """The address of a [nt, cols] CUDA tensor whose rows are contiguous (any row stride)."""
+    if t.dtype is not dtype or t.get_device() != index:
+        raise TypeError(f"{what}: expected {dtype} on cuda:{index}, got {t.dtype} on {t.device}")
+    if t.dim() != 2 or t.shape[0] != nt or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected [{nt}, {cols}] with contiguous rows, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _vec(t, n, dtype, index, what):
+    """The address of a contiguous CUDA tensor of n values; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != index:
+        raise TypeError(f"{what}: expected {dtype} on cuda:{index}, got {t.dtype} on {t.device}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous values, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def mq_rope_table(freqs, device=None):
+    """The rotation's steps (a CUDA int64 tensor of 64-bit fractions of a turn)
+    for freqs, the radians per position of each pair."""
+    import torch
+    f = np.ascontiguousarray(freqs, dtype=np.float64).reshape(-1)
+    out = np.empty(f.size, np.uint64)
+    _check(lib().mq_rope_table(_np_ptr(f), f.size, _np_ptr(out)), "mq_rope_table")
+    return torch.from_numpy(out.view(np.int64)).to(device or "cuda")
+
+
+def mq_rope_append(kv: MQKVCache, q, k, v, positions, pages, q_out=None, rope=None, style: str = "half",
+                   q_bias=None, k_bias=None, v_bias=None, q_gain=None, k_gain=None, eps: float = 1e-6,
+                   seq=None, status=None, stream=None):
+    """Bias, per-head norm (q_gain, k_gain) and rotation of the rows q, k, v
+    ([nt, heads * head_dim] f32), and the append of k and v to the cache, in
+    one launch.  Returns the rotated queries q_out.
+
+    positions: int32 [nt] (negative: a padding row, left out); pages: int32
+    [sequences, pages per sequence]; seq: int32 [nt], the sequence of each
+    row (row t is sequence t when None); rope: mq_rope_table's steps (None:
+    no rotation); style: "half" or "pairs"; status: int32 [1], gets 1 OR-ed
+    in when a row names no valid page."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    dev, d, hkv = kv.device_index, kv.head_dim, kv.n_kv_heads
+    _on_current(dev)
+    nt, nq = q.shape
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=f32, device=q.device)
+    if pages.dim() != 2:
+        raise ValueError("pages: expected [sequences, pages per sequence]")
+    if seq is None and pages.shape[0] < nt:
+        raise ValueError(f"pages: {nt} rows but {pages.shape[0]} sequences")
+    if nq % d != 0:
+        raise ValueError(f"q: {nq} columns are no whole heads of {d}")
+    half = 0 if rope is None else rope.numel()
+    args = _RopeAppendStruct(
+        nt, nq // d, 2 * half, ROPE_STYLES[style], eps,
+        _rows(q, nt, nq, f32, dev, "q"), _rows(k, nt, hkv * d, f32, dev, "k"),
+        _rows(v, nt, hkv * d, f32, dev, "v"), q.stride(0) if nt > 1 else nq,
+        k.stride(0) if nt > 1 else hkv * d, v.stride(0) if nt > 1 else hkv * d,
+        _rows(q_out, nt, nq, f32, dev, "q_out"), q_out.stride(0) if nt > 1 else nq,
+        _vec(q_bias, nq, f32, dev, "q_bias"), _vec(k_bias, hkv * d, f32, dev, "k_bias"),
+        _vec(v_bias, hkv * d, f32, dev, "v_bias"), _vec(q_gain, d, f32, dev, "q_gain"),
+        _vec(k_gain, d, f32, dev, "k_gain"), _vec(rope, half, torch.int64, dev, "rope"),
+        _vec(positions, nt, i32, dev, "positions"), _vec(seq, nt, i32, dev, "seq"),
+        _vec(pages, pages.numel(), i32, dev, "pages"), pages.shape[0], pages.shape[1],
+        _vec(status, 1, i32, dev, "status"))
+    _check(lib().mq_rope_append(kv._ref, ctypes.byref(args), _raw_stream(stream, dev)), "mq_rope_append")
+    return q_out

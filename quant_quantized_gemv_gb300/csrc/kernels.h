@@ -197,6 +197,25 @@ cudaError_t launch_repack(int fmt, const void *src, void *dst, int rows, int col
 // (copy.cu), as a kernel that takes part in the launch chain.
 cudaError_t launch_copy(void *dst, const void *src, size_t bytes, int pdl, cudaStream_t st);
 
+// Rotation and paged append (rope_append.cu): nt rows of queries, keys and
+// values as mq_rope_append takes them, already checked.
+struct RopeAppendLaunch {
+    const float *q, *k, *v;
+    long long q_stride, k_stride, v_stride, q_out_stride;  // values between rows
+    float *q_out;
+    const float *q_bias, *k_bias, *v_bias, *q_gain, *k_gain;  // or null
+    const unsigned long long *rope_table;
+    const int *positions, *seq, *pages;  // seq may be null: row t is sequence t
+    int *status;                         // or null
+    uint8_t *k_pages, *v_pages;
+    size_t page_stride, head_bytes;      // bytes from page to page, from head to head in a page
+    int type, n_pages, page_size, n_kv_heads, head_dim;  // the cache (type: MQ_KV_*)
+    int nt, n_heads, rope_dims, style, n_seqs, pages_stride;
+    float eps;
+    int lanes_per_head, units, ctas_per_row;  // set by the launch
+};
+cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_t st);
+
 // The process-wide programmatic-dependent-launch setting (mq_set_pdl).
 int pdl_setting();
 

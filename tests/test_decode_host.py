@@ -1,0 +1,129 @@
+"""Host side of the operators around the GEMVs of a decode step, without a GPU:
+sizes, the rotation's table, and every refusal before a launch."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+NO_GPU = pytest.mark.skipif(__import__("torch").cuda.is_available(),
+                            reason="fake device pointers are only passed where no GPU exists")
+
+
+@pytest.fixture(scope="module")
+def mq():
+    from quant_quantized_gemv_gb300 import build
+    build.build()
+    import quant_quantized_gemv_gb300 as m
+    m.lib()
+    return m
+
+
+def test_page_bytes(mq):
+    assert mq.mq_kv_page_bytes("f16", 8, 16, 128) == 8 * 16 * 128 * 2
+    assert mq.mq_kv_page_bytes("bf16", 1, 48, 96) == 48 * 96 * 2
+    assert mq.mq_kv_page_bytes("q8", 4, 32, 64) == 4 * 32 * (64 + 4)
+    for bad in (("f16", 0, 16, 128), ("f16", 8, 0, 128), ("f16", 8, 24, 128), ("f16", 8, 16, 80),
+                ("f16", -1, 16, 128), ("q8", 8, -16, 128)):
+        assert mq.mq_kv_page_bytes(*bad) == 0, bad
+    assert mq.lib().mq_kv_page_bytes(4, 8, 16, 128) == 0
+
+
+def table_of(mq, freqs):
+    f = np.asarray(freqs, np.float64)
+    out = np.zeros(f.size, np.uint64)
+    st = mq.lib().mq_rope_table(f.ctypes.data_as(ctypes.c_void_p), f.size, out.ctypes.data_as(ctypes.c_void_p))
+    assert st == mq.MQ_OK
+    return out
+
+
+def test_rope_table_is_the_fraction_of_a_turn(mq):
+    freqs = [1.0, 0.5, 1e-6, 0.0, 2 * math.pi, 7.0, -1.0, 1e6 ** (-126 / 128)]
+    for f, got in zip(freqs, table_of(mq, freqs)):
+        want = f / (2 * math.pi)
+        diff = (int(got) / 2 ** 64 - want) % 1.0
+        # one division and one subtraction in 53 bits; 2^-64 of the truncation
+        assert min(diff, 1 - diff) <= 2.0 ** -52 * max(1.0, abs(want)), f
+
+
+def test_rope_table_angle_at_far_positions(mq):
+    """position * F mod 2^64 is the angle: checked in exact integers against
+    the fraction of position * freq / 2 pi in 80 digits."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 80
+    two_pi = Decimal("6.28318530717958647692528676655900576839433879875021164194988918461563")
+    freqs = [1e6 ** (-2 * i / 128) for i in range(64)]
+    for f, F in zip(freqs, table_of(mq, freqs)):
+        for pos in (1, 4097, 1 << 20, 2 ** 31 - 1):
+            turns = Decimal(pos) * Decimal(f) / two_pi
+            want = turns - int(turns)
+            got = Decimal((pos * int(F)) % 2 ** 64) / Decimal(2 ** 64)
+            diff = abs(got - want)
+            # the step's division rounds twice at 2^-53 of f / 2 pi < f, and its last
+            # bit is 2^-64 of a turn (truncated); the product is exact
+            tol = Decimal(pos) * (Decimal(2) ** -52 * Decimal(f) + Decimal(2) ** -64)
+            assert min(diff, 1 - diff) <= tol, (f, pos)
+
+
+def test_rope_table_refusals(mq):
+    L, one = mq.lib(), np.ones(1)
+    p = one.ctypes.data_as(ctypes.c_void_p)
+    assert L.mq_rope_table(None, 1, p) == mq.MQ_ERR_NULL
+    assert L.mq_rope_table(p, 1, None) == mq.MQ_ERR_NULL
+    assert L.mq_rope_table(p, 0, p) == mq.MQ_ERR_SHAPE
+    for bad in (math.inf, math.nan):
+        b = np.array([bad])
+        assert L.mq_rope_table(b.ctypes.data_as(ctypes.c_void_p), 1, p) == mq.MQ_ERR_SHAPE
+
+
+def cache(mq, **kw):
+    a = dict(type=1, n_pages=4, page_size=16, n_kv_heads=2, head_dim=128, k=0x10000, v=0x20000, page_stride=0)
+    a.update(kw)
+    return mq._KVStruct(**a)
+
+
+BAD_CACHES = [(dict(k=None), "NULL"), (dict(v=None), "NULL"), (dict(type=0), "SHAPE"), (dict(type=4), "SHAPE"),
+              (dict(n_pages=0), "SHAPE"), (dict(page_size=24), "SHAPE"), (dict(head_dim=80), "SHAPE"),
+              (dict(n_kv_heads=0), "SHAPE"), (dict(page_stride=-16), "SHAPE"), (dict(page_stride=16), "SHAPE"),
+              (dict(page_stride=2 * 16 * 128 * 2 + 8), "ALIGN"), (dict(k=0x10008), "ALIGN"), (dict(v=0x20002), "ALIGN")]
+
+
+def append_args(mq, **kw):
+    a = dict(nt=1, n_heads=4, rope_dims=128, rope_style=0, eps=1e-6, q=0x30000, k=0x40000, v=0x50000,
+             q_stride=512, k_stride=256, v_stride=256, q_out=0x60000, q_out_stride=512, rope_table=0x70000,
+             positions=0x80000, pages=0x90000, n_seqs=1, pages_stride=4)
+    a.update(kw)
+    return mq._RopeAppendStruct(**a)
+
+
+@NO_GPU
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_append_refuses_a_bad_cache(mq, bad, status):
+    st = mq.lib().mq_rope_append(ctypes.byref(cache(mq, **bad)), ctypes.byref(append_args(mq)), None)
+    assert st == getattr(mq, "MQ_ERR_" + status)
+
+
+@NO_GPU
+@pytest.mark.parametrize("bad,status", [
+    (dict(nt=0), "SHAPE"), (dict(nt=-1), "SHAPE"), (dict(n_heads=0), "SHAPE"), (dict(n_heads=3), "SHAPE"),
+    (dict(nt=2 ** 31 - 1), "SHAPE"), (dict(rope_dims=-8), "SHAPE"), (dict(rope_dims=136), "SHAPE"),
+    (dict(rope_dims=4), "SHAPE"), (dict(rope_style=2), "SHAPE"), (dict(rope_style=-1), "SHAPE"),
+    (dict(n_seqs=0), "SHAPE"), (dict(pages_stride=0), "SHAPE"), (dict(q_stride=508), "SHAPE"),
+    (dict(q_out_stride=0), "SHAPE"), (dict(k_stride=252), "SHAPE"), (dict(v_stride=-256), "SHAPE"),
+    (dict(q=None), "NULL"), (dict(k=None), "NULL"), (dict(v=None), "NULL"), (dict(q_out=None), "NULL"),
+    (dict(positions=None), "NULL"), (dict(pages=None), "NULL"), (dict(rope_table=None), "NULL"),
+    (dict(q=0x30004), "ALIGN"), (dict(q_out=0x60008), "ALIGN"), (dict(k_bias=0x10004), "ALIGN"),
+    (dict(q_gain=0x10008), "ALIGN"), (dict(q_stride=514), "ALIGN"), (dict(v_stride=257), "ALIGN"),
+    (dict(rope_table=0x70004), "ALIGN"), (dict(positions=0x80002), "ALIGN"), (dict(status=0x80001), "ALIGN")])
+def test_append_refuses_bad_arguments(mq, bad, status):
+    st = mq.lib().mq_rope_append(ctypes.byref(cache(mq)), ctypes.byref(append_args(mq, **bad)), None)
+    assert st == getattr(mq, "MQ_ERR_" + status)
+
+
+@NO_GPU
+def test_append_refuses_null_structs_and_odd_wide_rotations(mq):
+    L = mq.lib()
+    assert L.mq_rope_append(None, ctypes.byref(append_args(mq)), None) == mq.MQ_ERR_NULL
+    assert L.mq_rope_append(ctypes.byref(cache(mq)), None, None) == mq.MQ_ERR_NULL
+    wide = append_args(mq, rope_dims=24, q_stride=1024, q_out_stride=1024, k_stride=512, v_stride=512)
+    assert L.mq_rope_append(ctypes.byref(cache(mq, head_dim=256)), ctypes.byref(wide), None) == mq.MQ_ERR_SHAPE
