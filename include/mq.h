@@ -625,6 +625,56 @@ typedef struct {
 int mq_rope_table(const double *freqs, int n, uint64_t *table);
 int mq_rope_append(const mq_kv_cache *kv, const mq_rope_append_args *args, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Attention of one new token per row over the paged cache (device), split
+ * over the cache's length and joined in the same launch.  For row t, query
+ * head h and its kv head h / (n_heads / n_kv_heads), with n = lens[t]:
+ *   s_j = scale * (q . k_j), or softcap * tanh(that / softcap) if softcap > 0,
+ *   for tokens j in [max(0, n - window), n) (window 0: all of them);
+ *   out = sum_j exp(s_j - max s) v_j / sum_j exp(s_j - max s).
+ * n counts the cached tokens the row sees, its own among them.  n == 0, or
+ * scores that are all -inf: the row is 0.  n < 0: the row is padding and
+ * nothing of it is written.  Cached values outside the tokens above are never
+ * used, whatever they hold.  Several rows may name one sequence with lengths
+ * of their own (the tokens of a speculative step).
+ * Products with the cache are exact to f32 (queries and probabilities go
+ * through the tensor cores in two fp16 or three bf16 parts); statistics and
+ * sums are f32.  The result does not depend on the run (the order is fixed).
+ *   max_len: no row is longer; the launch and its split are sized by it.  A
+ *     longer row is out of range (see above).
+ *   q, out: rows of n_heads * head_dim f32, strides in values, multiples of 4.
+ *   q8: NULL, or nt planes of n_heads * head_dim values back to back
+ *     (mq_q8_bytes each): out's quantization, what mq_quantize_q8_batch gives.
+ *   ws: mq_attn_workspace_bytes(kv, n_heads, nt, max_len) bytes or more (a
+ *     workspace sized for larger nt and max_len serves), device, 16-byte aligned,
+ *     zero-filled before its first use; every completed call leaves its counters
+ *     zero.  NULL when 0 bytes are needed.  Calls that share a workspace,
+ *     replayed graphs among them, must be ordered on one stream.
+ * Shapes: n_heads a multiple of n_kv_heads; max_len >= 1; window >= 0;
+ *   softcap >= 0; scale and softcap finite.
+ * Errors: MQ_ERR_NULL, MQ_ERR_SHAPE, MQ_ERR_ALIGN, MQ_ERR_WORKSPACE,
+ *         MQ_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int nt, n_heads;               /* rows; query heads                    */
+    int max_len, window;
+    float scale, softcap;
+    const float *q;
+    float *out;
+    long long q_stride, out_stride;
+    void *q8;                      /* or NULL                              */
+    const int *lens;               /* [nt]                                 */
+    const int *seq;                /* [nt], or NULL                        */
+    const int *pages;              /* [n_seqs][pages_stride]               */
+    int n_seqs, pages_stride;
+    void *ws;
+    size_t ws_bytes;
+    int *status;                   /* or NULL                              */
+} mq_attn_args;
+
+size_t mq_attn_workspace_bytes(const mq_kv_cache *kv, int n_heads, int nt, int max_len);
+int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

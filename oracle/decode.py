@@ -25,11 +25,9 @@ def unpack_pages(raw: np.ndarray, kv: str, ps: int, d: int) -> np.ndarray:
 
 def gather(pages: np.ndarray, table_row, n: int) -> np.ndarray:
     """The first n cached tokens of a sequence: [heads, n, d]."""
-    ps = pages.shape[2]
-    out = np.empty((pages.shape[1], n, pages.shape[3]))
-    for j in range(n):
-        out[:, j] = pages[table_row[j // ps], :, j % ps]
-    return out
+    _, h, ps, d = pages.shape
+    used = np.asarray(table_row[: -(-n // ps)], np.int64)
+    return pages[used].transpose(1, 0, 2, 3).reshape(h, -1, d)[:, :n]
 
 
 # ------------------------------------------------------------------ rotation and append
@@ -62,19 +60,51 @@ def rotate(x, mag, pos, freqs, style):
 
 
 # ------------------------------------------------------------------ attention
-def attention(q, k, v, scale, softcap=0.0, window=0):
-    """One query row [heads, d] over k, v [kv heads, n, d] (float64)."""
+def attention(q, k, v, scale, softcap=0.0, window=0, parts=False):
+    """One query row [heads, d] over k, v [kv heads, n, d] (float64).  parts:
+    also the probabilities, |score| sums and v that an error bound needs."""
     hq, d = q.shape
     hkv, n, _ = k.shape
     first = max(0, n - window) if window else 0
     if n - first == 0:
-        return np.zeros((hq, d))
+        return (np.zeros((hq, d)), None) if parts else np.zeros((hq, d))
     qg = q.astype(np.float64).reshape(hkv, hq // hkv, d)
-    s = np.einsum("hgd,hnd->hgn", qg, k[:, first:]) * scale
+    s = np.matmul(qg, k[:, first:].transpose(0, 2, 1)) * scale
     if softcap:
         s = softcap * np.tanh(s / softcap)
     e = np.exp(s - s.max(-1, keepdims=True))
-    return (np.einsum("hgn,hnd->hgd", e, v[:, first:]) / e.sum(-1, keepdims=True)).reshape(hq, d)
+    e /= e.sum(-1, keepdims=True)
+    out = np.matmul(e, v[:, first:]).reshape(hq, d)
+    if not parts:
+        return out
+    mag = np.matmul(np.abs(qg), np.abs(k[:, first:]).transpose(0, 2, 1)) * abs(scale)
+    return out, (e, mag, s.max(-1, keepdims=True) - s, v[:, first:])
+
+
+def attention_bound(out, parts, softcap=0.0):
+    """How far an f32 evaluation of `attention` with exact products may be off,
+    value by value, in units of 2^-24:
+    a score: q's parts (2^-22) 4, 16 sums of the products (truncating, 2^-23) 32,
+      the factor 3, all of sum |q k| scale; the difference to the maximum 2 of it;
+      a capped score: tanh 4 and two products of the cap;
+    a probability: its score's error, exp2 4, its split 4, one rescaling product
+      a tile is common to the sum and cancels but for its rounding: taken as 16;
+    the sums over tokens: 2 a tile of 16 of a warp's quarter, of sum p |v|; the
+    division and the join 16;
+    and, not relative to p: its fp16 parts end at fp16's last step, 2^-25 under
+    a factor of 2^14 (and of up to 2 of the largest value in a q8 tile), so a
+    term is off by up to 2^-38 max |v| however small p is (f32 itself ends at
+    2^-126)."""
+    if parts is None:
+        return np.zeros_like(out)
+    e, mag, gap, v = parts
+    n = e.shape[-1]
+    r = 39 * mag + 2 * gap + 24 + 6 * softcap
+    hkv, grp, _ = e.shape
+    pv = np.matmul(e * (r + n / 32 + 16), np.abs(v))       # each term's own error
+    common = (e * r).sum(-1, keepdims=True)                              # the sum that divides
+    floor = 2.0 ** -38 * n * np.abs(v).max(axis=(1, 2), keepdims=True)
+    return (2.0 ** -24 * (pv + common * np.matmul(e, np.abs(v))) + floor).reshape(out.shape)
 
 
 # ------------------------------------------------------------------ sampling

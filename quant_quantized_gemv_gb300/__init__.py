@@ -36,6 +36,7 @@ EXPORTS = [
     "mq_check_coverage", "mq_gemv_plan_for", "mq_set_pdl", "mq_gemv_q6k_q8_noalloc",
     "mq_gemv_group_workspace_bytes", "mq_gemv_group_q8", "mq_gemv_group_q8_plan",
     "mq_kv_page_bytes", "mq_rope_table", "mq_rope_append",
+    "mq_attn_workspace_bytes", "mq_attn_decode",
     "mq_gemv_q6k_q8_subdots",
     "mq_gemv_q4k_q8_subdots", "mq_device_sms",
     "mq_quantize_q8_batch", "mq_rmsnorm_quant_q8_batch", "mq_swiglu_quant_q8_batch",
@@ -146,6 +147,8 @@ def lib():
         "mq_kv_page_bytes": ([I, I, I, I], S),
         "mq_rope_table": ([P, I, P], I),
         "mq_rope_append": ([P, P, P], I),
+        "mq_attn_workspace_bytes": ([P, I, I, I], S),
+        "mq_attn_decode": ([P, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -739,6 +742,17 @@ class _RopeAppendStruct(ctypes.Structure):
                 + [("n_seqs", ctypes.c_int), ("pages_stride", ctypes.c_int), ("status", ctypes.c_void_p)])
 
 
+class _AttnStruct(ctypes.Structure):
+    """mq_attn_args of include/mq.h"""
+    _fields_ = ([(n, ctypes.c_int) for n in ("nt", "n_heads", "max_len", "window")]
+                + [(n, ctypes.c_float) for n in ("scale", "softcap")]
+                + [("q", ctypes.c_void_p), ("out", ctypes.c_void_p)]
+                + [("q_stride", ctypes.c_longlong), ("out_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("q8", "lens", "seq", "pages")]
+                + [("n_seqs", ctypes.c_int), ("pages_stride", ctypes.c_int)]
+                + [("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p)])
+
+
 def mq_kv_page_bytes(kv_type: str, n_kv_heads: int, page_size: int, head_dim: int) -> int:
     """Bytes of one cache page (0 on a bad shape)."""
     return lib().mq_kv_page_bytes(KV_TYPES[kv_type], n_kv_heads, page_size, head_dim)
@@ -871,3 +885,59 @@ def mq_rope_append(kv: MQKVCache, q, k, v, positions, pages, q_out=None, rope=No
         _vec(status, 1, i32, dev, "status"))
     _check(lib().mq_rope_append(kv._ref, ctypes.byref(args), _raw_stream(stream, dev)), "mq_rope_append")
     return q_out
+
+
+def mq_attn_workspace_bytes(kv: MQKVCache, n_heads: int, nt: int, max_len: int) -> int:
+    """Workspace bytes of mq_attn_decode for up to nt rows of up to max_len cached tokens."""
+    return lib().mq_attn_workspace_bytes(kv._ref, n_heads, nt, max_len)
+
+
+def mq_attn_workspace(kv: MQKVCache, n_heads: int, nt: int, max_len: int):
+    """A zero-filled workspace of that size (None when not needed)."""
+    import torch
+    nbytes = mq_attn_workspace_bytes(kv, n_heads, nt, max_len)
+    return None if nbytes == 0 else torch.zeros(nbytes, dtype=torch.uint8, device=kv.k.device)
+
+
+def mq_attn_decode(kv: MQKVCache, q, lens, pages, scale: float, out=None, q8=None, ws=None,
+                   softcap: float = 0.0, window: int = 0, max_len: int = None, seq=None, status=None,
+                   stream=None):
+    """Attention of the rows q ([nt, heads * head_dim] f32, one new token each)
+    over their cached tokens, in one launch; returns out (f32, the same shape).
+
+    lens: int32 [nt], the cached tokens each row sees (0: the row is 0;
+    negative: a padding row, left as it is); pages, seq, status: as
+    mq_rope_append; max_len: no row is longer (None: what the page table
+    holds); q8: a uint8 tensor that gets nt q8 planes of out; ws: from
+    mq_attn_workspace (made for this call when None and one is needed)."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    dev, d = kv.device_index, kv.head_dim
+    _on_current(dev)
+    nt, nq = q.shape
+    if out is None:
+        out = torch.empty(q.shape, dtype=f32, device=q.device)
+    if pages.dim() != 2:
+        raise ValueError("pages: expected [sequences, pages per sequence]")
+    if seq is None and pages.shape[0] < nt:
+        raise ValueError(f"pages: {nt} rows but {pages.shape[0]} sequences")
+    if nq % d != 0:
+        raise ValueError(f"q: {nq} columns are no whole heads of {d}")
+    if max_len is None:
+        max_len = pages.shape[1] * kv.page_size
+    if q8 is not None:
+        _vec(q8, q8.numel(), torch.uint8, dev, "q8")
+        if q8.numel() < nt * mq_q8_bytes(nq):
+            raise ValueError(f"q8: smaller than {nt} planes of {nq} values")
+    if ws is None:
+        ws = mq_attn_workspace(kv, nq // d, nt, max_len)
+    wsb = 0 if ws is None else ws.numel() * ws.element_size()
+    args = _AttnStruct(
+        nt, nq // d, max_len, window, scale, softcap, _rows(q, nt, nq, f32, dev, "q"),
+        _rows(out, nt, nq, f32, dev, "out"), q.stride(0) if nt > 1 else nq, out.stride(0) if nt > 1 else nq,
+        None if q8 is None else q8.data_ptr(), _vec(lens, nt, i32, dev, "lens"), _vec(seq, nt, i32, dev, "seq"),
+        _vec(pages, pages.numel(), i32, dev, "pages"), pages.shape[0], pages.shape[1],
+        None if ws is None else _vec(ws, ws.numel(), torch.uint8, dev, "ws"), wsb,
+        _vec(status, 1, i32, dev, "status"))
+    _check(lib().mq_attn_decode(kv._ref, ctypes.byref(args), _raw_stream(stream, dev)), "mq_attn_decode")
+    return out

@@ -1,11 +1,12 @@
 // decode.cpp -- the C ABI of the operators around the GEMVs of a decode step
-// (include/mq.h: paged cache, rotation and append): argument checks, then the
-// launch.  Nothing here allocates.
+// (include/mq.h: paged cache, rotation and append, attention): argument checks,
+// the attention's split, then the launch.  Nothing here allocates.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "kernels.h"
+#include "layout.h"
 #include "mq.h"
 
 namespace {
@@ -35,6 +36,71 @@ int kv_check(const mq_kv_cache *kv, size_t *page_stride, size_t *head_bytes)
     *page_stride = kv->page_stride ? (size_t)kv->page_stride : page;
     *head_bytes = kv_head_bytes(kv->type, kv->page_size, kv->head_dim);
     return MQ_OK;
+}
+
+// How the tokens of an attention call are cut: pieces of a unit (a row's group
+// of up to 8 heads of one kv head) and tokens of a piece, for `span` tokens at
+// the most.  Few units: as many pieces as fill the GPU once, of 64 tokens or
+// more.  Many: pieces of 1024 tokens or more, up to a few waves, so that ragged
+// rows even out.
+struct AttnPlan {
+    int pieces, piece_len;
+};
+
+constexpr long long kPieceQuantum = kAttnWarps * kAttnTile;  // a piece is whole rounds of its warps
+constexpr int kAttnWaves = 4;
+
+long long attn_wave(int sms) { return (long long)sms * 3; }  // CTAs resident at once
+
+AttnPlan attn_plan(long long units, long long span, int sms)
+{
+    const long long rounds = (span + kPieceQuantum - 1) / kPieceQuantum;
+    long long few = attn_wave(sms) / units, many = kAttnWaves * attn_wave(sms) / units;
+    if (few > rounds) few = rounds;
+    if (many > span / 1024) many = span / 1024;
+    long long pieces = few > many ? few : many;
+    if (pieces > kAttnMaxPieces) pieces = kAttnMaxPieces;
+    if (pieces < 1) pieces = 1;
+    const long long len = (rounds + pieces - 1) / pieces * kPieceQuantum;
+    return AttnPlan{(int)((span + len - 1) / len), (int)len};
+}
+
+// Workspace of calls of up to `units` units and max_len tokens, any window.
+// First the arrival counters, in a place and number that no call changes (a
+// workspace may serve calls of different sizes, and every counter must be zero
+// before each): units of 2 pieces or more number at most half of all the CTAs
+// planned.  Then the partial results: at most units x the pieces of the
+// longest row, and never more than the CTAs planned; both bounds only grow with
+// units and max_len.
+size_t attn_count_bytes(int sms)
+{
+    return ((size_t)(kAttnWaves * attn_wave(sms) / 2) * 4 + 15) & ~(size_t)15;
+}
+
+size_t attn_ws_bytes(long long units, int max_len, int sms, int head_dim)
+{
+    const long long span = (long long)max_len + kAttnTile - 1;
+    long long most = (span + kPieceQuantum - 1) / kPieceQuantum;
+    if (max_len <= kPieceQuantum) return 0;
+    if (most > kAttnMaxPieces) most = kAttnMaxPieces;
+    long long parts = units * most;
+    if (parts > kAttnWaves * attn_wave(sms)) parts = kAttnWaves * attn_wave(sms);
+    return attn_count_bytes(sms) + (size_t)parts * attn_part_floats(head_dim) * 4;
+}
+
+bool attn_shape_ok(const mq_kv_cache *kv, int n_heads, int nt, int max_len)
+{
+    if (mq_kv_page_bytes(kv->type, kv->n_kv_heads, kv->page_size, kv->head_dim) == 0) return false;
+    if (nt < 1 || n_heads < 1 || n_heads % kv->n_kv_heads != 0 || max_len < 1) return false;
+    if (max_len > 0x7fffffff - 4096) return false;
+    // the grid: every unit in its most pieces; a q8 plane's values
+    return (long long)nt * n_heads < (1LL << 24) && (long long)n_heads * kv->head_dim < (1LL << 30);
+}
+
+long long attn_units(const mq_kv_cache *kv, int n_heads, int nt)
+{
+    const int group = n_heads / kv->n_kv_heads;
+    return (long long)nt * kv->n_kv_heads * ((group + kAttnHeads - 1) / kAttnHeads);
 }
 
 }  // namespace
@@ -107,6 +173,63 @@ int mq_rope_append(const mq_kv_cache *kv, const mq_rope_append_args *a, void *st
     r.n_seqs = a->n_seqs, r.pages_stride = a->pages_stride, r.eps = a->eps;
     const cudaError_t e = launch_rope_append(r, sms, pdl_setting(), (cudaStream_t)stream);
     return e == cudaSuccess ? MQ_OK : cuda_fail("rope_append launch", e);
+}
+
+size_t mq_attn_workspace_bytes(const mq_kv_cache *kv, int n_heads, int nt, int max_len)
+{
+    if (!kv || !attn_shape_ok(kv, n_heads, nt, max_len)) return 0;
+    const int sms = mq_device_sms();
+    if (sms <= 0) return 0;
+    return attn_ws_bytes(attn_units(kv, n_heads, nt), max_len, sms, kv->head_dim);
+}
+
+int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *a, void *stream)
+{
+    if (!kv || !a) return MQ_ERR_NULL;
+    size_t page_stride, head_bytes;
+    const int st = kv_check(kv, &page_stride, &head_bytes);
+    if (st != MQ_OK) return st;
+    if (!a->q || !a->out || !a->lens || !a->pages) return MQ_ERR_NULL;
+    if (!attn_shape_ok(kv, a->n_heads, a->nt, a->max_len)) return MQ_ERR_SHAPE;
+    const int D = kv->head_dim, n = a->n_heads * D;
+    if (a->n_seqs < 1 || a->pages_stride < 1 || a->window < 0 || !isfinite(a->scale) ||
+        !isfinite(a->softcap) || a->softcap < 0.0f || a->q_stride < n || a->out_stride < n)
+        return MQ_ERR_SHAPE;
+    if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->q8, 16) || !aligned(a->ws, 16) ||
+        (a->q_stride | a->out_stride) % 4 != 0 || !aligned(a->lens, 4) || !aligned(a->seq, 4) ||
+        !aligned(a->pages, 4) || !aligned(a->status, 4))
+        return MQ_ERR_ALIGN;
+    const int sms = mq_device_sms();
+    if (sms <= 0) return MQ_ERR_CUDA;
+    AttnLaunch r = {};
+    r.group = a->n_heads / kv->n_kv_heads;
+    r.subgroups = (r.group + kAttnHeads - 1) / kAttnHeads;
+    const long long units = attn_units(kv, a->n_heads, a->nt);
+    // a window starts inside a tile of its own
+    long long span = a->max_len;
+    if (a->window > 0 && (long long)a->window + kAttnTile - 1 < span) span = (long long)a->window + kAttnTile - 1;
+    const AttnPlan plan = attn_plan(units, span, sms);
+    if (plan.pieces > 1) {
+        if (!a->ws) return MQ_ERR_NULL;
+        if (a->ws_bytes < attn_count_bytes(sms) + (size_t)units * plan.pieces * attn_part_floats(D) * 4)
+            return MQ_ERR_WORKSPACE;
+    }
+    r.pieces = plan.pieces, r.piece_len = plan.piece_len;
+    r.ws_cnt = (unsigned *)a->ws;
+    r.ws_part = plan.pieces > 1 ? (float *)((uint8_t *)a->ws + attn_count_bytes(sms)) : nullptr;
+    r.q = a->q, r.out = a->out, r.q_stride = a->q_stride, r.out_stride = a->out_stride;
+    r.q8 = (uint8_t *)a->q8;
+    r.q8_stride = (unsigned)q8_plane_bytes(n);
+    r.q8_d_off = (unsigned)q8_d_offset(n), r.q8_sum_off = (unsigned)q8_sum_offset(n);
+    r.lens = a->lens, r.seq = a->seq, r.pages = a->pages, r.status = a->status;
+    r.k_pages = (const uint8_t *)kv->k, r.v_pages = (const uint8_t *)kv->v;
+    r.page_stride = page_stride, r.head_bytes = head_bytes;
+    r.type = kv->type, r.n_pages = kv->n_pages, r.page_size = kv->page_size;
+    r.n_kv_heads = kv->n_kv_heads, r.head_dim = D;
+    r.nt = a->nt, r.n_heads = a->n_heads, r.n_seqs = a->n_seqs, r.pages_stride = a->pages_stride;
+    r.max_len = a->max_len, r.window = a->window, r.scale = a->scale, r.softcap = a->softcap;
+    const cudaError_t e = launch_attn_decode(r, pdl_setting(), (cudaStream_t)stream);
+    return e == cudaSuccess ? MQ_OK : cuda_fail("attn_decode launch", e);
 }
 
 }  // extern "C"

@@ -216,6 +216,37 @@ struct RopeAppendLaunch {
 };
 cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_t st);
 
+// Attention over the paged cache (attn_decode.cu), already checked.  A unit
+// is a row's group of up to kAttnHeads query heads of one kv head; its tokens
+// are cut into pieces of piece_len, one CTA each.  Units of more than one
+// piece leave partial results in ws_part (attn_part_floats each) and the
+// piece that arrives last joins them.
+constexpr int kAttnHeads = 8;        // query heads of a CTA (rows of its matrix products)
+constexpr int kAttnWarps = 4;        // warps of a CTA
+constexpr int kAttnTile = 16;        // tokens a warp takes at a time
+constexpr int kAttnMaxPieces = 128;  // most pieces of a unit
+constexpr int attn_part_floats(int head_dim) { return kAttnHeads * (head_dim + 2); }
+
+struct AttnLaunch {
+    const float *q;
+    float *out;
+    long long q_stride, out_stride;  // values between rows
+    uint8_t *q8;                     // planes of out, or null
+    unsigned q8_stride, q8_d_off, q8_sum_off;
+    const int *lens, *seq, *pages;   // seq may be null: row t is sequence t
+    int *status;                     // or null
+    const uint8_t *k_pages, *v_pages;
+    size_t page_stride, head_bytes;
+    int type, n_pages, page_size, n_kv_heads, head_dim;
+    int nt, n_heads, n_seqs, pages_stride, max_len, window;
+    float scale, softcap;
+    int group, subgroups;            // query heads of a kv head; CTAs' groups of 8 in it
+    int pieces, piece_len;
+    unsigned *ws_cnt;                // arrivals, one per unit
+    float *ws_part;
+};
+cudaError_t launch_attn_decode(const AttnLaunch &a, int pdl, cudaStream_t st);
+
 // The process-wide programmatic-dependent-launch setting (mq_set_pdl).
 int pdl_setting();
 

@@ -127,3 +127,44 @@ def test_append_refuses_null_structs_and_odd_wide_rotations(mq):
     assert L.mq_rope_append(ctypes.byref(cache(mq)), None, None) == mq.MQ_ERR_NULL
     wide = append_args(mq, rope_dims=24, q_stride=1024, q_out_stride=1024, k_stride=512, v_stride=512)
     assert L.mq_rope_append(ctypes.byref(cache(mq, head_dim=256)), ctypes.byref(wide), None) == mq.MQ_ERR_SHAPE
+
+
+def attn_args(mq, **kw):
+    a = dict(nt=1, n_heads=4, max_len=1000, window=0, scale=0.1, softcap=0.0, q=0x30000, out=0x40000,
+             q_stride=512, out_stride=512, lens=0x50000, pages=0x60000, n_seqs=1, pages_stride=64, ws=0x70000,
+             ws_bytes=1 << 30)
+    a.update(kw)
+    return mq._AttnStruct(**a)
+
+
+@NO_GPU
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_attention_refuses_a_bad_cache(mq, bad, status):
+    st = mq.lib().mq_attn_decode(ctypes.byref(cache(mq, **bad)), ctypes.byref(attn_args(mq)), None)
+    assert st == getattr(mq, "MQ_ERR_" + status)
+
+
+@NO_GPU
+@pytest.mark.parametrize("bad,status", [
+    (dict(nt=0), "SHAPE"), (dict(n_heads=0), "SHAPE"), (dict(n_heads=5), "SHAPE"), (dict(nt=1 << 24), "SHAPE"),
+    (dict(max_len=0), "SHAPE"), (dict(max_len=-1), "SHAPE"), (dict(max_len=2 ** 31 - 1), "SHAPE"),
+    (dict(window=-1), "SHAPE"), (dict(scale=math.inf), "SHAPE"), (dict(scale=math.nan), "SHAPE"),
+    (dict(softcap=-2.0), "SHAPE"), (dict(softcap=math.nan), "SHAPE"), (dict(q_stride=508), "SHAPE"),
+    (dict(out_stride=-512), "SHAPE"), (dict(n_seqs=0), "SHAPE"), (dict(pages_stride=0), "SHAPE"),
+    (dict(q=None), "NULL"), (dict(out=None), "NULL"), (dict(lens=None), "NULL"), (dict(pages=None), "NULL"),
+    (dict(q=0x30004), "ALIGN"), (dict(out=0x40008), "ALIGN"), (dict(q8=0x10004), "ALIGN"),
+    (dict(ws=0x70008), "ALIGN"), (dict(q_stride=513), "ALIGN"), (dict(lens=0x50002), "ALIGN"),
+    (dict(seq=0x50001), "ALIGN"), (dict(pages=0x60002), "ALIGN"), (dict(status=0x10002), "ALIGN")])
+def test_attention_refuses_bad_arguments(mq, bad, status):
+    st = mq.lib().mq_attn_decode(ctypes.byref(cache(mq)), ctypes.byref(attn_args(mq, **bad)), None)
+    assert st == getattr(mq, "MQ_ERR_" + status)
+
+
+@NO_GPU
+def test_attention_refuses_null_structs(mq):
+    L = mq.lib()
+    assert L.mq_attn_decode(None, ctypes.byref(attn_args(mq)), None) == mq.MQ_ERR_NULL
+    assert L.mq_attn_decode(ctypes.byref(cache(mq)), None, None) == mq.MQ_ERR_NULL
+    assert L.mq_attn_workspace_bytes(None, 4, 1, 100) == 0
+    assert L.mq_attn_workspace_bytes(ctypes.byref(cache(mq)), 5, 1, 100) == 0
+    assert L.mq_attn_workspace_bytes(ctypes.byref(cache(mq)), 4, 0, 100) == 0
