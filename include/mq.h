@@ -632,10 +632,11 @@ int mq_rope_append(const mq_kv_cache *kv, const mq_rope_append_args *args, void 
  *   s_j = scale * (q . k_j), or softcap * tanh(that / softcap) if softcap > 0,
  *   for tokens j in [max(0, n - window), n) (window 0: all of them);
  *   out = sum_j exp(s_j - max s) v_j / sum_j exp(s_j - max s).
- * n counts the cached tokens the row sees, its own among them.  n == 0, or
- * scores that are all -inf: the row is 0.  n < 0: the row is padding and
- * nothing of it is written.  Cached values outside the tokens above are never
- * used, whatever they hold.  Several rows may name one sequence with lengths
+ * n counts the cached tokens the row sees, its own among them.  n == 0: the
+ * row is 0.  n < 0: the row is padding and nothing of it is written.  Cached
+ * values outside the tokens above are never used, whatever they hold; an
+ * infinity or NaN among those seen makes the heads that see it NaN, or is left
+ * out where its score is -inf.  Several rows may name one sequence with lengths
  * of their own (the tokens of a speculative step).
  * Products with the cache are exact to f32 (queries and probabilities go
  * through the tensor cores in two fp16 or three bf16 parts); statistics and
@@ -674,6 +675,46 @@ typedef struct {
 
 size_t mq_attn_workspace_bytes(const mq_kv_cache *kv, int n_heads, int nt, int max_len);
 int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *args, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Draw of a token (device): nt rows of logits to one token each, by
+ * temperature, top-k, top-p and min-p, from given random numbers, in one
+ * launch.  For a row, with the tokens ordered by logit (descending; equal
+ * logits by index) and weights w_i = exp((logit_i - max) / temperature):
+ *   top_k > 0: the first top_k tokens of that order;
+ *   top_p < 1: the shortest prefix whose weights reach top_p of the weights
+ *              that top_k left, one token at the least;
+ *   min_p > 0: the tokens with w >= min_p (min_p of the largest probability).
+ * The tokens that pass all three are kept.  The token drawn is the first in
+ * the order of the vocabulary at which the kept weights, added up, exceed
+ * u times their sum; prob is its share of that sum.
+ *   temperature <= 0 (or NaN): the largest logit, the lowest index where equal;
+ *     prob is 1.  top_k <= 0: no such filter; top_p <= 0 keeps one token.
+ *   A NaN logit counts as -inf; -inf is never drawn.  A row of nothing else
+ *     gives token -1 and prob 0.  Infinite logits share the draw evenly.
+ *   u: in [0, 1); outside it counts as the nearest end.
+ * Weights are summed as 64-bit integers (2^-42 of the largest; the border of
+ * top_p 2^-32), so the result depends on nothing but the inputs.
+ *   logits: nt rows of vocab f32 (4-byte aligned, any stride >= vocab).
+ *   temperature, top_k, top_p, min_p: one value a row (device), or NULL: 1, and
+ *     no filter.  u, token: one a row.  prob: one a row, or NULL.
+ * Shapes: 1 <= vocab <= MQ_SAMPLE_MAX_VOCAB; nt >= 1.
+ * Errors: MQ_ERR_NULL, MQ_ERR_SHAPE, MQ_ERR_ALIGN, MQ_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+#define MQ_SAMPLE_MAX_VOCAB 655360
+
+typedef struct {
+    int nt, vocab;
+    const float *logits;
+    long long stride;            /* values between rows                    */
+    const float *u;
+    const float *temperature, *top_p, *min_p; /* or NULL                   */
+    const int *top_k;            /* or NULL                                */
+    int *token;
+    float *prob;                 /* or NULL                                */
+} mq_sample_args;
+
+int mq_sample(const mq_sample_args *args, void *stream);
 
 #ifdef __cplusplus
 }

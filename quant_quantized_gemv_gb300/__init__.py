@@ -36,7 +36,7 @@ EXPORTS = [
     "mq_check_coverage", "mq_gemv_plan_for", "mq_set_pdl", "mq_gemv_q6k_q8_noalloc",
     "mq_gemv_group_workspace_bytes", "mq_gemv_group_q8", "mq_gemv_group_q8_plan",
     "mq_kv_page_bytes", "mq_rope_table", "mq_rope_append",
-    "mq_attn_workspace_bytes", "mq_attn_decode",
+    "mq_attn_workspace_bytes", "mq_attn_decode", "mq_sample",
     "mq_gemv_q6k_q8_subdots",
     "mq_gemv_q4k_q8_subdots", "mq_device_sms",
     "mq_quantize_q8_batch", "mq_rmsnorm_quant_q8_batch", "mq_swiglu_quant_q8_batch",
@@ -149,6 +149,7 @@ def lib():
         "mq_rope_append": ([P, P, P], I),
         "mq_attn_workspace_bytes": ([P, I, I, I], S),
         "mq_attn_decode": ([P, P, P], I),
+        "mq_sample": ([P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -721,6 +722,7 @@ def mq_gemv_q5k_q8_subdots(Wp, q8, rows: int, cols: int, stream=None):
 # ------------------------------------------------------------------ around the GEMVs of a decode step
 KV_TYPES = {"f16": 1, "bf16": 2, "q8": 3}
 ROPE_STYLES = {"half": 0, "pairs": 1}
+MQ_SAMPLE_MAX_VOCAB = 655360
 
 
 class _KVStruct(ctypes.Structure):
@@ -751,6 +753,13 @@ class _AttnStruct(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("q8", "lens", "seq", "pages")]
                 + [("n_seqs", ctypes.c_int), ("pages_stride", ctypes.c_int)]
                 + [("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p)])
+
+
+class _SampleStruct(ctypes.Structure):
+    """mq_sample_args of include/mq.h"""
+    _fields_ = ([("nt", ctypes.c_int), ("vocab", ctypes.c_int), ("logits", ctypes.c_void_p),
+                 ("stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("u", "temperature", "top_p", "min_p", "top_k", "token", "prob")])
 
 
 def mq_kv_page_bytes(kv_type: str, n_kv_heads: int, page_size: int, head_dim: int) -> int:
@@ -941,3 +950,27 @@ def mq_attn_decode(kv: MQKVCache, q, lens, pages, scale: float, out=None, q8=Non
         _vec(status, 1, i32, dev, "status"))
     _check(lib().mq_attn_decode(kv._ref, ctypes.byref(args), _raw_stream(stream, dev)), "mq_attn_decode")
     return out
+
+
+def mq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, token=None, prob=None,
+              stream=None):
+    """One token per row of logits ([nt, vocab] f32, any row stride), drawn
+    with the random numbers u (f32 [nt], in [0, 1)); returns token (int32 [nt]).
+
+    temperature, top_p, min_p: f32 [nt]; top_k: int32 [nt]; None leaves the
+    filter out (temperature 1).  temperature 0 is the most likely token.
+    prob: an f32 tensor [nt] that gets the token's probability among those
+    kept.  A row without a finite logit gives -1."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    dev = _on_current(logits.get_device())
+    nt, vocab = logits.shape
+    if token is None:
+        token = torch.empty(nt, dtype=i32, device=logits.device)
+    args = _SampleStruct(
+        nt, vocab, _rows(logits, nt, vocab, f32, dev, "logits"), logits.stride(0) if nt > 1 else vocab,
+        _vec(u, nt, f32, dev, "u"), _vec(temperature, nt, f32, dev, "temperature"),
+        _vec(top_p, nt, f32, dev, "top_p"), _vec(min_p, nt, f32, dev, "min_p"), _vec(top_k, nt, i32, dev, "top_k"),
+        _vec(token, nt, i32, dev, "token"), _vec(prob, nt, f32, dev, "prob"))
+    _check(lib().mq_sample(ctypes.byref(args), _raw_stream(stream, dev)), "mq_sample")
+    return token

@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 SO = os.path.join(BUILD, "libmq.so")
 SOURCES = ["gemv.cu", "gemv_batch.cu", "gemv_gateup.cu", "gemv_f32.cu", "producers.cu", "noalloc.cu",
-           "readfloor.cu", "copy.cu", "repack_device.cu", "rope_append.cu", "attn_decode.cu",
+           "readfloor.cu", "copy.cu", "repack_device.cu", "rope_append.cu", "attn_decode.cu", "sample.cu",
            "api.cpp", "repack.cpp", "decode.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,6 +1,6 @@
 // decode.cpp -- the C ABI of the operators around the GEMVs of a decode step
-// (include/mq.h: paged cache, rotation and append, attention): argument checks,
-// the attention's split, then the launch.  Nothing here allocates.
+// (include/mq.h: paged cache, rotation and append, attention, draw): argument
+// checks, the attention's split, then the launch.  Nothing here allocates.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -134,10 +134,11 @@ int mq_rope_append(const mq_kv_cache *kv, const mq_rope_append_args *a, void *st
     size_t page_stride, head_bytes;
     const int st = kv_check(kv, &page_stride, &head_bytes);
     if (st != MQ_OK) return st;
+    if (a->nt < 1) return MQ_ERR_SHAPE;  // empty tensors have no address
     if (!a->q || !a->k || !a->v || !a->q_out || !a->positions || !a->pages) return MQ_ERR_NULL;
     const int D = kv->head_dim;
     const long long nq = (long long)a->n_heads * D, nk = (long long)kv->n_kv_heads * D;
-    if (a->nt < 1 || a->n_heads < 1 || a->n_heads % kv->n_kv_heads != 0 || a->n_heads > (1 << 20) ||
+    if (a->n_heads < 1 || a->n_heads % kv->n_kv_heads != 0 || a->n_heads > (1 << 20) ||
         kv->n_kv_heads > (1 << 20) || a->n_seqs < 1 || a->pages_stride < 1)
         return MQ_ERR_SHAPE;
     if (a->rope_dims < 0 || a->rope_dims > D || a->rope_dims % (D > 128 ? 16 : 8) != 0 ||
@@ -189,6 +190,7 @@ int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *a, void *stream)
     size_t page_stride, head_bytes;
     const int st = kv_check(kv, &page_stride, &head_bytes);
     if (st != MQ_OK) return st;
+    if (a->nt < 1) return MQ_ERR_SHAPE;  // empty tensors have no address
     if (!a->q || !a->out || !a->lens || !a->pages) return MQ_ERR_NULL;
     if (!attn_shape_ok(kv, a->n_heads, a->nt, a->max_len)) return MQ_ERR_SHAPE;
     const int D = kv->head_dim, n = a->n_heads * D;
@@ -230,6 +232,28 @@ int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *a, void *stream)
     r.max_len = a->max_len, r.window = a->window, r.scale = a->scale, r.softcap = a->softcap;
     const cudaError_t e = launch_attn_decode(r, pdl_setting(), (cudaStream_t)stream);
     return e == cudaSuccess ? MQ_OK : cuda_fail("attn_decode launch", e);
+}
+
+int mq_sample(const mq_sample_args *a, void *stream)
+{
+    if (!a) return MQ_ERR_NULL;
+    if (a->nt < 1 || a->vocab < 1) return MQ_ERR_SHAPE;  // empty tensors have no address
+    if (!a->logits || !a->u || !a->token) return MQ_ERR_NULL;
+    // the grid: up to 16 CTAs a row
+    if (a->nt > (1 << 24) || a->vocab > MQ_SAMPLE_MAX_VOCAB || a->stride < a->vocab)
+        return MQ_ERR_SHAPE;
+    const void *p4[] = {a->logits, a->u, a->temperature, a->top_p, a->min_p, a->top_k, a->token, a->prob};
+    for (const void *p : p4)
+        if (!aligned(p, 4)) return MQ_ERR_ALIGN;
+    const int sms = mq_device_sms();
+    if (sms <= 0) return MQ_ERR_CUDA;
+    SampleLaunch r = {};
+    r.logits = a->logits, r.stride = a->stride, r.u = a->u;
+    r.temperature = a->temperature, r.top_p = a->top_p, r.min_p = a->min_p, r.top_k = a->top_k;
+    r.token = a->token, r.prob = a->prob;
+    r.nt = a->nt, r.vocab = a->vocab;
+    const cudaError_t e = launch_sample(r, sms, pdl_setting(), (cudaStream_t)stream);
+    return e == cudaSuccess ? MQ_OK : cuda_fail("sample launch", e);
 }
 
 }  // extern "C"

@@ -247,6 +247,19 @@ struct AttnLaunch {
 };
 cudaError_t launch_attn_decode(const AttnLaunch &a, int pdl, cudaStream_t st);
 
+// Draw of a token (sample.cu): one cluster per row.
+struct SampleLaunch {
+    const float *logits;
+    long long stride;                         // values between rows
+    const float *u, *temperature, *top_p, *min_p;  // the last three may be null
+    const int *top_k;                         // or null
+    int *token;
+    float *prob;                              // or null
+    int nt, vocab;
+    int slice, seg;                           // values of a CTA and of a thread (set by the launch)
+};
+cudaError_t launch_sample(SampleLaunch a, int sms, int pdl, cudaStream_t st);
+
 // The process-wide programmatic-dependent-launch setting (mq_set_pdl).
 int pdl_setting();
 

@@ -168,3 +168,58 @@ def test_attention_refuses_null_structs(mq):
     assert L.mq_attn_workspace_bytes(None, 4, 1, 100) == 0
     assert L.mq_attn_workspace_bytes(ctypes.byref(cache(mq)), 5, 1, 100) == 0
     assert L.mq_attn_workspace_bytes(ctypes.byref(cache(mq)), 4, 0, 100) == 0
+
+
+@NO_GPU
+@pytest.mark.parametrize("bad,status", [
+    (dict(nt=0), "SHAPE"), (dict(nt=-3), "SHAPE"), (dict(nt=(1 << 24) + 1), "SHAPE"), (dict(vocab=0), "SHAPE"),
+    (dict(vocab=655361, stride=655361), "SHAPE"), (dict(stride=99), "SHAPE"), (dict(stride=-100), "SHAPE"),
+    (dict(logits=None), "NULL"), (dict(u=None), "NULL"), (dict(token=None), "NULL"),
+    (dict(logits=0x10002), "ALIGN"), (dict(top_k=0x10001), "ALIGN"), (dict(prob=0x10003), "ALIGN")])
+def test_sample_refuses_bad_arguments(mq, bad, status):
+    a = dict(nt=1, vocab=100, logits=0x10000, stride=100, u=0x20000, token=0x30000)
+    a.update(bad)
+    st = mq.lib().mq_sample(ctypes.byref(mq._SampleStruct(**a)), None)
+    assert st == getattr(mq, "MQ_ERR_" + status)
+
+
+@NO_GPU
+def test_sample_refuses_null_arguments(mq):
+    assert mq.lib().mq_sample(None, None) == mq.MQ_ERR_NULL
+
+
+# the references against what they can be checked with on paper
+def test_reference_sample_by_hand():
+    from oracle import decode as ref
+    x = np.log(np.array([0.1, 0.4, 0.2, 0.3]))
+    assert ref.sample(x, 0.0)[0] == 0 and ref.sample(x, 0.3)[0] == 1 and ref.sample(x, 0.95)[0] == 3
+    tok, p, kept, _ = ref.sample(x, 0.5, k=2)          # keeps 0.4 and 0.3
+    assert kept.tolist() == [False, True, False, True] and tok == 1 and abs(p - 4 / 7) < 1e-12
+    assert ref.sample(x, 0.6, k=2)[0] == 3
+    assert ref.sample(x, 0.0, p=0.65)[2].tolist() == [False, True, False, True]
+    assert ref.sample(x, 0.0, p=0.71)[2].tolist() == [False, True, True, True]
+    assert ref.sample(x, 0.0, m=0.6)[2].tolist() == [False, True, False, True]
+    assert ref.sample(x, 0.9, t=0.0)[0] == 1
+    assert ref.sample(np.full(4, -np.inf), 0.5)[0] == -1
+    assert ref.sample(np.array([1.0, 1.0, 1.0]), 0.0, k=2)[2].tolist() == [True, True, False]
+
+
+def test_reference_attention_by_hand():
+    from oracle import decode as ref
+    q = np.array([[1.0, 0.0]])
+    k = np.array([[[0.0, 5.0], [np.log(3.0), -2.0]]])
+    v = np.array([[[4.0, 0.0], [0.0, 8.0]]])
+    assert np.allclose(ref.attention(q, k, v, 1.0), [[1.0, 6.0]])      # weights 1/4 and 3/4
+    assert np.allclose(ref.attention(q, k, v, 1.0, window=1), [[0.0, 8.0]])
+    assert np.allclose(ref.attention(q, k, v, 1e9, softcap=np.log(3.0)), [[1.0, 6.0]])
+    assert np.all(ref.attention(q, k[:, :0], v[:, :0], 1.0) == 0)
+
+
+def test_reference_rotation_by_hand():
+    from oracle import decode as ref
+    x = np.array([[[1.0, 0.0, 0.0, 2.0]]])
+    f = np.array([np.pi / 2, np.pi])
+    half, _ = ref.rotate(x, np.abs(x), [1], f, "half")                  # pairs (0, 2), (1, 3)
+    assert np.allclose(half, [[[0.0, 0.0, 1.0, -2.0]]])
+    pairs, _ = ref.rotate(x, np.abs(x), [1], f, "pairs")                # pairs (0, 1), (2, 3)
+    assert np.allclose(pairs, [[[0.0, 1.0, 0.0, -2.0]]])
