@@ -230,8 +230,9 @@ def _own_attn(s):
 
 def _own_sample(s):
     import quant_quantized_gemv_gb300 as mq
-    return mq.mq_sample(s["logits"], s["u"], temperature=s["t"], top_k=s["k"], top_p=s["p"], min_p=s["m"],
-                        token=s["token"], prob=s["prob"])
+    mq.mq_sample(s["logits"], s["u"], temperature=s["t"], top_k=s["k"], top_p=s["p"], min_p=s["m"],
+                 token=s["token"], prob=s["prob"])
+    return s["token"], s["prob"]
 
 
 # ------------------------------------------------------------------ the plain forms
