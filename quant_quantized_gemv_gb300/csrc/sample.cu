@@ -7,32 +7,49 @@
 // cluster's distributed shared memory: one launch, no workspace, no sort of
 // the vocabulary.
 //   1. the row's maximum;
-//   2. if top-k or top-p is on: counts and weight sums of the tokens in bins
-//      of (max - logit) / temperature, 32 to a factor of two; the CTAs add
-//      theirs into rank 0's, which finds the bin where the filter ends;
-//   3. the tokens of that bin alone are gathered in rank 0 and ranked, which
-//      gives the last token kept, as a 64-bit place in the order (logit, then
-//      index).  A bin of more tokens than the list holds (ties, flat logits)
-//      is first narrowed by 11 bits of that place at a time;
-//   4. every CTA sums the weights of its kept tokens in the order of the
-//      vocabulary; the sums before it and the random number say which CTA,
-//      which thread and which token the draw falls on.
+//   2. if top-k or top-p is on: the tokens are counted in bins of
+//      (max - logit) / temperature, 64 to a factor of two, and the bins summed
+//      in 64 groups.  To find the bin where a sum ends, every CTA adds up the
+//      groups over the cluster, then the bins of one group;
+//   3. top-k ends in the bin where the counts reach k.  With few tokens down
+//      to that bin (the usual chain of filters) they alone are gathered in
+//      rank 0, which applies every filter and draws.  Else the bin's tokens are
+//      gathered and ranked, which gives the last token kept, as a 64-bit place
+//      in the order (logit, then index): every CTA gets the list and ranks its
+//      own tokens.  A bin of more tokens than the list holds (ties) is first
+//      narrowed by 8 bits of that place at a time;
+//   4. top-p: the counts times the bins' weights name a bin.  One pass then sums
+//      the weights of all tokens, of those above a window of bins around it and
+//      of the window's bins one by one, exactly, and sets the window's tokens
+//      aside: that settles the bin (or moves the window), whose tokens are
+//      ranked as in 3;
+//   5. every CTA sums the weights of its kept tokens in the order of the
+//      vocabulary (after 4: the sums above the window, and the window's tokens
+//      that were set aside); the sums before it and the random number say which
+//      CTA, which thread and which token is drawn.
+//
+// What bounds it: with many rows the instructions of step 4's pass (about 45 a
+// token; the row itself is read once); with few, the steps one after another
+// (a cluster barrier each).  Nothing uses 64-bit floating point (a division by
+// every thread took 2.9 us), and conversions between float and integer, at an
+// eighth of the rate of an addition, are kept to one a weight: the others add
+// 1.5 x 2^23 and take the low bits.
 //
 // Weights.  w = 2^-t, t = (max - logit) log2(e) / temperature, as an integer in
-// units of 2^-42: integer sums do not depend on their order, so neither the
-// bins' atomics nor the split of the row over CTAs can change a draw.  t is
-// formed with its rounding errors carried (max - logit and the product have
-// two parts each): with t near 20 one f32 rounding would be 10^-6 of w, and a
-// draw compares sums over the whole vocabulary with borders that close.  Then
+// units of 2^-42: integer sums do not depend on their order, so neither
+// atomics nor the split of the row over CTAs can change a draw.  t is formed
+// with its rounding errors carried (max - logit and the product have two parts
+// each): with t near 20 one f32 rounding would be 10^-6 of w, and a draw
+// compares sums over the whole vocabulary with borders that close.  Then
 // t = n - f, |f| <= 1/2, and 2^f - 1 = f ln2 + (f ln2)^2 / 2 + ... to degree 8
 // (the rest is under 2^-32) is added to 1 as an integer: w is right to 5 x
-// 2^-26 at worst, 2^-27 in the mean.  The bins hold weights in units of 2^-32, as two sums of 16 bits each
-// (shared memory adds 32-bit integers at once, 64-bit ones in a loop).
+// 2^-26 at worst, 2^-27 in the mean.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <atomic>
+#include <utility>
 
 #include "kernels.h"
 
@@ -43,32 +60,54 @@ namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
 constexpr int kThreads = 512;
-constexpr int kBins = 2048;
-constexpr int kList = 1024;      // tokens that rank 0 ranks at once
+constexpr int kBins = 4096;
+constexpr int kGroups = 64;      // groups of as many bins
+constexpr float kBinsPerOctave = 64.0f;
+constexpr int kList = 512;       // tokens that rank 0 ranks at once
+constexpr int kMine = 1024;      // tokens that a CTA sets aside
 constexpr int kMaxCluster = 16;  // CTAs of a row (over 8: the non-portable size)
 constexpr int kFixBits = 42;     // a weight of 1 is 2^42
+constexpr int kWindow = 25;      // bins whose weights are summed one by one
+constexpr int kDigits = 256;     // values of 8 bits of a place
+// sums of the exact pass: all, above the window, its bins; the bins' counts; tokens that found no room
+constexpr int kSums = 2 + 2 * kWindow + 1;
 
-// What the CTAs of a row tell each other, and rank 0's findings (copied to all).
-struct Control {
+struct Shared {
+    union {
+        unsigned cnt[kBins];                     // this CTA's bins
+        struct {
+            u64 mine[kMine];                     // afterwards: its tokens that may matter
+            union {
+                struct {
+                    u64 list[kList], weight[kList];  // the gathered tokens
+                };
+                u64 extra[kThreads];             // at the end: what each thread's set-aside tokens weigh
+            };
+        };
+    };
+    union {
+        u64 sums[kSums];                         // the exact pass
+        struct {
+            u64 digit_w[kDigits];                // narrowing a bin
+            unsigned digit_n[kDigits];
+        };
+    };
+    u64 all[kSums];                              // the sums over the cluster
+    u64 part[2][kThreads / 32];                  // the exact pass: warps' sums, bins' sums and counts
+    unsigned bin_lo[kWindow], bin_hi[kWindow], bin_n[kWindow];
+    u64 group_w[kGroups], groups_w[kGroups];     // estimated weights of the groups: this CTA's, the row's
+    unsigned group_n[kGroups], groups_n[kGroups];
+    unsigned bins_n[kGroups];                    // the row's bins of one group
+    u64 octave[64];                              // 2^30 2^(-b / 64)
+    u64 warp_sums[kThreads / 32];
     float maxes[kMaxCluster];
     int argmax[kMaxCluster];
     u64 totals[kMaxCluster];
-    u64 warp_sums[kThreads / 32];
-    u64 target, above;       // what is still wanted of the current set; weights kept above it
-    u64 prefix;              // set of a narrowed bin: places whose top `bits` bits are prefix
-    u64 boundary;            // last place kept
-    u64 total;               // weights that top-k left (2^-32)
-    unsigned population, list_n;
-    int bin, bits, found;
+    u64 boundary, narrow_left;
+    unsigned list_n, mine_n, at, at_n, narrow_n, narrow_digit;
 };
-
-struct Shared {
-    unsigned cnt[kBins], hi[kBins], lo[kBins];  // this CTA's bins; later rank 0's list
-    u64 all_w[kBins];                            // rank 0: the row's
-    unsigned all_cnt[kBins];
-    Control c;
-};
-static_assert(sizeof(u64) * 2 * kList <= sizeof(unsigned) * 3 * kBins, "the list lies over the bins");
+static_assert(kBins / kGroups == 64 && kGroups == 64 && kThreads == 8 * kGroups,
+              "8 threads a group, 8 bins a thread; 8 threads a bin of one group");
 
 // Order of the logits as unsigned integers: larger logit, larger key.
 __device__ __forceinline__ unsigned key_of(float x)
@@ -86,43 +125,104 @@ __device__ __forceinline__ u64 place_of(float x, int index)
     return (u64)key_of(x) << 32 | (0xffffffffu - (unsigned)index);
 }
 
+constexpr float kMagic = 12582912.0f;  // 1.5 x 2^23: a float + this has the rounded integer in its low bits
+
+// Two floats an instruction (each rounded as its scalar form).
+struct Two {
+    u64 v;
+};
+__device__ __forceinline__ Two two(float a, float b)
+{
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(Two x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b)
+{
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
 struct Weight {
     float top, c_hi, c_lo;  // the row's maximum; log2(e) / temperature in two parts
 
-    __device__ __forceinline__ float exponent(float x) const { return (top - x) * c_hi; }
+    // The bin of a logit: t, in steps of 1 / kBinsPerOctave, rounded.
+    __device__ __forceinline__ int bin(float x) const { return bin_of((top - x) * (c_hi * kBinsPerOctave)); }
+    __device__ __forceinline__ static int bin_of(float steps)
+    {
+        return __float_as_int(fminf(steps, (float)(kBins - 1)) + kMagic) & 0xffff;
+    }
+
+    __device__ __forceinline__ void bins(float x0, float x1, int &b0, int &b1) const
+    {
+        const float c = c_hi * kBinsPerOctave;
+        float s0, s1;
+        split(mul2(fma2(two(x0, x1), two(-1.0f, -1.0f), two(top, top)), two(c, c)), s0, s1);
+        b0 = bin_of(s0), b1 = bin_of(s1);
+    }
+
+    // The weights of two logits, each as a * m, two 32-bit factors (adding such a product to a sum is
+    // one instruction), and their bins.
+    __device__ __forceinline__ void pair(float x0, float x1, unsigned (&a)[2], unsigned (&m)[2], int (&bin)[2]) const
+    {
+        const Two x = two(x0, x1), tp = two(top, top), minus = two(-1.0f, -1.0f);
+        const Two ch = two(c_hi, c_hi), cl = two(c_lo, c_lo);
+        const Two d = fma2(x, minus, tp);
+        const Two t = mul2(d, ch);
+        // d + e = top - x exactly; t + r = (d + e) * (c_hi + c_lo) to f32's square
+        const Two b = fma2(tp, minus, d);
+        const Two e = fma2(add2(x, b), minus, fma2(fma2(b, minus, d), minus, tp));
+        const Two nt = mul2(t, minus);
+        const Two r = add2(fma2(d, ch, nt), fma2(d, cl, mul2(e, ch)));
+        const Two nm = add2(t, two(kMagic, kMagic));
+        const Two f = fma2(r, minus, add2(add2(nm, two(-kMagic, -kMagic)), nt));
+        // 2^30 (2^f - 1) / f by its series in f ln2
+        constexpr float k = 1073741824.0f;
+        Two s = two(1.3215486790144307e-6f * k, 1.3215486790144307e-6f * k);
+        s = fma2(s, f, two(1.5252733804059841e-5f * k, 1.5252733804059841e-5f * k));
+        s = fma2(s, f, two(1.5403530393381609e-4f * k, 1.5403530393381609e-4f * k));
+        s = fma2(s, f, two(1.3333558146428443e-3f * k, 1.3333558146428443e-3f * k));
+        s = fma2(s, f, two(9.6181291076284772e-3f * k, 9.6181291076284772e-3f * k));
+        s = fma2(s, f, two(5.5504108664821580e-2f * k, 5.5504108664821580e-2f * k));
+        s = fma2(s, f, two(2.4022650695910071e-1f * k, 2.4022650695910071e-1f * k));
+        s = fma2(s, f, two(6.9314718055994531e-1f * k, 6.9314718055994531e-1f * k));
+        float p[2], tt[2], nn[2], steps[2];
+        split(mul2(s, f), p[0], p[1]);
+        split(t, tt[0], tt[1]);
+        split(nm, nn[0], nn[1]);
+        split(mul2(t, two(kBinsPerOctave, kBinsPerOctave)), steps[0], steps[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const unsigned one = (1u << 30) + (unsigned)__float2int_rn(p[i]);
+            const int n = (int)(__float_as_uint(nn[i]) & 63u);  // the weight is one * 2^(42 - 30 - n)
+            a[i] = tt[i] < (float)kFixBits + 0.5f ? one >> max(n - (kFixBits - 30), 0) : 0u;
+            m[i] = 1u << max(kFixBits - 30 - n, 0);
+            bin[i] = bin_of(steps[i]);
+        }
+    }
 
     __device__ __forceinline__ u64 operator()(float x) const
     {
-        if (x == top) return 1ull << kFixBits;  // also +inf, whose difference is no number
-        const float d = top - x;
-        const float t = d * c_hi;
-        if (!(t < (float)kFixBits + 0.5f)) return 0;  // also x = -inf, top = +inf
-        // d + e = top - x exactly; t + r = (d + e) * (c_hi + c_lo) to f32's square
-        const float b = d - top;
-        const float e = (top - (d - b)) - (x + b);
-        const float r = fmaf(d, c_hi, -t) + fmaf(d, c_lo, e * c_hi);
-        const float n = rintf(t);
-        const float f = (n - t) - r;
-        // (2^f - 1) / f by its series in f ln2
-        float s = 1.3215486790144307e-6f;
-        s = fmaf(s, f, 1.5252733804059841e-5f);
-        s = fmaf(s, f, 1.5403530393381609e-4f);
-        s = fmaf(s, f, 1.3333558146428443e-3f);
-        s = fmaf(s, f, 9.6181291076284772e-3f);
-        s = fmaf(s, f, 5.5504108664821580e-2f);
-        s = fmaf(s, f, 2.4022650695910071e-1f);
-        s = fmaf(s, f, 6.9314718055994531e-1f);
-        const u64 one = (1u << 30) + (unsigned)__float2int_rn(s * f * 1073741824.0f);
-        return (one << (kFixBits - 30)) >> (int)n;
+        unsigned a[2], m[2];
+        int none[2];
+        pair(x, x, a, m, none);
+        return (u64)a[0] * m[0];
     }
 };
-
-// A weight in units of 2^-32 (the largest is one unit short: it has to fit 32 bits).
-__device__ __forceinline__ unsigned coarse(u64 w)
-{
-    const u64 c = (w + (1u << 9)) >> 10;
-    return c > 0xffffffffu ? 0xffffffffu : (unsigned)c;
-}
 
 // Exclusive prefix sum over the CTA's threads, and the total (all threads call it).
 __device__ __forceinline__ u64 block_scan(u64 v, u64 *warp_sums, u64 *total)
@@ -148,6 +248,27 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64 *warp_sums, u64 *total)
     return before + s - v;
 }
 
+// Where the sums of 64 values (this lane's are number 2 * lane and 2 * lane + 1), in order, reach
+// the target: the value's number, and what is before it.  Every lane gets both, and the total.
+__device__ __forceinline__ int reach(u64 v0, u64 v1, u64 target, u64 *before, u64 *total)
+{
+    const int lane = threadIdx.x & 31;
+    u64 s = v0 + v1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 t = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += t;
+    }
+    *total = __shfl_sync(0xffffffffu, s, 31);
+    const unsigned reached = __ballot_sync(0xffffffffu, s >= target);
+    const int at = reached ? __ffs(reached) - 1 : 31;
+    u64 b = s - v0 - v1;
+    const bool second = b + v0 < target;
+    if (second) b += v0;
+    *before = __shfl_sync(0xffffffffu, b, at);
+    return __shfl_sync(0xffffffffu, 2 * lane + (second ? 1 : 0), at);
+}
+
 __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
@@ -160,13 +281,17 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
     Shared &root = *cluster.map_shared_rank(&sh, 0);
 
     griddep_launch_dependents();
-    for (int i = tid; i < kBins; i += kThreads) {
-        sh.cnt[i] = sh.hi[i] = sh.lo[i] = 0;
-        sh.all_w[i] = 0;
-        sh.all_cnt[i] = 0;
-    }
-    if (tid == 0) sh.c.list_n = 0;
+    for (int i = tid; i < kBins; i += kThreads) sh.cnt[i] = 0;
+    if (tid < 64) sh.octave[tid] = __float2uint_rn(exp2f((float)tid * (-1.0f / kBinsPerOctave)) * 1073741824.0f);
+    if (tid == 0) sh.list_n = sh.mine_n = 0;
+    auto started = cluster.barrier_arrive();
     griddep_wait();  // the logits may come from the preceding kernel
+
+    const float temperature = a.temperature ? __ldcg(a.temperature + row) : 1.0f;
+    const float top_p = a.top_p ? __ldcg(a.top_p + row) : 1.0f;
+    const float min_p = a.min_p ? __ldcg(a.min_p + row) : 0.0f;
+    const int top_k = a.top_k ? __ldcg(a.top_k + row) : 0;
+    const float u = __ldcg(a.u + row);
 
     // this CTA's slice: values [rank * slice, ..) counted from the last 16-byte border at or before the row
     const float *src = a.logits + row * a.stride;
@@ -175,44 +300,42 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
     const int base = rank * a.slice;  // in shifted places; index = place - shift
     const int lo = shift, hi = shift + a.vocab;
     float mx = -INFINITY;
-    for (int i = tid * 4; i < a.seg * kThreads; i += kThreads * 4) {
-        const int p = base + i;
-        float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (i < a.slice) {
-            if (p >= lo && p + 4 <= hi) {
-                const float4 f = __ldcg(reinterpret_cast<const float4 *>(src + p));
-                v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (p + j >= lo && p + j < hi) v[j] = __ldcg(src + p + j);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x = v[j] == v[j] ? v[j] + 0.0f : -INFINITY;  // NaN is never drawn; -0 is 0
-            xs[i + j] = x;
-            mx = fmaxf(mx, x);
-        }
+    // NaN is never drawn (the maximum of NaN and a number is the number); -0 is 0
+    auto clean = [&](float v) {
+        v = fmaxf(v + 0.0f, -INFINITY);
+        mx = fmaxf(mx, v);
+        return v;
+    };
+    // whole groups of four inside the row; the row's first and last groups and the padding one by one
+    const int whole = max(0, min(a.slice, (hi & ~3) - base));
+#pragma unroll 4
+    for (int i = tid * 4; i < whole; i += kThreads * 4) {
+        if (base + i < lo) continue;
+        const float4 f = __ldcg(reinterpret_cast<const float4 *>(src + base + i));
+        *reinterpret_cast<float4 *>(xs + i) = make_float4(clean(f.x), clean(f.y), clean(f.z), clean(f.w));
     }
-    const float temperature = a.temperature ? __ldcg(a.temperature + row) : 1.0f;
-    const float top_p = a.top_p ? __ldcg(a.top_p + row) : 1.0f;
-    const float min_p = a.min_p ? __ldcg(a.min_p + row) : 0.0f;
-    const int top_k = a.top_k ? __ldcg(a.top_k + row) : 0;
-    const float u = __ldcg(a.u + row);
+    for (int i = whole + tid; i < a.seg * kThreads; i += kThreads) {
+        const int p = base + i;
+        xs[i] = clean(i < a.slice && p >= lo && p < hi ? __ldcg(src + p) : -INFINITY);
+    }
+    if (base < lo && tid < 4 && whole > 0) {
+        const int p = base + tid;
+        xs[tid] = clean(p >= lo && p < hi ? __ldcg(src + p) : -INFINITY);
+    }
 
     // the row's maximum
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) sh.c.warp_sums[warp] = __float_as_uint(mx);
-    cluster.sync();  // every CTA of the row runs, its bins are zero
+    if (lane == 0) sh.warp_sums[warp] = __float_as_uint(mx);
+    __syncthreads();
+    cluster.barrier_wait(std::move(started));  // every CTA of the row runs
     if (tid < ranks) {
         float m = -INFINITY;
-        for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, __uint_as_float((unsigned)sh.c.warp_sums[w]));
-        cluster.map_shared_rank(&sh, tid)->c.maxes[rank] = m;
+        for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, __uint_as_float((unsigned)sh.warp_sums[w]));
+        cluster.map_shared_rank(&sh, tid)->maxes[rank] = m;
     }
     cluster.sync();
-    mx = sh.c.maxes[0];
-    for (int r = 1; r < ranks; ++r) mx = fmaxf(mx, sh.c.maxes[r]);
+    mx = sh.maxes[0];
+    for (int r = 1; r < ranks; ++r) mx = fmaxf(mx, sh.maxes[r]);
 
     if (mx == -INFINITY) {  // nothing to draw from
         if (rank == 0 && tid == 0) {
@@ -230,248 +353,523 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
                 break;
             }
         for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
-        if (lane == 0) sh.c.warp_sums[warp] = (unsigned)best;
+        if (lane == 0) sh.warp_sums[warp] = (unsigned)best;
         __syncthreads();
         if (tid == 0) {
-            for (int w = 0; w < kThreads / 32; ++w) best = min(best, (int)sh.c.warp_sums[w]);
-            root.c.argmax[rank] = best;
+            for (int w = 0; w < kThreads / 32; ++w) best = min(best, (int)sh.warp_sums[w]);
+            root.argmax[rank] = best;
         }
         cluster.sync();
         if (rank == 0 && tid == 0) {
-            for (int r = 0; r < ranks; ++r) best = min(best, sh.c.argmax[r]);
+            for (int r = 0; r < ranks; ++r) best = min(best, sh.argmax[r]);
             a.token[row] = best;
             if (a.prob) a.prob[row] = 1.0f;
         }
         return;
     }
 
-    const double c = 1.4426950408889634 / (double)temperature;
+    if (mx == INFINITY) {  // those logits share the draw: as equal ones
+        for (int i = tid; i < a.seg * kThreads; i += kThreads) xs[i] = xs[i] == mx ? 0.0f : -INFINITY;
+        mx = 0.0f;
+        __syncthreads();
+    }
+
+    // log2(e) / temperature in two parts: the quotient, and what its product leaves
     Weight weight;
     weight.top = mx;
-    weight.c_hi = (float)fmin(c, 1e30);
-    weight.c_lo = c < 1e30 ? (float)(c - (double)weight.c_hi) : 0.0f;
-    const u64 floor_w = min_p > 0.0f ? (u64)ceil((double)min_p * (double)(1ull << kFixBits)) : 0;
+    weight.c_hi = fminf(1.44269502f / temperature, 1e30f);
+    weight.c_lo = (fmaf(-weight.c_hi, temperature, 1.44269502f) + 1.92596299e-8f) / temperature;
+    if (!(fabsf(weight.c_lo) < weight.c_hi)) weight.c_lo = 0.0f;  // clamped, or an infinite temperature
+    const u64 floor_w = min_p > 0.0f ? __float2ull_ru(min_p * (float)(1ull << kFixBits)) : 0;
     const bool by_count = top_k > 0 && top_k < a.vocab, by_weight = top_p < 1.0f;
-    auto bin_of = [&](float x) { return (int)fminf(weight.exponent(x) * 32.0f, (float)(kBins - 1)); };
+    const int first = tid * a.seg;  // this thread's values, in the order of the vocabulary
+    auto index_of = [&](int i) { return base + i - shift; };
+    auto place = [&](int i) { return place_of(xs[i], index_of(i)); };
+    // a share s < 1 of a sum: its floor, by the 64 bits behind the point
+    auto share_of = [](float s, u64 all, bool up) {
+        const u64 f = __float2ull_rz(s * 18446744073709551616.0f);
+        return __umul64hi(f, all) + (up && f * all != 0 ? 1 : 0);
+    };
+    auto drawn_at = [&](u64 all) { return u > 0.0f ? (u < 1.0f ? share_of(u, all, false) : all - 1) : 0; };
+    auto wanted = [&](u64 all) { return max(share_of(top_p, all, true), (u64)1); };  // top-p of a sum
+    auto share_f32 = [](u64 w, u64 all) {  // w / all: the quotient and one correction
+        const float wh = __ull2float_rn(w), ah = __ull2float_rn(all);
+        const float wl = __ll2float_rn((long long)(w - __float2ull_rn(wh)));
+        const float al = __ll2float_rn((long long)(all - __float2ull_rn(ah)));
+        const float q = wh / ah;
+        return q + ((fmaf(-q, ah, wh) + wl) - q * al) / ah;
+    };
 
-    // Adds this CTA's tokens of the current set into its bins, then those into rank 0's.  Without
-    // a set (c.bin < 0) the bins are bin_of's, else the next 11 bits of the place, largest first.
-    auto histogram = [&](int bin, int bits, u64 prefix) {
-        for (int j = 0; j < a.seg; ++j) {
-            const float x = xs[tid * a.seg + j];
-            if (x == -INFINITY) continue;
-            int b = mx == INFINITY ? (x == mx ? 0 : kBins - 1) : bin_of(x);
-            if (bin >= 0) {
-                if (b != bin) continue;
-                const u64 place = place_of(x, base + tid * a.seg + j - shift);
-                if (bits && place >> (64 - bits) != prefix) continue;
-                const int left = 64 - bits;
-                b = kBins - 1 - (int)((left >= 11 ? place >> (left - 11) : place << (11 - left)) & (kBins - 1));
+    // The filters' last token: logit and index (no filter: every finite logit passes).
+    float last_x = -INFINITY;
+    int last_i = -4;  // the padding before a row has indexes -3 to -1
+    auto passes = [&](float x, int i) { return x > last_x || (x == last_x && index_of(i) <= last_i); };
+    auto set_last = [&](u64 p) { last_x = logit_of((unsigned)(p >> 32)), last_i = (int)~(unsigned)p; };
+
+    // This thread's tokens (0: none) into the list of every CTA, or of rank 0 alone; the CTA asks
+    // rank 0 for room once.  They are known to fit.
+    auto send = [&](u64 p0, u64 p1, bool everywhere) {
+        if (tid == 0) sh.at_n = 0;
+        __syncthreads();
+        const unsigned n = (p0 ? 1 : 0) + (p1 ? 1 : 0);
+        unsigned at = 0;
+        if (n) at = atomicAdd(&sh.at_n, n);
+        __syncthreads();
+        if (tid == 0 && sh.at_n) sh.at = atomicAdd(&root.list_n, sh.at_n);
+        __syncthreads();
+        at += sh.at;
+        if (n && at + n <= kList)
+            for (int r = 0; r < (everywhere ? ranks : 1); ++r) {
+                u64 *to = cluster.map_shared_rank(&sh, r)->list + at;
+                to[0] = p0 ? p0 : p1;
+                if (n == 2) to[1] = p1;
             }
-            atomicAdd(&sh.cnt[b], 1u);
-            if (by_weight) {
-                const unsigned w = coarse(weight(x));
-                if (w >> 16) atomicAdd(&sh.hi[b], w >> 16);
-                if (w & 0xffffu) atomicAdd(&sh.lo[b], w & 0xffffu);
-            }
+    };
+    // Sends this row's tokens of bins [bin_lo, bin_hi] that pass (and, with bits > 0, of places whose
+    // top `bits` bits are prefix).
+    auto gather = [&](int bin_lo, int bin_hi, int bits, u64 prefix, bool everywhere) {
+        if (tid == 0) sh.mine_n = 0;
+        __syncthreads();
+        auto look = [&](float x, int b, int i) {
+            if (b < bin_lo || b > bin_hi || !passes(x, i)) return;
+            const u64 p = place(i);
+            if (bits && p >> (64 - bits) != prefix) return;
+            const unsigned at = atomicAdd(&sh.mine_n, 1u);
+            if (at < kMine) sh.mine[at] = p;
+        };
+#pragma unroll 2
+        for (int i = tid * 2; i < a.seg * kThreads; i += 2 * kThreads) {
+            const float2 x = *reinterpret_cast<const float2 *>(xs + i);
+            int b0, b1;
+            weight.bins(x.x, x.y, b0, b1);
+            look(x.x, b0, i);
+            look(x.y, b1, i + 1);
         }
         __syncthreads();
-        for (int b = tid; b < kBins; b += kThreads) {
-            const unsigned n = sh.cnt[b];
-            if (n) {
-                atomicAdd(&root.all_cnt[b], n);
-                const u64 w = ((u64)sh.hi[b] << 16) + sh.lo[b];
-                if (w) atomicAdd(&root.all_w[b], w);
-            }
-        }
+        send(tid < (int)sh.mine_n ? sh.mine[tid] : 0, 0, everywhere);
         cluster.sync();
     };
-    // Rank 0: the bin where the target is reached; what is left of it, the weights above the bin
-    // and the bin's tokens go to every CTA.
-    auto find_bin = [&](bool counts) {
-        if (rank == 0) {
-            constexpr int kPer = kBins / kThreads;
-            const u64 target = sh.c.target, kept_above = sh.c.above;  // read before the scans' barriers
-            u64 mine = 0, weights = 0, total, all;
-            for (int j = 0; j < kPer; ++j) {
-                weights += sh.all_w[tid * kPer + j];
-                mine += sh.all_cnt[tid * kPer + j];
-            }
-            u64 w_before = block_scan(weights, sh.c.warp_sums, &all);
-            u64 before = counts ? block_scan(mine, sh.c.warp_sums, &total) : w_before;
-            if (!counts) mine = weights;
-            if (before < target && target <= before + mine) {
-                for (int j = 0; j < kPer; ++j) {
-                    const int b = tid * kPer + j;
-                    const u64 here = counts ? sh.all_cnt[b] : sh.all_w[b];
-                    if (target <= before + here) {
-                        const u64 left = target - before, above = kept_above + w_before;
-                        for (int r = 0; r < ranks; ++r) {
-                            Control &o = cluster.map_shared_rank(&sh, r)->c;
-                            o.bin = b, o.target = left, o.above = above, o.population = sh.all_cnt[b];
-                        }
-                        break;
-                    }
-                    before += here;
-                    w_before += sh.all_w[b];
-                }
-            }
+    static_assert(kList <= kThreads, "one token a thread");
+    // Ranks the tokens [from, to) of a list of n.  body(i, tokens before i, weights before i) runs in
+    // one thread for each of them; several threads share the comparisons of one token.
+    auto rank_list = [&](int n, int from, int to, auto &&body) {
+        for (int i = tid; i < n; i += kThreads) sh.weight[i] = weight(logit_of((unsigned)(sh.list[i] >> 32)));
+        __syncthreads();
+        int by = 1;
+        while (by < 32 && (to - from) * by * 2 <= kThreads) by *= 2;
+        const int i = from + tid / by, sub = tid & (by - 1);
+        int before = 0;
+        u64 w_before = 0;
+        if (i < to) {
+            const u64 p = sh.list[i];
+            for (int j = sub; j < n; j += by)
+                if (sh.list[j] > p) ++before, w_before += sh.weight[j];
         }
-        cluster.sync();
+        for (int o = 1; o < by; o <<= 1) {
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+            w_before += __shfl_xor_sync(0xffffffffu, w_before, o);
+        }
+        if (i < to && sub == 0) body(i, before, w_before);
     };
-    // The last place kept when the order's tokens are taken until `target` (of counts, or of
-    // weights) is reached; rank 0 leaves it in every CTA's c.boundary, and the weights up to it in
-    // its own c.total.
-    auto select = [&](bool counts) {
-        find_bin(counts);
-        const int bin = sh.c.bin;
+    // The last token of a list (in every CTA) whose order is followed until `left` counts or weights
+    // are reached: the CTA that sent it finds it and tells the others.
+    auto end_of_list = [&](int n, bool counts, u64 left) {
+        const int from = sh.at_n ? (int)sh.at : 0, to = min(from + (int)sh.at_n, kList);
+        rank_list(n, from, to, [&](int i, int before, u64 w_before) {
+            const bool last = counts ? (u64)before + 1 == left : w_before < left && left <= w_before + sh.weight[i];
+            if (last)
+                for (int r = 0; r < ranks; ++r) cluster.map_shared_rank(&sh, r)->boundary = sh.list[i];
+        });
+        if (rank == 0 && tid == 0) sh.list_n = 0;
+        cluster.sync();
+        set_last(sh.boundary);
+    };
+    // The last token within a bin of `population` tokens that pass.
+    auto end_of_bin = [&](int bin, unsigned population, bool counts, u64 left) {
         int bits = 0;
         u64 prefix = 0;
-        while (sh.c.population > kList) {
-            for (int i = tid; i < kBins; i += kThreads) {
-                sh.cnt[i] = sh.hi[i] = sh.lo[i] = 0;
-                if (rank == 0) sh.all_w[i] = 0, sh.all_cnt[i] = 0;
+        while (population > kList && bits < 64) {  // a place is one token's: it ends there at the latest
+            for (int i = tid; i < kDigits; i += kThreads) sh.digit_n[i] = 0, sh.digit_w[i] = 0;
+            __syncthreads();
+            for (int j = 0; j < a.seg; ++j) {
+                const float x = xs[first + j];
+                if (weight.bin(x) != bin || !passes(x, first + j)) continue;
+                const u64 p = place(first + j);
+                if (bits && p >> (64 - bits) != prefix) continue;
+                const int digit = (int)(p >> (56 - bits)) & (kDigits - 1);
+                atomicAdd(&sh.digit_n[kDigits - 1 - digit], 1u);
+                if (!counts) atomicAdd(&sh.digit_w[kDigits - 1 - digit], weight(x));
             }
             cluster.sync();
-            histogram(bin, bits, prefix);
-            find_bin(counts);
-            const int left = 64 - bits, step = left < 11 ? left : 11;
-            const u64 digit = (u64)(kBins - 1 - sh.c.bin) >> (11 - step);
-            prefix = prefix << step | digit;
-            bits += step;
-        }
-        u64 *list = reinterpret_cast<u64 *>(root.cnt);  // rank 0's bins are used up
-        for (int j = 0; j < a.seg; ++j) {
-            const float x = xs[tid * a.seg + j];
-            if (x == -INFINITY) continue;
-            const int b = mx == INFINITY ? (x == mx ? 0 : kBins - 1) : bin_of(x);
-            if (b != bin) continue;
-            const u64 place = place_of(x, base + tid * a.seg + j - shift);
-            if (bits && place >> (64 - bits) != prefix) continue;
-            const unsigned at = atomicAdd(&root.c.list_n, 1u);
-            if (at < kList) list[at] = place;
-        }
-        cluster.sync();
-        if (rank == 0) {
-            u64 *mine = reinterpret_cast<u64 *>(sh.cnt), *sorted = mine + kList;
-            const int n = min((int)sh.c.list_n, kList);
-            for (int i = tid; i < n; i += kThreads) {
-                const u64 p = mine[i];
-                int before = 0;
-                for (int j = 0; j < n; ++j) before += mine[j] > p;
-                sorted[before] = p;
-            }
-            __syncthreads();
-            // two ranked tokens a thread: their weights and counts, added up in order
-            constexpr int kPer = kList / kThreads;
-            u64 w[kPer], mine_sum = 0, total;
-            for (int j = 0; j < kPer; ++j) {
-                const int i = tid * kPer + j;
-                w[j] = i < n ? coarse(weight(logit_of((unsigned)(sorted[i] >> 32)))) : 0;
-                mine_sum += w[j];
-            }
-            u64 sum = block_scan(mine_sum, sh.c.warp_sums, &total);
-            const u64 target = sh.c.target, above = sh.c.above;
-            for (int j = 0; j < kPer; ++j) {
-                const int i = tid * kPer + j;
-                const u64 before = sum;
-                sum += w[j];
-                const bool last = counts ? (u64)i + 1 == target : before < target && target <= sum;
-                if (i < n && last) {
-                    for (int r = 0; r < ranks; ++r) cluster.map_shared_rank(&sh, r)->c.boundary = sorted[i];
-                    sh.c.total = above + sum;
+            u64 n = 0, w = 0, total;
+            if (tid < kDigits)
+                for (int r = 0; r < ranks; ++r) {
+                    const Shared &o = *cluster.map_shared_rank(&sh, r);
+                    n += o.digit_n[tid];
+                    w += o.digit_w[tid];
                 }
-            }
-            if (tid == 0) sh.c.list_n = 0;
+            const u64 v = counts ? n : w;
+            const u64 before = block_scan(v, sh.warp_sums, &total);
+            if (before < left && left <= before + v)
+                sh.narrow_left = left - before, sh.narrow_n = (unsigned)n, sh.narrow_digit = kDigits - 1 - tid;
+            cluster.sync();  // and every CTA has read the others' digits
+            left = sh.narrow_left;
+            population = sh.narrow_n;
+            prefix = prefix << 8 | sh.narrow_digit;
+            bits += 8;
         }
-        cluster.sync();
-        return bits > 0;  // the row's bins are gone
+        gather(bin, bin, bits, prefix, true);
+        end_of_list(min((int)population, kList), counts, left);
     };
 
-    u64 boundary = 0;
+    bool summed = false;  // `mine` is what this thread's kept tokens weigh
+    u64 mine = 0;
     if (by_count || by_weight) {
-        histogram(-1, 0, 0);
-        bool stale = false, cut = false;
-        if (by_count) {
-            // tokens that are -inf are not in the bins: with fewer others than top_k nothing is cut
-            u64 n = 0, total;
-            if (rank == 0) {
-                for (int b = tid; b < kBins; b += kThreads) n += sh.all_cnt[b];
-                block_scan(n, sh.c.warp_sums, &total);
-                if (tid == 0) {
-                    for (int r = 0; r < ranks; ++r) {
-                        Control &o = cluster.map_shared_rank(&sh, r)->c;
-                        o.found = total > (u64)top_k;
-                        o.target = (u64)top_k, o.above = 0;
-                    }
-                }
+        // interleaved: the order does not matter here
+#pragma unroll 2
+        for (int i = tid * 2; i < a.seg * kThreads; i += 2 * kThreads) {
+            const float2 x = *reinterpret_cast<const float2 *>(xs + i);
+            int b0, b1;
+            weight.bins(x.x, x.y, b0, b1);
+            if (x.x != -INFINITY) atomicAdd(&sh.cnt[b0], 1u);
+            if (x.y != -INFINITY) atomicAdd(&sh.cnt[b1], 1u);
+        }
+        __syncthreads();
+        // a bin's weight in the estimate, 2^-30 of the largest
+        auto middle = [&](int b) { return sh.octave[b & 63] >> (b >> 6); };
+        {
+            unsigned n = 0;
+            u64 w = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int b = (tid >> 3) * 64 + j * 8 + (tid & 7);
+                const unsigned here = sh.cnt[b];
+                n += here;
+                if (by_weight) w += here * middle(b);
             }
-            cluster.sync();
-            cut = sh.c.found;
-            cluster.sync();
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                n += __shfl_xor_sync(0xffffffffu, n, o);
+                w += __shfl_xor_sync(0xffffffffu, w, o);
+            }
+            if ((tid & 7) == 0) sh.group_n[tid >> 3] = n, sh.group_w[tid >> 3] = w;
+        }
+        cluster.sync();
+        {
+            unsigned n = 0;
+            u64 w = 0;
+            for (int r = tid & 7; r < ranks; r += 8) {
+                const Shared &o = *cluster.map_shared_rank(&sh, r);
+                n += o.group_n[tid >> 3];
+                w += o.group_w[tid >> 3];
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                n += __shfl_xor_sync(0xffffffffu, n, o);
+                w += __shfl_xor_sync(0xffffffffu, w, o);
+            }
+            if ((tid & 7) == 0) sh.groups_n[tid >> 3] = n, sh.groups_w[tid >> 3] = w;
+        }
+        __syncthreads();
+        // the row's bins of one group
+        auto read_group = [&](int group) {
+            unsigned n = 0;
+            for (int r = tid & 7; r < ranks; r += 8) n += cluster.map_shared_rank(&sh, r)->cnt[group * 64 + (tid >> 3)];
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            if ((tid & 7) == 0) sh.bins_n[tid >> 3] = n;
+            __syncthreads();
+        };
+        bool cut = false;
+        int cut_bin = kBins - 1;
+        unsigned cut_left = 0;
+        unsigned cut_n = 0;  // tokens of the cut's bin
+        u64 cut_w = 0;       // estimated weights down to the cut
+        if (by_count) {
+            u64 before, n_all;
+            const int group = reach(sh.groups_n[2 * lane], sh.groups_n[2 * lane + 1], (u64)top_k, &before, &n_all);
+            // -inf is in no bin: with no more than top_k others, top-k leaves everything
+            cut = n_all > (u64)top_k;
             if (cut) {
-                stale = select(true);
-                boundary = sh.c.boundary;
+                read_group(group);
+                auto read = cluster.barrier_arrive();
+                u64 in_group, bins_all;
+                const int at = reach(sh.bins_n[2 * lane], sh.bins_n[2 * lane + 1], (u64)top_k - before, &in_group, &bins_all);
+                cut_bin = group * 64 + at;
+                cut_left = (unsigned)((u64)top_k - before - in_group);
+                cut_n = sh.bins_n[at];
+                const unsigned cut_to = (unsigned)top_k - cut_left + cut_n;
+                cluster.barrier_wait(std::move(read));  // nobody reads this CTA's bins for this any more
+                if (cut_to <= kList) {
+                    // everything that can be kept, in one list; rank 0 alone goes on
+                    gather(0, cut_bin, 0, 0, false);
+                    if (rank != 0) return;
+                    const int n = min((int)sh.list_n, kList);
+                    bool in = false;
+                    int my_i = 0;
+                    u64 my_w = 0, my_before = 0, all;
+                    rank_list(n, 0, n, [&](int i, int before_i, u64 w_before) {
+                        in = before_i < top_k;
+                        my_i = i, my_before = w_before;
+                        my_w = in ? sh.weight[i] : 0;
+                    });
+                    if (by_weight) {
+                        block_scan(my_w, sh.warp_sums, &all);
+                        in = in && my_before < wanted(all);
+                    }
+                    in = in && my_w >= floor_w && my_w > 0;
+                    const u64 kept_w = in ? my_w : 0;
+                    block_scan(kept_w, sh.warp_sums, &all);
+                    // in the order of the vocabulary: what is kept before each token
+                    if (tid < n) sh.weight[tid] = 0;
+                    __syncthreads();
+                    if (in) sh.weight[my_i] = kept_w;
+                    __syncthreads();
+                    const u64 target = drawn_at(all);
+                    if (in) {
+                        const unsigned mine_low = (unsigned)sh.list[my_i];
+                        u64 sum = 0;
+#pragma unroll 4
+                        for (int j = 0; j < n; ++j)
+                            if ((unsigned)sh.list[j] > mine_low) sum += sh.weight[j];  // a lower index
+                        if (sum <= target && target < sum + kept_w) {
+                            a.token[row] = (int)~mine_low;
+                            if (a.prob) a.prob[row] = share_f32(kept_w, all);
+                        }
+                    }
+                    return;
+                }
+                // the estimate of what top-k keeps, while the bins are at hand
+                if (by_weight) {
+                    u64 w0 = 0, w1 = 0, none, sum;
+                    const int b = 2 * lane;
+                    if (b < group) w0 = sh.groups_w[b];
+                    if (b + 1 < group) w1 = sh.groups_w[b + 1];
+                    if (b <= at) w0 += (b < at ? sh.bins_n[b] : cut_left) * middle(group * 64 + b);
+                    if (b + 1 <= at) w1 += (b + 1 < at ? sh.bins_n[b + 1] : cut_left) * middle(group * 64 + b + 1);
+                    reach(w0, w1, 1, &none, &sum);
+                    cut_w = sum;
+                }
             }
         }
+        int guess_bin = 0;
         if (by_weight) {
-            if (stale) {
-                for (int i = tid; i < kBins; i += kThreads) {
-                    sh.cnt[i] = sh.hi[i] = sh.lo[i] = 0;
-                    if (rank == 0) sh.all_w[i] = 0, sh.all_cnt[i] = 0;
-                }
-                cluster.sync();
-                histogram(-1, 0, 0);
-            }
-            if (rank == 0) {
-                u64 w = 0, total;
-                for (int b = tid; b < kBins; b += kThreads) w += sh.all_w[b];
-                block_scan(w, sh.c.warp_sums, &total);
-                if (tid == 0) {
-                    if (cut) total = sh.c.total;
-                    const u64 target = (u64)ceil((double)top_p * (double)total);
-                    for (int r = 0; r < ranks; ++r) {
-                        Control &o = cluster.map_shared_rank(&sh, r)->c;
-                        o.target = target < 1 ? 1 : target, o.above = 0;
+            // where the estimate says that top-p ends
+            u64 before, all, none;
+            reach(sh.groups_w[2 * lane], sh.groups_w[2 * lane + 1], 1, &before, &all);
+            const u64 guess = wanted(cut ? cut_w : all);
+            const int group = reach(sh.groups_w[2 * lane], sh.groups_w[2 * lane + 1], guess, &before, &all);
+            __syncthreads();  // every warp is done with the cut's bins
+            read_group(group);
+            const int b = 2 * lane;
+            const int at = reach(sh.bins_n[b] * middle(group * 64 + b),
+                                 sh.bins_n[b + 1] * middle(group * 64 + b + 1), guess - min(before, guess), &none, &all);
+            guess_bin = min(group * 64 + at, cut_bin);
+        }
+        cluster.sync();  // every CTA has read the others' bins
+        if (cut) end_of_bin(cut_bin, cut_n, true, cut_left);
+        if (by_weight) {
+            int from = max(0, min(guess_bin - kWindow / 2, kBins - kWindow));
+            u64 left = 0;
+            int bin = 0;
+            unsigned population = 0;
+            for (;;) {
+                // exact sums: all that passes, above the window, the window's bins; its tokens are set aside
+                for (int i = tid; i < kSums; i += kThreads) sh.sums[i] = 0;
+                if (tid < kWindow) sh.bin_lo[tid] = sh.bin_hi[tid] = sh.bin_n[tid] = 0;
+                if (tid == 0) sh.mine_n = 0;
+                __syncthreads();
+                u64 total = 0, above = 0;
+                unsigned aside_bits = 0;  // of up to 32 values: those in the window
+                auto take = [&](float x, int i, unsigned wa, unsigned wm, int bin_x, int bit) {
+                    const bool in = passes(x, i);
+                    const int b = bin_x - from;
+                    wa = in ? wa : 0;
+                    total += (u64)wa * wm;
+                    above += (u64)(b < 0 ? wa : 0) * wm;
+                    aside_bits |= in && (unsigned)b < (unsigned)kWindow ? 1u << bit : 0u;
+                };
+                unsigned wa[2], wm[2];
+                int bins[2];
+                for (int chunk = first; chunk < first + a.seg; chunk += 32) {
+                    const int to = min(first + a.seg, chunk + 32);
+                    int i = chunk;
+#pragma unroll 2
+                    for (; i + 1 < to; i += 2) {
+                        const float x0 = xs[i], x1 = xs[i + 1];
+                        weight.pair(x0, x1, wa, wm, bins);
+                        take(x0, i, wa[0], wm[0], bins[0], i - chunk);
+                        take(x1, i + 1, wa[1], wm[1], bins[1], i - chunk + 1);
+                    }
+                    if (i < to) {
+                        weight.pair(xs[i], xs[i], wa, wm, bins);
+                        take(xs[i], i, wa[0], wm[0], bins[0], i - chunk);
+                    }
+                    // room for the warp's at once
+                    if (__any_sync(0xffffffffu, aside_bits != 0)) {
+                        const unsigned n = __popc(aside_bits);
+                        unsigned sum = n;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const unsigned t = __shfl_up_sync(0xffffffffu, sum, o);
+                            if (lane >= o) sum += t;
+                        }
+                        unsigned room = 0;
+                        if (lane == 31) room = atomicAdd(&sh.mine_n, sum);
+                        room = __shfl_sync(0xffffffffu, room, 31) + sum - n;
+                        for (; aside_bits; aside_bits &= aside_bits - 1, ++room)
+                            if (room < kMine) sh.mine[room] = place(chunk + __ffs(aside_bits) - 1);
                     }
                 }
+                mine = above;
+                for (int o = 16; o > 0; o >>= 1) {
+                    total += __shfl_xor_sync(0xffffffffu, total, o);
+                    above += __shfl_xor_sync(0xffffffffu, above, o);
+                }
+                if (lane == 0) sh.part[0][warp] = total, sh.part[1][warp] = above;
+                __syncthreads();
+                if (tid < 2) {
+                    u64 sum = 0;
+                    for (int w = 0; w < kThreads / 32; ++w) sum += sh.part[tid][w];
+                    sh.sums[tid] = sum;
+                }
+                const int aside = (int)sh.mine_n;
+                if (aside <= kMine) {
+                    // a weight in 21 and 22 bits: 32-bit sums of up to kMine (shared memory adds 32-bit
+                    // integers at once, 64-bit ones in a loop that 500 threads would queue for)
+                    for (int i = tid; i < aside; i += kThreads) {
+                        const float x = logit_of((unsigned)(sh.mine[i] >> 32));
+                        const int b = weight.bin(x) - from;
+                        const u64 w = weight(x);
+                        atomicAdd(&sh.bin_lo[b], (unsigned)w & 0x1fffffu);
+                        atomicAdd(&sh.bin_hi[b], (unsigned)(w >> 21));
+                        atomicAdd(&sh.bin_n[b], 1u);
+                    }
+                    __syncthreads();
+                    if (tid < kWindow) {
+                        sh.sums[2 + tid] = ((u64)sh.bin_hi[tid] << 21) + sh.bin_lo[tid];
+                        sh.sums[2 + kWindow + tid] = sh.bin_n[tid];
+                    }
+                } else {  // no room: from the values again
+                    if (tid == 0) sh.sums[kSums - 1] = 1;
+                    for (int j = 0; j < a.seg; ++j) {
+                        const float x = xs[first + j];
+                        const int b = weight.bin(x) - from;
+                        if ((unsigned)b >= (unsigned)kWindow || !passes(x, first + j)) continue;
+                        atomicAdd(&sh.sums[2 + b], weight(x));
+                        atomicAdd(&sh.sums[2 + kWindow + b], 1ull);
+                    }
+                }
+                cluster.sync();
+                if (tid < kSums) {
+                    u64 s = 0;
+#pragma unroll 4
+                    for (int r = 0; r < ranks; ++r) s += cluster.map_shared_rank(&sh, r)->sums[tid];
+                    sh.all[tid] = s;
+                }
+                __syncthreads();
+                const u64 target = wanted(sh.all[0]);
+                u64 w = sh.all[1];
+                bool in_window = false;
+                if (target > w)
+                    for (int b = 0; b < kWindow; ++b) {
+                        const u64 here = sh.all[2 + b];
+                        if (target <= w + here) {
+                            in_window = true;
+                            bin = from + b, left = target - w, population = (unsigned)sh.all[2 + kWindow + b];
+                            break;
+                        }
+                        w += here;
+                    }
+                if (in_window) break;
+                from = target <= sh.all[1] ? max(0, from - kWindow) : min(kBins - kWindow, from + kWindow);
+                cluster.sync();  // every CTA has read the others' sums
             }
-            cluster.sync();
-            select(false);
-            boundary = boundary > sh.c.boundary ? boundary : sh.c.boundary;
+            summed = sh.all[kSums - 1] == 0 && population <= kList;
+            if (summed) {
+                // the bin's tokens are among those set aside
+                const int n = (int)sh.mine_n;
+                static_assert(kMine == 2 * kThreads, "two tokens a thread");
+                auto of_bin = [&](int i) {
+                    const u64 p = i < n ? sh.mine[i] : 0;
+                    return p && weight.bin(logit_of((unsigned)(p >> 32))) == bin ? p : 0;
+                };
+                send(of_bin(tid), of_bin(tid + kThreads), true);
+                cluster.sync();
+                end_of_list((int)population, false, left);
+                // what each thread keeps of them
+                sh.extra[tid] = 0;
+                __syncthreads();
+                for (int i = tid; i < n; i += kThreads) {
+                    const u64 p = sh.mine[i];
+                    const int at = (int)~(unsigned)p + shift - base;
+                    if (passes(xs[at], at)) atomicAdd(&sh.extra[at / a.seg], weight(xs[at]));
+                }
+                __syncthreads();
+                mine += sh.extra[tid];
+                summed = floor_w == 0;
+            } else {
+                cluster.sync();  // every CTA has read the others' sums
+                end_of_bin(bin, population, false, left);
+            }
         }
     }
 
     // the kept weights, in the order of the vocabulary
-    auto kept = [&](int j) -> u64 {
-        const float x = xs[tid * a.seg + j];
-        if (x == -INFINITY) return 0;
-        if (boundary && place_of(x, base + tid * a.seg + j - shift) < boundary) return 0;
+    auto kept = [&](int i) -> u64 {
+        const float x = xs[i];
+        if (!passes(x, i)) return 0;
         const u64 w = weight(x);
         return w >= floor_w ? w : 0;
     };
-    u64 mine = 0, total;
-    for (int j = 0; j < a.seg; ++j) mine += kept(j);
-    u64 before = block_scan(mine, sh.c.warp_sums, &total);
-    if (tid < ranks) cluster.map_shared_rank(&sh, tid)->c.totals[rank] = total;
+    if (!summed) {
+        mine = 0;
+        auto take = [&](float x, int i, unsigned wa, unsigned wm) {
+            const u64 w = (u64)wa * wm;
+            if (passes(x, i) && w >= floor_w) mine += w;
+        };
+        unsigned wa[2], wm[2];
+        int bins[2];
+        weight.pair(xs[first], xs[first], wa, wm, bins);
+        take(xs[first], first, wa[0], wm[0]);
+#pragma unroll 2
+        for (int i = first + 1; i < first + a.seg; i += 2) {
+            const float x0 = xs[i], x1 = xs[i + 1];
+            weight.pair(x0, x1, wa, wm, bins);
+            take(x0, i, wa[0], wm[0]);
+            take(x1, i + 1, wa[1], wm[1]);
+        }
+    }
+    u64 total;
+    u64 before = block_scan(mine, sh.warp_sums, &total);
+    if (tid < ranks) cluster.map_shared_rank(&sh, tid)->totals[rank] = total;
     cluster.sync();
     u64 all = 0;
     for (int r = 0; r < ranks; ++r) {
         if (r == rank) before += all;
-        all += sh.c.totals[r];
+        all += sh.totals[r];
     }
-    // the first token whose sum exceeds u * all
-    u64 target = u > 0.0f ? (u64)((double)u * (double)all) : 0;
-    if (target >= all) target = all - 1;
-    if (before <= target && target < before + mine) {
-        for (int j = 0; j < a.seg; ++j) {
-            const u64 w = kept(j);
-            before += w;
-            if (before > target) {
-                a.token[row] = base + tid * a.seg + j - shift;
-                if (a.prob) a.prob[row] = (float)((double)w / (double)all);
-                break;
+    // the first token whose sum exceeds u * all: its thread's warp looks for it together
+    const u64 target = drawn_at(all);
+    const unsigned owner = __ballot_sync(0xffffffffu, before <= target && target < before + mine);
+    if (owner) {
+        const int from = __ffs(owner) - 1;
+        before = __shfl_sync(0xffffffffu, before, from);
+        const int start = __shfl_sync(0xffffffffu, first, from);
+        for (int j = 0; j < a.seg; j += 32) {
+            const int i = start + j + lane;
+            const u64 w = j + lane < a.seg ? kept(i) : 0;
+            u64 to = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 t = __shfl_up_sync(0xffffffffu, to, o);
+                if (lane >= o) to += t;
             }
+            if (before + to - w <= target && target < before + to) {
+                a.token[row] = index_of(i);
+                if (a.prob) a.prob[row] = share_f32(w, all);
+            }
+            before += __shfl_sync(0xffffffffu, to, 31);
         }
     }
 }
