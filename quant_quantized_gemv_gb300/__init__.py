@@ -814,7 +814,7 @@ class MQKVCache:
 def _on_current(index: int):
     """The calls below run on the current device; its index, if it is `index`."""
     import torch
-    if torch.cuda.current_device() != index:
+    if torch._C._cuda_getDevice() != index:
         raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
     return index
 
@@ -824,24 +824,39 @@ def _raw_stream(stream, index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _rows(t, nt, cols, dtype, index, what):
-    """The address of a [nt, cols] CUDA tensor whose rows are contiguous (any row stride)."""
+def _bad_tensor(t, shape, dtype, index, what):
     if t.dtype is not dtype or t.get_device() != index:
         raise TypeError(f"{what}: expected {dtype} on cuda:{index}, got {t.dtype} on {t.device}")
-    if t.dim() != 2 or t.shape[0] != nt or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: expected [{nt}, {cols}] with contiguous rows, got {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{what}: expected {shape}, got {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _rows(t, nt, cols, dtype, index, what):
+    """The address of a [nt, cols] CUDA tensor whose rows are contiguous, and its row stride."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (nt, cols):
+        _bad_tensor(t, f"[{nt}, {cols}] with contiguous rows", dtype, index, what)
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    if cols > 1 and t.stride(1) != 1:
+        _bad_tensor(t, f"[{nt}, {cols}] with contiguous rows", dtype, index, what)
+    return t.data_ptr(), t.stride(0)
 
 
 def _vec(t, n, dtype, index, what):
     """The address of a contiguous CUDA tensor of n values; None for None."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.get_device() != index:
-        raise TypeError(f"{what}: expected {dtype} on cuda:{index}, got {t.dtype} on {t.device}")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what}: expected {n} contiguous values, got {tuple(t.shape)}")
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        _bad_tensor(t, f"{n} contiguous values", dtype, index, what)
     return t.data_ptr()
+
+
+def _page_table(pages, nt, seq):
+    if pages.dim() != 2:
+        raise ValueError("pages: expected [sequences, pages per sequence]")
+    n_seqs, per_seq = pages.shape
+    if seq is None and n_seqs < nt:
+        raise ValueError(f"pages: {nt} rows but {n_seqs} sequences")
+    return n_seqs, per_seq
 
 
 def mq_rope_table(freqs, device=None):
@@ -873,26 +888,24 @@ def mq_rope_append(kv: MQKVCache, q, k, v, positions, pages, q_out=None, rope=No
     nt, nq = q.shape
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=f32, device=q.device)
-    if pages.dim() != 2:
-        raise ValueError("pages: expected [sequences, pages per sequence]")
-    if seq is None and pages.shape[0] < nt:
-        raise ValueError(f"pages: {nt} rows but {pages.shape[0]} sequences")
+    n_seqs, per_seq = _page_table(pages, nt, seq)
     if nq % d != 0:
         raise ValueError(f"q: {nq} columns are no whole heads of {d}")
-    half = 0 if rope is None else rope.numel()
+    half, nk = 0 if rope is None else rope.numel(), hkv * d
+    qp, qs = _rows(q, nt, nq, f32, dev, "q")
+    kp, ks = _rows(k, nt, nk, f32, dev, "k")
+    vp, vs = _rows(v, nt, nk, f32, dev, "v")
+    op, os_ = _rows(q_out, nt, nq, f32, dev, "q_out")
     args = _RopeAppendStruct(
-        nt, nq // d, 2 * half, ROPE_STYLES[style], eps,
-        _rows(q, nt, nq, f32, dev, "q"), _rows(k, nt, hkv * d, f32, dev, "k"),
-        _rows(v, nt, hkv * d, f32, dev, "v"), q.stride(0) if nt > 1 else nq,
-        k.stride(0) if nt > 1 else hkv * d, v.stride(0) if nt > 1 else hkv * d,
-        _rows(q_out, nt, nq, f32, dev, "q_out"), q_out.stride(0) if nt > 1 else nq,
-        _vec(q_bias, nq, f32, dev, "q_bias"), _vec(k_bias, hkv * d, f32, dev, "k_bias"),
-        _vec(v_bias, hkv * d, f32, dev, "v_bias"), _vec(q_gain, d, f32, dev, "q_gain"),
+        nt, nq // d, 2 * half, ROPE_STYLES[style], eps, qp, kp, vp, qs, ks, vs, op, os_,
+        _vec(q_bias, nq, f32, dev, "q_bias"), _vec(k_bias, nk, f32, dev, "k_bias"),
+        _vec(v_bias, nk, f32, dev, "v_bias"), _vec(q_gain, d, f32, dev, "q_gain"),
         _vec(k_gain, d, f32, dev, "k_gain"), _vec(rope, half, torch.int64, dev, "rope"),
         _vec(positions, nt, i32, dev, "positions"), _vec(seq, nt, i32, dev, "seq"),
-        _vec(pages, pages.numel(), i32, dev, "pages"), pages.shape[0], pages.shape[1],
-        _vec(status, 1, i32, dev, "status"))
-    _check(lib().mq_rope_append(kv._ref, ctypes.byref(args), _raw_stream(stream, dev)), "mq_rope_append")
+        _vec(pages, n_seqs * per_seq, i32, dev, "pages"), n_seqs, per_seq, _vec(status, 1, i32, dev, "status"))
+    st = (_lib or lib()).mq_rope_append(kv._ref, ctypes.byref(args), _raw_stream(stream, dev))
+    if st:
+        raise MQError(st, "mq_rope_append")
     return q_out
 
 
@@ -926,29 +939,28 @@ def mq_attn_decode(kv: MQKVCache, q, lens, pages, scale: float, out=None, q8=Non
     nt, nq = q.shape
     if out is None:
         out = torch.empty(q.shape, dtype=f32, device=q.device)
-    if pages.dim() != 2:
-        raise ValueError("pages: expected [sequences, pages per sequence]")
-    if seq is None and pages.shape[0] < nt:
-        raise ValueError(f"pages: {nt} rows but {pages.shape[0]} sequences")
+    n_seqs, per_seq = _page_table(pages, nt, seq)
     if nq % d != 0:
         raise ValueError(f"q: {nq} columns are no whole heads of {d}")
     if max_len is None:
-        max_len = pages.shape[1] * kv.page_size
+        max_len = per_seq * kv.page_size
     if q8 is not None:
         _vec(q8, q8.numel(), torch.uint8, dev, "q8")
         if q8.numel() < nt * mq_q8_bytes(nq):
             raise ValueError(f"q8: smaller than {nt} planes of {nq} values")
     if ws is None:
         ws = mq_attn_workspace(kv, nq // d, nt, max_len)
-    wsb = 0 if ws is None else ws.numel() * ws.element_size()
+    wsb = 0 if ws is None else ws.numel()
+    qp, qs = _rows(q, nt, nq, f32, dev, "q")
+    op, os_ = _rows(out, nt, nq, f32, dev, "out")
     args = _AttnStruct(
-        nt, nq // d, max_len, window, scale, softcap, _rows(q, nt, nq, f32, dev, "q"),
-        _rows(out, nt, nq, f32, dev, "out"), q.stride(0) if nt > 1 else nq, out.stride(0) if nt > 1 else nq,
+        nt, nq // d, max_len, window, scale, softcap, qp, op, qs, os_,
         None if q8 is None else q8.data_ptr(), _vec(lens, nt, i32, dev, "lens"), _vec(seq, nt, i32, dev, "seq"),
-        _vec(pages, pages.numel(), i32, dev, "pages"), pages.shape[0], pages.shape[1],
-        None if ws is None else _vec(ws, ws.numel(), torch.uint8, dev, "ws"), wsb,
+        _vec(pages, n_seqs * per_seq, i32, dev, "pages"), n_seqs, per_seq, _vec(ws, wsb, torch.uint8, dev, "ws"), wsb,
         _vec(status, 1, i32, dev, "status"))
-    _check(lib().mq_attn_decode(kv._ref, ctypes.byref(args), _raw_stream(stream, dev)), "mq_attn_decode")
+    st = (_lib or lib()).mq_attn_decode(kv._ref, ctypes.byref(args), _raw_stream(stream, dev))
+    if st:
+        raise MQError(st, "mq_attn_decode")
     return out
 
 
@@ -967,10 +979,12 @@ def mq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     nt, vocab = logits.shape
     if token is None:
         token = torch.empty(nt, dtype=i32, device=logits.device)
+    lp, ls = _rows(logits, nt, vocab, f32, dev, "logits")
     args = _SampleStruct(
-        nt, vocab, _rows(logits, nt, vocab, f32, dev, "logits"), logits.stride(0) if nt > 1 else vocab,
-        _vec(u, nt, f32, dev, "u"), _vec(temperature, nt, f32, dev, "temperature"),
+        nt, vocab, lp, ls, _vec(u, nt, f32, dev, "u"), _vec(temperature, nt, f32, dev, "temperature"),
         _vec(top_p, nt, f32, dev, "top_p"), _vec(min_p, nt, f32, dev, "min_p"), _vec(top_k, nt, i32, dev, "top_k"),
         _vec(token, nt, i32, dev, "token"), _vec(prob, nt, f32, dev, "prob"))
-    _check(lib().mq_sample(ctypes.byref(args), _raw_stream(stream, dev)), "mq_sample")
+    st = (_lib or lib()).mq_sample(ctypes.byref(args), _raw_stream(stream, dev))
+    if st:
+        raise MQError(st, "mq_sample")
     return token

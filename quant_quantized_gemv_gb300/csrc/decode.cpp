@@ -1,6 +1,6 @@
 // decode.cpp -- the C ABI of the operators around the GEMVs of a decode step
 // (include/mq.h: paged cache, rotation and append, attention, draw): argument
-// checks, the attention's split, then the launch.  Nothing here allocates.
+// checks, the attention's grid, then the launch.  Nothing here allocates.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -38,54 +38,44 @@ int kv_check(const mq_kv_cache *kv, size_t *page_stride, size_t *head_bytes)
     return MQ_OK;
 }
 
-// How the tokens of an attention call are cut: pieces of a unit (a row's group
-// of up to 8 heads of one kv head) and tokens of a piece, for `span` tokens at
-// the most.  Few units: as many pieces as fill the GPU once, of 64 tokens or
-// more.  Many: pieces of 1024 tokens or more, up to a few waves, so that ragged
-// rows even out.
-struct AttnPlan {
-    int pieces, piece_len;
-};
-
-constexpr long long kPieceQuantum = kAttnWarps * kAttnTile;  // a piece is whole rounds of its warps
-constexpr int kAttnWaves = 4;
-
-long long attn_wave(int sms) { return (long long)sms * 3; }  // CTAs resident at once
-
-AttnPlan attn_plan(long long units, long long span, int sms)
+// CTAs of an attention launch over `units` units (a row's group of up to 8
+// heads of one kv head) of up to `span` tokens each: one resident wave, or fewer
+// when there are fewer rounds of tokens than that.  Beyond kAttnMaxRows rows: a
+// CTA per unit.
+int attn_wave(int sms, int head_dim)
 {
-    const long long rounds = (span + kPieceQuantum - 1) / kPieceQuantum;
-    long long few = attn_wave(sms) / units, many = kAttnWaves * attn_wave(sms) / units;
-    if (few > rounds) few = rounds;
-    if (many > span / 1024) many = span / 1024;
-    long long pieces = few > many ? few : many;
-    if (pieces > kAttnMaxPieces) pieces = kAttnMaxPieces;
-    if (pieces < 1) pieces = 1;
-    const long long len = (rounds + pieces - 1) / pieces * kPieceQuantum;
-    return AttnPlan{(int)((span + len - 1) / len), (int)len};
+    const int n = sms * attn_ctas(head_dim);
+    return n < kAttnMaxCtas ? n : kAttnMaxCtas;
 }
 
-// Workspace of calls of up to `units` units and max_len tokens, any window.
-// First the arrival counters, in a place and number that no call changes (a
-// workspace may serve calls of different sizes, and every counter must be zero
-// before each): units of 2 pieces or more number at most half of all the CTAs
-// planned.  Then the partial results: at most units x the pieces of the
-// longest row, and never more than the CTAs planned; both bounds only grow with
-// units and max_len.
-size_t attn_count_bytes(int sms)
+long long attn_rounds(long long span, int head_dim)
 {
-    return ((size_t)(kAttnWaves * attn_wave(sms) / 2) * 4 + 15) & ~(size_t)15;
+    const int round = attn_warps(head_dim) * kAttnTile;
+    return (span + round - 1) / round;
 }
 
-size_t attn_ws_bytes(long long units, int max_len, int sms, int head_dim)
+long long attn_grid(long long units, long long span, int nt, int sms, int head_dim)
 {
-    const long long span = (long long)max_len + kAttnTile - 1;
-    long long most = (span + kPieceQuantum - 1) / kPieceQuantum;
-    if (max_len <= kPieceQuantum) return 0;
-    if (most > kAttnMaxPieces) most = kAttnMaxPieces;
-    long long parts = units * most;
-    if (parts > kAttnWaves * attn_wave(sms)) parts = kAttnWaves * attn_wave(sms);
-    return attn_count_bytes(sms) + (size_t)parts * attn_part_floats(head_dim) * 4;
+    if (nt > kAttnMaxRows) return units;
+    const long long rounds = units * attn_rounds(span, head_dim);
+    const long long wave = attn_wave(sms, head_dim);
+    return rounds < wave ? rounds : wave;
+}
+
+// Workspace of a call: a counter and two partial results for each CTA that
+// shares out the work, in places that no call changes (a workspace may serve
+// calls of different sizes, and every counter must be zero before each).  None
+// for rows so short that no unit is cut.
+size_t attn_count_bytes(int sms, int head_dim)
+{
+    return ((size_t)attn_wave(sms, head_dim) * 4 + 15) & ~(size_t)15;
+}
+
+size_t attn_ws_bytes(int max_len, int sms, int head_dim)
+{
+    if (attn_rounds((long long)max_len + kAttnTile - 1, head_dim) <= kAttnWhole) return 0;
+    return attn_count_bytes(sms, head_dim) +
+           (size_t)attn_wave(sms, head_dim) * 2 * attn_part_floats(head_dim) * 4;
 }
 
 bool attn_shape_ok(const mq_kv_cache *kv, int n_heads, int nt, int max_len)
@@ -93,8 +83,10 @@ bool attn_shape_ok(const mq_kv_cache *kv, int n_heads, int nt, int max_len)
     if (mq_kv_page_bytes(kv->type, kv->n_kv_heads, kv->page_size, kv->head_dim) == 0) return false;
     if (nt < 1 || n_heads < 1 || n_heads % kv->n_kv_heads != 0 || max_len < 1) return false;
     if (max_len > 0x7fffffff - 4096) return false;
-    // the grid: every unit in its most pieces; a q8 plane's values
-    return (long long)nt * n_heads < (1LL << 24) && (long long)n_heads * kv->head_dim < (1LL << 30);
+    // the grid and the rounds of a row and of all rows; a q8 plane's values
+    const long long rounds = attn_rounds((long long)max_len + kAttnTile - 1, kv->head_dim);
+    return (long long)nt * n_heads < (1LL << 24) && (long long)n_heads * kv->head_dim < (1LL << 30) &&
+           n_heads * rounds < (1LL << 31) && nt * rounds < (1LL << 31);
 }
 
 long long attn_units(const mq_kv_cache *kv, int n_heads, int nt)
@@ -181,7 +173,7 @@ size_t mq_attn_workspace_bytes(const mq_kv_cache *kv, int n_heads, int nt, int m
     if (!kv || !attn_shape_ok(kv, n_heads, nt, max_len)) return 0;
     const int sms = mq_device_sms();
     if (sms <= 0) return 0;
-    return attn_ws_bytes(attn_units(kv, n_heads, nt), max_len, sms, kv->head_dim);
+    return nt > kAttnMaxRows ? 0 : attn_ws_bytes(max_len, sms, kv->head_dim);
 }
 
 int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *a, void *stream)
@@ -210,15 +202,14 @@ int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *a, void *stream)
     // a window starts inside a tile of its own
     long long span = a->max_len;
     if (a->window > 0 && (long long)a->window + kAttnTile - 1 < span) span = (long long)a->window + kAttnTile - 1;
-    const AttnPlan plan = attn_plan(units, span, sms);
-    if (plan.pieces > 1) {
+    r.ctas = (int)attn_grid(units, span, a->nt, sms, D);
+    if (a->nt <= kAttnMaxRows && attn_rounds(span, D) > kAttnWhole) {
         if (!a->ws) return MQ_ERR_NULL;
-        if (a->ws_bytes < attn_count_bytes(sms) + (size_t)units * plan.pieces * attn_part_floats(D) * 4)
+        if (a->ws_bytes < attn_count_bytes(sms, D) + (size_t)r.ctas * 2 * attn_part_floats(D) * 4)
             return MQ_ERR_WORKSPACE;
+        r.ws_cnt = (unsigned *)a->ws;
+        r.ws_part = (float *)((uint8_t *)a->ws + attn_count_bytes(sms, D));
     }
-    r.pieces = plan.pieces, r.piece_len = plan.piece_len;
-    r.ws_cnt = (unsigned *)a->ws;
-    r.ws_part = plan.pieces > 1 ? (float *)((uint8_t *)a->ws + attn_count_bytes(sms)) : nullptr;
     r.q = a->q, r.out = a->out, r.q_stride = a->q_stride, r.out_stride = a->out_stride;
     r.q8 = (uint8_t *)a->q8;
     r.q8_stride = (unsigned)q8_plane_bytes(n);

@@ -212,19 +212,23 @@ struct RopeAppendLaunch {
     int type, n_pages, page_size, n_kv_heads, head_dim;  // the cache (type: MQ_KV_*)
     int nt, n_heads, rope_dims, style, n_seqs, pages_stride;
     float eps;
-    int lanes_per_head, units, ctas_per_row;  // set by the launch
+    int lanes_per_head, groups_per_cta, ctas_per_row;  // set by the launch
 };
 cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_t st);
 
 // Attention over the paged cache (attn_decode.cu), already checked.  A unit
-// is a row's group of up to kAttnHeads query heads of one kv head; its tokens
-// are cut into pieces of piece_len, one CTA each.  Units of more than one
-// piece leave partial results in ws_part (attn_part_floats each) and the
-// piece that arrives last joins them.
+// is a row's group of up to kAttnHeads query heads of one kv head.  Up to
+// kAttnMaxRows rows: `ctas` CTAs share out the tokens of all units evenly, and
+// units cut by it leave partial results in ws_part (two of attn_part_floats a
+// CTA) and meet by the counters of ws_cnt (one a CTA).  More rows: a CTA a unit.
 constexpr int kAttnHeads = 8;        // query heads of a CTA (rows of its matrix products)
-constexpr int kAttnWarps = 4;        // warps of a CTA
 constexpr int kAttnTile = 16;        // tokens a warp takes at a time
-constexpr int kAttnMaxPieces = 128;  // most pieces of a unit
+constexpr int kAttnMaxRows = 1024;
+constexpr int kAttnMaxCtas = 512;    // CTAs that share out the work
+constexpr int kAttnWhole = 2;        // units of so many rounds or less are not cut
+// Warps of a CTA and CTAs of an SM for a head size (what a tile's registers allow).
+__host__ __device__ constexpr int attn_warps(int head_dim) { return head_dim <= 128 ? 12 : 8; }
+__host__ __device__ constexpr int attn_ctas(int head_dim) { return 1; }
 constexpr int attn_part_floats(int head_dim) { return kAttnHeads * (head_dim + 2); }
 
 struct AttnLaunch {
@@ -241,8 +245,8 @@ struct AttnLaunch {
     int nt, n_heads, n_seqs, pages_stride, max_len, window;
     float scale, softcap;
     int group, subgroups;            // query heads of a kv head; CTAs' groups of 8 in it
-    int pieces, piece_len;
-    unsigned *ws_cnt;                // arrivals, one per unit
+    int ctas;                        // CTAs of the launch
+    unsigned *ws_cnt;
     float *ws_part;
 };
 cudaError_t launch_attn_decode(const AttnLaunch &a, int pdl, cudaStream_t st);

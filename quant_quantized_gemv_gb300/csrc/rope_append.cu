@@ -17,15 +17,19 @@
 // values a head), so 16 lanes (head_dim <= 64) or 32 hold a head, loads and
 // f32 stores are float4, and the partner of a value under MQ_ROPE_HALF is
 // rope_dims / 2 values away in another lane at the same place (rope_dims a
-// multiple of 2 EPL): one shuffle per value, no shared memory.  A lane's
-// cosines and sines depend on its place in the head and the row's position
-// only: computed once, used for every head the warp takes.  A q8 block is
-// 32 / EPL lanes: max and codes as in the q8 producers.
+// multiple of 2 EPL): one shuffle per value.  A q8 block is 32 / EPL lanes: max
+// and codes as in the q8 producers.
 //
-// Work: a row has n_heads + 2 n_kv_heads heads; a warp takes `units` groups
-// of heads of one row (a group is what its 32 lanes hold).  Few rows: one
-// group a warp, for latency.  Many rows: more groups a warp share the angles
-// (launch_rope_append states the rule and what it measured).
+// Work: a row's heads, queries | keys | values, in groups of what a warp's lanes
+// hold, are shared by the CTAs of the row.  A CTA first writes down where each
+// of its groups is read and what becomes of it, then all its loads are under way
+// while it finds the row's page and one thread per pair computes an angle.
+//
+// What bounds it: few rows, the launch and three dependent loads (2.9 us a call
+// in a captured chain).  Many rows, latency and instructions before HBM: 4096
+// rows of the 14B shape (40 + 8 + 8 heads of 128) take 53 us, 4.1 TB/s, where
+// their 218 MB take 33; 28 groups a CTA of 4 warps (56 in 8 warps: 55, one load
+// ahead and every warp its own angles: 57 to 65, one group a warp: 123).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,11 +42,26 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4;
+constexpr int kUnits = 7;  // groups of heads a warp takes when there are many rows
+constexpr int kMaxGroups = kWarps * kUnits;
 
 template <int EPL>
 struct Vals {
     float v[EPL];
 };
+
+// Biases and gains are weights, which no preceding kernel writes.
+template <int EPL>
+__device__ __forceinline__ Vals<EPL> load_weight(const float *p)
+{
+    Vals<EPL> r;
+#pragma unroll
+    for (int i = 0; i < EPL; i += 4) {
+        const float4 f = __ldg(reinterpret_cast<const float4 *>(p + i));
+        r.v[i] = f.x, r.v[i + 1] = f.y, r.v[i + 2] = f.z, r.v[i + 3] = f.w;
+    }
+    return r;
+}
 
 template <int EPL>
 __device__ __forceinline__ Vals<EPL> load_cg(const float *p)
@@ -70,139 +89,168 @@ __device__ __forceinline__ void store16(uint8_t *dst, const Vals<EPL> &x)
     else *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<uint4 *>(t);
 }
 
+// A group of heads: where it is read, its biases, and its first head.
+struct alignas(16) Group {
+    const float *src, *bias;
+    float *dst;             // queries: their place in q_out
+    int kind, head, heads;  // 0 queries, 1 keys, 2 values; heads that exist (1 or 2)
+};
+
 template <int EPL>
 __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppendLaunch a)
 {
+    constexpr int kBatch = EPL == 4 ? kUnits : (kUnits + 1) / 2;  // groups a warp loads at a time
+    __shared__ Group groups[kMaxGroups];
+    __shared__ float cosine[128], sine[128];
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x / a.ctas_per_row;
-    const int first = ((blockIdx.x - t * a.ctas_per_row) * kWarps + (threadIdx.x >> 5)) * a.units;
-    const int lph = a.lanes_per_head;               // 16 or 32
-    const int sub = lane & ~(lph - 1);              // first lane of this lane's head
-    const int e = (lane - sub) * EPL;               // first value of this lane
-    const int D = a.head_dim;
-    const bool in_head = e < D;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, D = a.head_dim;
+    const int lph = a.lanes_per_head, hpw = 32 / lph;  // lanes of a head: 16 or 32
     const int half = a.rope_dims >> 1;
-    const bool rotated = e < a.rope_dims;
-    const bool upper = e >= half;                   // MQ_ROPE_HALF: the b of its pairs
-    const int hpw = 32 / lph;
+    const int sub = lane >= lph ? 1 : 0, e = (lane & (lph - 1)) * EPL;  // this lane's head of a group, first value
+    const bool in_head = e < D, rotated = e < a.rope_dims;
+    const bool upper = e >= half;  // MQ_ROPE_HALF: the b of its pairs
+    const int from = (lane + (rotated ? (upper ? -half : half) / EPL : 0)) & 31;
+
+    // this CTA's row and groups
+    const int t = blockIdx.x / a.ctas_per_row, c = blockIdx.x - t * a.ctas_per_row;
+    const int gq = (a.n_heads + hpw - 1) / hpw, gk = (a.n_kv_heads + hpw - 1) / hpw;
+    const int first = c * a.groups_per_cta, n = min(a.groups_per_cta, gq + 2 * gk - first);
+    for (int i = tid; i < n; i += kWarps * 32) {
+        const int gr = first + i, kind = gr < gq ? 0 : gr < gq + gk ? 1 : 2;
+        const int h = (kind == 0 ? gr : kind == 1 ? gr - gq : gr - gq - gk) * hpw;
+        const float *bias = kind == 0 ? a.q_bias : kind == 1 ? a.k_bias : a.v_bias;
+        Group &g = groups[i];
+        g.src = (kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride) + h * D;
+        g.bias = bias ? bias + h * D : nullptr;
+        g.dst = a.q_out + t * a.q_out_stride + h * D;
+        g.kind = kind, g.head = h;
+        g.heads = min(hpw, (kind == 0 ? a.n_heads : a.n_kv_heads) - h);
+    }
+    const unsigned long long step = tid < half ? __ldg(a.rope_table + tid) : 0;  // no preceding kernel writes it
+    __syncthreads();
     griddep_wait();  // q, k, v (and the positions) may come from the preceding kernels
 
     const int pos = __ldcg(a.positions + t);
+    Vals<EPL> x[kBatch];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + k * kWarps;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) x[k].v[j] = 0.0f;
+            if (i < n && in_head && sub < groups[i].heads) x[k] = load_cg<EPL>(groups[i].src + sub * D + e);
+        }
+    };
+    load(warp);  // on their way while the page and the angles are found
     if (pos < 0) return;  // padding
 
+    if (tid < half) {
+        // a signed fraction of a turn, rounded once: x 2^-64, then x 2 for sincospi's half turns
+        const float h = __ll2float_rn((long long)((unsigned long long)pos * step)) * 0x1p-63f;
+        sincospif(h, &sine[tid], &cosine[tid]);
+    }
     // the row's page; a row that names none writes nothing but NaN queries
     const int seq = a.seq ? __ldcg(a.seq + t) : t;
     const int pi = pos / a.page_size, slot = pos - pi * a.page_size;
-    bool ok = (unsigned)seq < (unsigned)a.n_seqs && pi < a.pages_stride;
-    const int page = ok ? __ldcg(a.pages + (size_t)seq * a.pages_stride + pi) : -1;
-    ok = (unsigned)page < (unsigned)a.n_pages;
-    if (!ok && a.status && first == 0 && lane == 0) atomicOr(a.status, 1);
-
+    const bool named = (unsigned)seq < (unsigned)a.n_seqs && pi < a.pages_stride;
+    const int page = named ? __ldcg(a.pages + (size_t)seq * a.pages_stride + pi) : -1;
+    const bool ok = (unsigned)page < (unsigned)a.n_pages;
+    if (!ok && a.status && c == 0 && tid == 0) atomicOr(a.status, 1);
+    const size_t page_at = (size_t)(ok ? page : 0) * a.page_stride, slot_at = (size_t)slot * D + e;
+    __syncthreads();
     float cs[EPL], sn[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         cs[i] = 1.0f, sn[i] = 0.0f;
         if (!rotated) continue;
         const int at = a.style == 0 ? e + i - (upper ? half : 0) : (e + i) >> 1;
-        if (a.style != 0 && (i & 1)) {
-            cs[i] = cs[i - 1], sn[i] = -sn[i - 1];  // the pair's b
-            continue;
-        }
-        const unsigned long long turn = (unsigned long long)pos * __ldg(a.rope_table + at);
-        // a signed fraction of a turn, rounded once: x 2^-64, then x 2 for sincospi's half turns
-        const float h = __ll2float_rn((long long)turn) * 0x1p-63f;
-        float s, c;
-        sincospif(h, &s, &c);
-        cs[i] = c;
-        sn[i] = a.style == 0 && upper ? s : -s;
+        cs[i] = cosine[at];
+        sn[i] = (a.style == 0 ? upper : (i & 1) != 0) ? sine[at] : -sine[at];
     }
-    const int heads = a.n_heads + 2 * a.n_kv_heads;
-    const int groups = (heads + hpw - 1) / hpw;
-    const int last = min(first + a.units, groups);
-    for (int gr = first; gr < last; ++gr) {  // uniform across the warp: the shuffles below see all lanes
-        const int hd = gr * hpw + (sub ? 1 : 0);
-        const bool valid = in_head && hd < heads;
-        const int kind = hd < a.n_heads ? 0 : hd < a.n_heads + a.n_kv_heads ? 1 : 2;
-        const int h = kind == 0 ? hd : kind == 1 ? hd - a.n_heads : hd - a.n_heads - a.n_kv_heads;
-        const float *src = kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
-        const float *bias = kind == 0 ? a.q_bias : kind == 1 ? a.k_bias : a.v_bias;
-        const float *gain = kind == 0 ? a.q_gain : kind == 1 ? a.k_gain : nullptr;
-        Vals<EPL> x;
+
+    for (int i0 = warp; i0 < n; i0 += kBatch * kWarps) {
+        if (i0 != warp) load(i0);
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) x.v[i] = 0.0f;
-        if (valid) {
-            x = load_cg<EPL>(src + h * D + e);
-            if (bias) {
-                const Vals<EPL> b = load_cg<EPL>(bias + h * D + e);
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + k * kWarps;  // uniform across the warp: the shuffles below see all lanes
+            if (i >= n) break;
+            const Group &g = groups[i];
+            const int kind = g.kind;
+            const bool valid = in_head && sub < g.heads;
+            if (g.bias && valid) {
+                const Vals<EPL> b = load_weight<EPL>(g.bias + sub * D + e);
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) x.v[i] += b.v[i];
+                for (int j = 0; j < EPL; ++j) x[k].v[j] += b.v[j];
             }
-        }
-        if (a.q_gain || a.k_gain) {
-            float ss = 0.0f;
+            if (kind < 2) {
+                const float *gain = kind == 0 ? a.q_gain : a.k_gain;
+                if (gain) {
+                    float ss = 0.0f;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) ss = fmaf(x.v[i], x.v[i], ss);
-            for (int o = lph >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-            if (valid && gain) {
-                const float scale = 1.0f / sqrtf(ss / (float)D + a.eps);
-                const Vals<EPL> g = load_cg<EPL>(gain + e);
+                    for (int j = 0; j < EPL; ++j) ss = fmaf(x[k].v[j], x[k].v[j], ss);
+                    for (int o = lph >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+                    if (valid) {
+                        const float scale = 1.0f / sqrtf(ss / (float)D + a.eps);
+                        const Vals<EPL> w = load_weight<EPL>(gain + e);
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) x.v[i] = (x.v[i] * scale) * g.v[i];
+                        for (int j = 0; j < EPL; ++j) x[k].v[j] = (x[k].v[j] * scale) * w.v[j];
+                    }
+                }
+                if (half > 0) {
+                    Vals<EPL> p;
+                    if (a.style == 0) {
+#pragma unroll
+                        for (int j = 0; j < EPL; ++j) p.v[j] = __shfl_sync(kFull, x[k].v[j], from);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < EPL; ++j) p.v[j] = x[k].v[j ^ 1];
+                    }
+                    if (rotated) {
+#pragma unroll
+                        for (int j = 0; j < EPL; ++j) x[k].v[j] = fmaf(x[k].v[j], cs[j], p.v[j] * sn[j]);
+                    }
+                }
+                if (kind == 0) {
+                    if (!ok) {
+#pragma unroll
+                        for (int j = 0; j < EPL; ++j) x[k].v[j] = __int_as_float(0x7fc00000);
+                    }
+                    if (valid) {
+                        float *dst = g.dst + sub * D + e;
+#pragma unroll
+                        for (int j = 0; j < EPL; j += 4)
+                            *reinterpret_cast<float4 *>(dst + j) =
+                                make_float4(x[k].v[j], x[k].v[j + 1], x[k].v[j + 2], x[k].v[j + 3]);
+                    }
+                    continue;
+                }
             }
-        }
-        if (half > 0) {
-            Vals<EPL> p;
-            if (a.style == 0) {
-                const int from = (lane + (rotated ? (upper ? -half : half) / EPL : 0)) & 31;
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) p.v[i] = __shfl_sync(kFull, x.v[i], from);
+            uint8_t *base = (kind == 1 ? a.k_pages : a.v_pages) + page_at + (size_t)(g.head + sub) * a.head_bytes;
+            const bool cached = valid && ok;
+            if (a.type == 1) {
+                if (cached) store16<EPL, __half>(base + slot_at * 2, x[k]);
+            } else if (a.type == 2) {
+                if (cached) store16<EPL, __nv_bfloat16>(base + slot_at * 2, x[k]);
             } else {
+                float am = 0.0f;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) p.v[i] = x.v[i ^ 1];
-            }
-            if (kind < 2 && rotated) {
+                for (int j = 0; j < EPL; ++j) am = fmaxf(am, fabsf(x[k].v[j]));
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) x.v[i] = fmaf(x.v[i], cs[i], p.v[i] * sn[i]);
-            }
-        }
-        if (kind == 0 && valid) {
-            float *dst = a.q_out + t * a.q_out_stride + h * D + e;
-            if (!ok) {
+                for (int o = 1; o < 32 / EPL; o <<= 1) am = fmaxf(am, __shfl_xor_sync(kFull, am, o));
+                const float d = am / 127.0f;
+                const float di = (d != 0.0f) ? 1.0f / d : 0.0f;
+                uint32_t w[EPL / 4];
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) x.v[i] = __int_as_float(0x7fc00000);
-            }
+                for (int j = 0; j < EPL; ++j) {
+                    const int q = max(-128, min(127, __float2int_rn(x[k].v[j] * di)));
+                    w[j / 4] = (j & 3) ? w[j / 4] | ((uint32_t)(q & 0xff) << (8 * (j & 3))) : (uint32_t)(q & 0xff);
+                }
+                if (cached) {
 #pragma unroll
-            for (int i = 0; i < EPL; i += 4)
-                *reinterpret_cast<float4 *>(dst + i) = make_float4(x.v[i], x.v[i + 1], x.v[i + 2], x.v[i + 3]);
-        }
-        uint8_t *base = (kind == 1 ? a.k_pages : a.v_pages) + (size_t)(ok ? page : 0) * a.page_stride +
-                        (size_t)h * a.head_bytes;
-        const bool cached = kind != 0 && valid && ok;
-        const size_t at = (size_t)slot * D + e;
-        if (a.type == 1) {
-            if (cached) store16<EPL, __half>(base + at * 2, x);
-        } else if (a.type == 2) {
-            if (cached) store16<EPL, __nv_bfloat16>(base + at * 2, x);
-        } else {
-            float am = 0.0f;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) am = fmaxf(am, fabsf(x.v[i]));
-#pragma unroll
-            for (int o = 1; o < 32 / EPL; o <<= 1) am = fmaxf(am, __shfl_xor_sync(kFull, am, o));
-            const float d = am / 127.0f;
-            const float di = (d != 0.0f) ? 1.0f / d : 0.0f;
-            uint32_t w[EPL / 4];
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int q = max(-128, min(127, __float2int_rn(x.v[i] * di)));
-                w[i / 4] = (i & 3) ? w[i / 4] | ((uint32_t)(q & 0xff) << (8 * (i & 3))) : (uint32_t)(q & 0xff);
-            }
-            if (cached) {
-#pragma unroll
-                for (int i = 0; i < EPL / 4; ++i) reinterpret_cast<uint32_t *>(base + at)[i] = w[i];
-                if ((e & 31) == 0)
-                    reinterpret_cast<__half *>(base + (size_t)a.page_size * D)[at >> 5] = __float2half_rn(d);
+                    for (int j = 0; j < EPL / 4; ++j) reinterpret_cast<uint32_t *>(base + slot_at)[j] = w[j];
+                    if ((e & 31) == 0)
+                        reinterpret_cast<__half *>(base + (size_t)a.page_size * D)[slot_at >> 5] = __float2half_rn(d);
+                }
             }
         }
     }
@@ -214,14 +262,14 @@ cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_
 {
     a.lanes_per_head = a.head_dim <= 64 ? 16 : 32;
     const int hpw = 32 / a.lanes_per_head;
-    const int groups = (a.n_heads + 2 * a.n_kv_heads + hpw - 1) / hpw;
-    // One group a warp while the grid is within two resident waves of 32 warps an SM; then as
-    // many as keep it there, up to 8.
-    const long long wave = (long long)sms * 64;
+    const int groups = (a.n_heads + hpw - 1) / hpw + 2 * ((a.n_kv_heads + hpw - 1) / hpw);
+    // Few rows: a group a warp, for latency.  More: up to kUnits groups a warp, which share the
+    // row's angles and its page.
+    const long long wave = (long long)sms * 32;  // warps
     long long units = ((long long)a.nt * groups + wave - 1) / wave;
-    a.units = (int)(units < 1 ? 1 : units > 8 ? 8 : units);
-    const int warps = (groups + a.units - 1) / a.units;
-    a.ctas_per_row = (warps + kWarps - 1) / kWarps;
+    units = units < 1 ? 1 : units > kUnits ? kUnits : units;
+    a.groups_per_cta = (int)units * kWarps;
+    a.ctas_per_row = (groups + a.groups_per_cta - 1) / a.groups_per_cta;
     const dim3 grid((unsigned)((long long)a.nt * a.ctas_per_row));
     const auto kernel = a.head_dim <= 128 ? rope_append_kernel<4> : rope_append_kernel<8>;
     return launch_maybe_pdl(kernel, grid, dim3(kWarps * 32), 0, pdl, st, a);
