@@ -7,28 +7,32 @@
 //
 // Every cached byte is used by the 1..8 query heads of its kv head, a handful
 // of operations a byte: the pass is bound by HBM when contexts are long and
-// by latency when they are short, never by the tensor cores.  So each warp
-// streams its tokens straight into registers, 16 at a time, with nothing
-// shared between warps until the end: no barrier and no shared-memory copy
-// of the cache.  tcgen05 products would need the tokens in shared memory and
-// a hand-over per tile, to fill 8 of 128 rows.
+// by latency when they are short, never by the tensor cores.  tcgen05 products
+// would fill 8 of their 128 rows and hand every tile over twice.
 //
-// One warp's 16 tokens, with m16n8k16 products (lane = 4 g + t):
+// Each warp streams its tokens, 16 at a time (a tile), through stages of its
+// own in shared memory, filled by 16-byte asynchronous copies: no warp waits for
+// another between a unit's first token and its last, and a warp's next tiles are
+// on their way, into the next unit too, while it works on one.  Rows are stored
+// with their 16-byte chunks permuted (chunk xor a key of the row) so that the
+// reads below touch every bank once.
+//
+// One tile, with m16n8k16 products (lane = 4 g + t):
 //   scores: rows 0..7 are the heads (one part of q), rows 8..15 the same heads
-//     (the next part of q), columns 8 tokens.  A lane's 16-byte load is 8
-//     consecutive values of token g; which values share a product's k slots is
-//     free as long as q's fragments follow, so the load needs no exchange.
+//     (the next part of q), columns 8 tokens.  A lane reads 8 consecutive values
+//     of token g; which values share a product's k slots is free as long as q's
+//     fragments follow, so nothing is exchanged.
 //   output: rows again heads and parts of p, k the 16 tokens, columns 8 values
-//     of v: a lane holds 8 consecutive values of tokens 2t, 2t+1, 2t+8, 2t+9,
-//     and one byte permute pairs two tokens of a value.  The scores' layout is
-//     the one p needs, so p never leaves its lane.
+//     of v: a lane reads consecutive values of tokens 2t, 2t+1, 2t+8, 2t+9, and
+//     one byte permute pairs two tokens of a value.  The scores' layout is the
+//     one p needs, so p never leaves its lane.
 // Parts: fp16 holds 11 bits, so q (scaled by a power of two a head) and p
 // (times 2^14) go in as hi + lo = 22 bits in the two halves of the 16 rows;
 // bf16 holds 8, so three parts in two products.  The cache's values are exact
 // in both (int8 codes in fp16).  Results then are as an f32 computation's.
 // q8: the scales of K (token, block of 32) multiply the block's partial
-// scores; the scales of V multiply p, block by block, scaled by a power of two
-// a tile (their maximum) to stay in fp16's range.
+// scores; the scales of V multiply p, block by block, in units of the largest
+// power of two met so far, to stay in fp16's range.
 //
 // Sums: every tile's products start from zero and are added to the f32
 // accumulators by the same fused multiply-add that rescales them, so no
@@ -42,7 +46,7 @@
 // memory at the end of a unit.  A unit that crosses from one share into the next
 // is joined through the workspace: its CTAs leave their partial results, and the
 // last to arrive (an atomic count; nobody waits) adds them in order.  Units of
-// kWhole rounds or less are not cut: the join costs more than they do.
+// kAttnWhole rounds or less are not cut: the join costs more than they do.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -106,97 +110,52 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel)
     return bits(__hsub2(half2_of(__byte_perm(w, 0x64646464u, sel)), half2_of(0x64806480u)));
 }
 
-// Registers of one 16-token tile: K rows of tokens g and 8 + g, V rows of
-// tokens 2t, 2t+1, 2t+8, 2t+9 (q8: and those tokens' scales).
-template <int TYPE, int D>
-struct Tile {
-    static constexpr int KC = D / 32, VC = (D + 63) / 64;
-    uint4 k[2][KC], v[4][VC];
-};
-template <int D>
-struct Tile<kQ8, D> {
-    static constexpr int KC = D / 32;
-    uint2 k[2][KC];
-    uint32_t v[4][KC];
-    alignas(8) __half ks[4][KC];
-    alignas(8) __half vs[4][KC];
-};
-
+// A token's scales, KC fp16 side by side.
 template <int KC>
 __device__ __forceinline__ void load_scales(__half (&s)[KC], const uint8_t *p)
 {
-    if constexpr (KC % 4 == 0) {
+    if constexpr (KC == 8) *reinterpret_cast<uint4 *>(&s[0]) = *reinterpret_cast<const uint4 *>(p);
+    else if constexpr (KC == 4) *reinterpret_cast<uint2 *>(&s[0]) = *reinterpret_cast<const uint2 *>(p);
+    else if constexpr (KC == 2) *reinterpret_cast<uint32_t *>(&s[0]) = *reinterpret_cast<const uint32_t *>(p);
+    else {
 #pragma unroll
-        for (int i = 0; i < KC; i += 4)
-            *reinterpret_cast<uint2 *>(&s[i]) = __ldcg(reinterpret_cast<const uint2 *>(p) + i / 4);
-    } else if constexpr (KC % 2 == 0) {
-        *reinterpret_cast<unsigned *>(&s[0]) = __ldcg(reinterpret_cast<const unsigned *>(p));
-    } else {
-#pragma unroll
-        for (int i = 0; i < KC; ++i) {
-            const unsigned short u = __ldcg(reinterpret_cast<const unsigned short *>(p) + i);
-            s[i] = *reinterpret_cast<const __half *>(&u);
-        }
+        for (int i = 0; i < KC; ++i) s[i] = reinterpret_cast<const __half *>(p)[i];
     }
 }
 
-template <int TYPE, int D>
-__device__ __forceinline__ void load_k(Tile<TYPE, D> &r, const uint8_t *head, int slot, int page_size, int g, int t)
+// 16 bytes to shared memory, asynchronously; `bytes` of them from src (0: all zero).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
 {
-    constexpr int KC = D / 32;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        if constexpr (TYPE == kQ8) {
-            const uint8_t *p = head + (size_t)(slot + 8 * j + g) * D + 8 * t;
-#pragma unroll
-            for (int c = 0; c < KC; ++c) r.k[j][c] = __ldcg(reinterpret_cast<const uint2 *>(p + 32 * c));
-        } else {
-            const uint8_t *p = head + ((size_t)(slot + 8 * j + g) * D + 8 * t) * 2;
-#pragma unroll
-            for (int c = 0; c < KC; ++c) r.k[j][c] = __ldcg(reinterpret_cast<const uint4 *>(p + 64 * c));
-        }
-    }
-    if constexpr (TYPE == kQ8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int tok = slot + 8 * (i >> 1) + 2 * t + (i & 1);
-            load_scales<KC>(r.ks[i], head + (size_t)page_size * D + (size_t)tok * (KC * 2));
-        }
-    }
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t shared_address(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// Tokens outside [lo, hi) (relative to the tile) are not read and count as 0.
+// Sizes of a kernel instance.
 template <int TYPE, int D>
-__device__ __forceinline__ void load_v(Tile<TYPE, D> &r, const uint8_t *head, int slot, int page_size, int g, int t,
-                                       int lo, int hi)
-{
-    constexpr int KC = D / 32, VC = (D + 63) / 64;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int tok = 8 * (i >> 1) + 2 * t + (i & 1);
-        const bool seen = tok >= lo && tok < hi;
-        if constexpr (TYPE == kQ8) {
-            const uint8_t *p = head + (size_t)(slot + tok) * D + 4 * g;
-#pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                r.v[i][c] = 0;
-                r.vs[i][c] = __ushort_as_half(0);
-            }
-            if (seen) {
-#pragma unroll
-                for (int c = 0; c < KC; ++c) r.v[i][c] = __ldcg(reinterpret_cast<const unsigned *>(p + 32 * c));
-                load_scales<KC>(r.vs[i], head + (size_t)page_size * D + (size_t)(slot + tok) * (KC * 2));
-            }
-        } else {
-            const uint8_t *p = head + ((size_t)(slot + tok) * D + 8 * g) * 2;
-#pragma unroll
-            for (int c = 0; c < VC; ++c) {
-                r.v[i][c] = make_uint4(0, 0, 0, 0);
-                if (seen && 64 * c + 8 * g < D) r.v[i][c] = __ldcg(reinterpret_cast<const uint4 *>(p + 128 * c));
-            }
-        }
-    }
-}
+struct Shape {
+    static constexpr int warps = attn_warps(TYPE, D), threads = warps * 32, round = warps * kAttnTile;
+    static constexpr int stages = attn_stages(TYPE, D);
+    static constexpr int KC = D / 32;
+    static constexpr int row = TYPE == kQ8 ? D : 2 * D;              // bytes of a token's K or V
+    static constexpr int pitch = row < 128 ? 128 : row == 192 ? 256 : row;  // the same in a stage: room for the permutation
+    static constexpr int matrix = kAttnTile * pitch;
+    static constexpr int scales = TYPE == kQ8 ? kAttnTile * KC * 2 : 0;  // bytes of a tile's K or V scales
+    static constexpr int stage = 2 * matrix + 2 * scales;            // K, V, K's scales, V's scales
+};
+
+// Keys of a row's chunk permutation.  A quarter of a warp reads 16 bytes of K from rows 2k, 2k+1 at 4
+// places each, and of V from rows of one parity at 2 places each; of q8's K it reads 32 bytes a row
+// from 4 rows in turn, of its V from every other row.
+template <int TYPE>
+__device__ __forceinline__ int k_key(int row) { return TYPE == kQ8 ? (row & 3) << 1 : (row & 1) << 2 | ((row >> 1) & 3); }
+template <int TYPE>
+__device__ __forceinline__ int v_key(int row) { return TYPE == kQ8 ? ((row >> 1) & 3) << 1 : row & 7; }
 
 // Place of accumulator j (pair element e) of lane t within a head.
 template <int TYPE>
@@ -205,62 +164,65 @@ __device__ __forceinline__ int value_of(int j, int e, int t)
     return TYPE == kQ8 ? 32 * (j >> 2) + 4 * (2 * t + e) + (j & 3) : 64 * (j >> 3) + 8 * (2 * t + e) + (j & 7);
 }
 
-template <int D>
-struct Shape {
-    static constexpr int warps = attn_warps(D), threads = warps * 32, round = warps * kAttnTile;
-    static constexpr int ctas = attn_ctas(D);
-};
-
-// Shared memory: q's fragments, the warps' exchange (later the join's weights), the rows' rounds.
 template <int TYPE, int D>
 struct Smem {
-    static constexpr int KC = D / 32, RS = D + 4;
-    uint4 q_frag[2 * KC][32];                              // q's parts as the products take them
-    uint2 q_low[TYPE == kBF16 ? 2 * KC : 1][32];           // bf16's third part
+    using S = Shape<TYPE, D>;
+    alignas(128) uint8_t ring[S::warps][S::stages][S::stage];
+    float q[S::stages + 1][kAttnHeads][D];                 // queries of the units on their way
+    uint4 q_frag[2 * S::KC][32];                           // q's parts as the products take them
+    uint2 q_low[TYPE == kBF16 ? 2 * S::KC : 1][32];        // bf16's third part
     union {
-        float x_o[Shape<D>::warps][kAttnHeads][RS];        // padded rows
+        float x_o[S::warps][kAttnHeads][D + 4];            // the warps' exchange
         float weight[kAttnMaxCtas][kAttnHeads];            // the join
     };
-    float x_m[Shape<D>::warps][kAttnHeads], x_l[Shape<D>::warps][kAttnHeads];
+    float x_m[S::warps][kAttnHeads], x_l[S::warps][kAttnHeads];
     float total[kAttnHeads];
-    int sums[Shape<D>::warps];
+    int sums[S::warps];
     int last;
-    int rounds[kAttnMaxRows + 1];                          // of the rows before each row
+    int rounds[kAttnMaxRows + 1], lens[kAttnMaxRows];      // rounds of the rows before each row; their tokens
+};
+
+// A place in the line of rounds: a unit, or the part of it that falls to this CTA.
+struct Segment {
+    int pos;                 // of its first round
+    int row, unit;           // unit of the row
+    int rounds, round, take; // of the unit; the first one here; how many here
 };
 
 template <int TYPE, int D>
-__global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::ctas) attn_decode_kernel(const AttnLaunch a)
+__global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel(const AttnLaunch a)
 {
-    constexpr int KC = D / 32;
-    constexpr int NJ = TYPE == kQ8 ? D / 8 : (D + 63) / 64 * 8;  // accumulator pairs a lane
-    constexpr int kWarps = Shape<D>::warps, kThreads = Shape<D>::threads, kRound = Shape<D>::round;
+    using S = Shape<TYPE, D>;
+    constexpr int KC = S::KC, VC = (D + 63) / 64, NS = S::stages;
+    constexpr int NJ = TYPE == kQ8 ? D / 8 : VC * 8;             // accumulator pairs a lane
+    constexpr int kWarps = S::warps, kThreads = S::threads, kRound = S::round;
     constexpr int kSlots = kAttnHeads * D / 4;                   // float4s of a unit's output
     constexpr int kPer = (kSlots + kThreads - 1) / kThreads;
     constexpr size_t part = kAttnHeads * (D + 2);                // attn_part_floats(D)
-    extern __shared__ __align__(16) unsigned char raw[];
+    extern __shared__ __align__(128) unsigned char raw[];
     Smem<TYPE, D> &sh = *reinterpret_cast<Smem<TYPE, D> *>(raw);
-    auto &q_frag = sh.q_frag;
-    auto &q_low = sh.q_low;
 
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     griddep_wait();  // queries, lengths, tables and the cache may come from the preceding kernels
 
     // first cached token and rounds of a row of n tokens (n < 0: padding, none; nothing to read: one)
-    auto start_of = [&](int n) { return (a.window > 0 ? max(0, n - a.window) : 0) & ~(kAttnTile - 1); };
+    auto first_of = [&](int n) { return a.window > 0 ? max(0, n - a.window) : 0; };
+    auto start_of = [&](int n) { return first_of(n) & ~(kAttnTile - 1); };
     auto too_long = [&](int n) { return n > a.max_len || (long long)n > (long long)a.pages_stride * a.page_size; };
     auto rounds_of = [&](int n) { return n < 0 ? 0 : n == 0 || too_long(n) ? 1 : (n - start_of(n) + kRound - 1) / kRound; };
 
     const int units = a.n_kv_heads * a.subgroups;  // of a row
     const bool shared_out = a.nt <= kAttnMaxRows;  // else a CTA per unit
-    long long pos, end;
-    long long share = 0;
+    int end, share = 0, single_n = 0;
+    Segment load_at;
     if (shared_out) {
         // rounds of the rows before each row
         int before = 0;
         for (int r0 = 0; r0 < a.nt; r0 += kThreads) {
             const int r = r0 + tid;
-            const int mine = r < a.nt ? rounds_of(__ldcg(a.lens + r)) : 0;
+            const int n = r < a.nt ? __ldcg(a.lens + r) : -1;
+            const int mine = rounds_of(n);
             int s = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -275,196 +237,269 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::ctas) attn_decode
                 if (w == warp) s += all;
                 all += sh.sums[w];
             }
-            if (r < a.nt) sh.rounds[r] = before + s - mine;
+            if (r < a.nt) sh.rounds[r] = before + s - mine, sh.lens[r] = n;
             before += all;
-            __syncthreads();
+            if (r0 + kThreads < a.nt) __syncthreads();
         }
         if (tid == 0) sh.rounds[a.nt] = before;
         __syncthreads();
-        const long long all = (long long)before * units;
-        share = max((all + gridDim.x - 1) / gridDim.x, 1LL);
-        pos = blockIdx.x * share;
-        end = min(pos + share, all);
+        const int all = before * units;
+        share = max((int)((all + gridDim.x - 1) / gridDim.x), 1);
+        load_at.pos = blockIdx.x * share;
+        end = min(load_at.pos + share, all);
+        if (load_at.pos >= end) return;
+        const int want = load_at.pos / units;
+        int lo = 0, hi = a.nt - 1;  // the last row whose rounds begin at or before
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (sh.rounds[mid] <= want) lo = mid;
+            else hi = mid - 1;
+        }
+        load_at.row = lo;
+        const int in_row = load_at.pos - sh.rounds[lo] * units, rounds = sh.rounds[lo + 1] - sh.rounds[lo];
+        load_at.unit = in_row / rounds;
+        load_at.round = in_row - load_at.unit * rounds;
     } else {
-        pos = 0, end = 1;
+        load_at.row = blockIdx.x / units;
+        load_at.unit = blockIdx.x - load_at.row * units;
+        load_at.pos = load_at.round = 0;
+        single_n = __ldcg(a.lens + load_at.row);
+        end = rounds_of(single_n);
     }
-
-    while (pos < end) {
-        // the unit at pos, its rounds and the first of them for this CTA
-        int row, unit, rounds, round;
-        if (shared_out) {
-            const int want = (int)(pos / units);
-            int lo = 0, hi = a.nt - 1;  // the last row whose rounds begin at or before
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (sh.rounds[mid] <= want) lo = mid;
-                else hi = mid - 1;
-            }
-            row = lo;
-            rounds = sh.rounds[row + 1] - sh.rounds[row];
-            const int in_row = (int)(pos - (long long)sh.rounds[row] * units);
-            unit = in_row / rounds;
-            round = in_row - unit * rounds;
-        } else {
-            row = blockIdx.x / units;
-            unit = blockIdx.x - row * units;
-            rounds = rounds_of(__ldcg(a.lens + row));
-            if (rounds == 0) return;
-            round = 0;
-            end = rounds;
-        }
-        const long long unit_at = pos - round;
-        int take = (int)min((long long)(rounds - round), end - pos);
-        if (shared_out && rounds <= kAttnWhole) {
+    auto n_of = [&](int row) { return shared_out ? sh.lens[row] : single_n; };
+    // completes a segment that begins where its fields say; false: none is left
+    auto enter = [&](Segment &s) {
+        for (;;) {
+            if (s.pos >= end) return false;
+            s.rounds = shared_out ? sh.rounds[s.row + 1] - sh.rounds[s.row] : end;
+            s.take = min(s.rounds - s.round, end - s.pos);
+            if (s.rounds > kAttnWhole) return true;
             // not cut: it belongs to the share in which it begins
-            if (round > 0) {
-                pos += rounds - round;
-                continue;
+            s.take = s.rounds;
+            if (s.round == 0) return true;
+            s.take = s.rounds - s.round;
+            s.pos += s.take, s.round = 0;
+            if (++s.unit == units) {
+                s.unit = 0;
+                do ++s.row;
+                while (s.row < a.nt && sh.rounds[s.row + 1] == sh.rounds[s.row]);
             }
-            take = rounds;
         }
-        pos += take;
-        const bool whole = take == rounds;
-        const int sg = unit % a.subgroups, kvh = unit / a.subgroups;
-        const int head0 = kvh * a.group + sg * kAttnHeads;
-        const int heads = min(kAttnHeads, a.group - sg * kAttnHeads);
+    };
+    auto leave = [&](Segment &s) {  // to where the next one begins
+        s.pos += s.take, s.round = 0;
+        if (++s.unit == units) {
+            s.unit = 0;
+            if (shared_out)
+                do ++s.row;
+                while (s.row < a.nt && sh.rounds[s.row + 1] == sh.rounds[s.row]);
+        }
+    };
 
-        const int n = __ldcg(a.lens + row);
-        const int seq = a.seq ? __ldcg(a.seq + row) : row;
+    // ---- the loading side: rounds ahead of the work
+    bool load_live = enter(load_at);
+    if (!load_live) return;
+    Segment at = load_at;  // the working side
+    int load_round = 0, load_count = 0;              // round of the segment; segments begun
+    int l_first = 0, l_n = 0, l_from = 0, l_to = 0, l_page = -1;
+    const int *l_table = nullptr;
+    size_t l_head = 0;
+    auto open_load = [&]() {
+        l_n = n_of(load_at.row);
+        const int seq = a.seq ? __ldcg(a.seq + load_at.row) : load_at.row;
+        const bool bad = (unsigned)seq >= (unsigned)a.n_seqs || too_long(l_n);
+        l_first = first_of(l_n);
+        l_from = start_of(l_n) + load_at.round * kRound + warp * kAttnTile;
+        l_to = bad ? 0 : min(l_n, start_of(l_n) + (load_at.round + load_at.take) * kRound);
+        l_table = a.pages + (bad ? 0 : (size_t)seq * a.pages_stride);
+        l_head = (size_t)(load_at.unit / a.subgroups) * a.head_bytes;
+    };
+    auto ask_page = [&]() {
+        if (l_from < l_to) l_page = __ldcg(l_table + l_from / a.page_size);
+    };
+    open_load();
+    ask_page();
+    unsigned missing = 0;  // stages whose page is not there
+    auto issue = [&](int stage) {
+        if (load_live) {
+            if (load_round == 0) {  // the unit's queries
+                const int sg = load_at.unit % a.subgroups, kvh = load_at.unit / a.subgroups;
+                const int head0 = kvh * a.group + sg * kAttnHeads, heads = min(kAttnHeads, a.group - sg * kAttnHeads);
+                const float *src = a.q + load_at.row * a.q_stride + (size_t)head0 * D;
+                const uint32_t dst = shared_address(sh.q[load_count % (NS + 1)]);
+                for (int i = tid; i < kSlots; i += kThreads)
+                    copy16(dst + i * 16, i < heads * (D / 4) ? src + i * 4 : src, i < heads * (D / 4) ? 16 : 0);
+            }
+            if (l_from < l_to) {
+                const bool there = (unsigned)l_page < (unsigned)a.n_pages;
+                missing = there ? missing & ~(1u << stage) : missing | 1u << stage;
+                const size_t page = (size_t)(there ? l_page : 0) * a.page_stride + l_head;
+                const int slot = l_from % a.page_size;
+                const uint8_t *k = a.k_pages + page + (size_t)slot * S::row, *v = a.v_pages + page + (size_t)slot * S::row;
+                const uint32_t to = shared_address(sh.ring[warp][stage]);
+                const int lo = l_first - l_from, hi = l_n - l_from;  // rows [lo, hi) are seen
+                constexpr int kChunks = S::row / 16;
+#pragma unroll
+                for (int j = 0; j < kAttnTile * kChunks / 32; ++j) {
+                    const int i = lane + 32 * j, r = i / kChunks, c = i % kChunks;
+                    copy16(to + r * S::pitch + ((c ^ k_key<TYPE>(r)) << 4), k + i * 16, 16);
+                }
+#pragma unroll
+                for (int j = 0; j < kAttnTile * kChunks / 32; ++j) {
+                    const int i = lane + 32 * j, r = i / kChunks, c = i % kChunks;
+                    // V's other rows are zeros: p is 0 there, whatever the cache holds
+                    copy16(to + S::matrix + r * S::pitch + ((c ^ v_key<TYPE>(r)) << 4), v + i * 16,
+                           r >= lo && r < hi ? 16 : 0);
+                }
+                if constexpr (TYPE == kQ8) {
+                    const size_t scales = (size_t)a.page_size * D + (size_t)slot * (KC * 2);
+                    const int i = lane & 15;
+                    if (i < 2 * KC)
+                        copy16(to + 2 * S::matrix + (lane >> 4) * S::scales + i * 16,
+                               (lane < 16 ? a.k_pages : a.v_pages) + page + scales + i * 16, 16);
+                }
+            }
+            ++load_round;
+            l_from += kRound;
+            if (load_round == load_at.take) {
+                leave(load_at);
+                load_live = enter(load_at);
+                load_round = 0, ++load_count;
+                if (load_live) open_load();
+            }
+            if (load_live) ask_page();
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < NS; ++s) issue(s);
+
+    // ---- the working side
+    const bool capped = a.softcap > 0.0f;
+    const float inv_cap = capped ? 1.0f / a.softcap : 0.0f;
+    int stage = 0;
+    for (int count = 0;; ++count) {
+        const int sg = at.unit % a.subgroups, kvh = at.unit / a.subgroups;
+        const int head0 = kvh * a.group + sg * kAttnHeads, heads = min(kAttnHeads, a.group - sg * kAttnHeads);
+        const int n = n_of(at.row), first = first_of(n);
+        const int from = start_of(n) + at.round * kRound + warp * kAttnTile;
+        const int seq = a.seq ? __ldcg(a.seq + at.row) : at.row;
         bool bad = (unsigned)seq >= (unsigned)a.n_seqs || too_long(n);
-        const int first = a.window > 0 ? max(0, n - a.window) : 0;  // tokens [first, n)
-        const int from = start_of(n) + round * kRound;
-        const int to = min(n, from + take * kRound);
-        const int *table = a.pages + (bad ? 0 : (size_t)seq * a.pages_stride);
+        const int to = bad ? 0 : min(n, start_of(n) + (at.round + at.take) * kRound);
+        const bool whole = at.take == at.rounds;
 
+        copies_wait<NS - 1>();
+        __syncthreads();  // the queries are there, in every warp's copies
         // q's fragments: lane (g, t) holds values 32 c + 8 t .. + 7 of head g.  The
         // factor brings the head's largest magnitude to [2^13, 2^14): its parts then
         // hold 22 bits of it, and the scores take the factor back.
-        float q_factor = 1.0f;
-        {
-            float x[KC][8];
+        float q_factor = 1.0f, up = 1.0f;
+        const float *q = sh.q[count % (NS + 1)][g] + 8 * t;
+        if constexpr (TYPE != kBF16) {
             float am = 0.0f;
-            const float *src = a.q + row * a.q_stride + (size_t)(head0 + g) * D + 8 * t;
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
-                float4 u = make_float4(0.f, 0.f, 0.f, 0.f), w = u;
-                if (g < heads) {
-                    u = __ldcg(reinterpret_cast<const float4 *>(src + 32 * c));
-                    w = __ldcg(reinterpret_cast<const float4 *>(src + 32 * c + 4));
-                }
-                x[c][0] = u.x, x[c][1] = u.y, x[c][2] = u.z, x[c][3] = u.w;
-                x[c][4] = w.x, x[c][5] = w.y, x[c][6] = w.z, x[c][7] = w.w;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(x[c][i]));
+                const float4 u = *reinterpret_cast<const float4 *>(q + 32 * c);
+                const float4 w = *reinterpret_cast<const float4 *>(q + 32 * c + 4);
+                am = fmaxf(am, fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))));
+                am = fmaxf(am, fmaxf(fmaxf(fabsf(w.x), fabsf(w.y)), fmaxf(fabsf(w.z), fabsf(w.w))));
             }
-            if constexpr (TYPE != kBF16) {
-                am = fmaxf(am, __shfl_xor_sync(kFull, am, 1));
-                am = fmaxf(am, __shfl_xor_sync(kFull, am, 2));
-                // 2^(13 - exponent), within f32's normal range both ways
-                const int e = min(max((int)(__float_as_uint(am) >> 23) - 127, -100), 100);
-                const float up = __uint_as_float((unsigned)(127 + 13 - e) << 23);
-                q_factor = __uint_as_float((unsigned)(127 - 13 + e) << 23);
-#pragma unroll
-                for (int c = 0; c < KC; ++c)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[c][i] *= up;
+            am = fmaxf(am, __shfl_xor_sync(kFull, am, 1));
+            am = fmaxf(am, __shfl_xor_sync(kFull, am, 2));
+            // 2^(13 - exponent), within f32's normal range both ways
+            const int e = min(max((int)(__float_as_uint(am) >> 23) - 127, -100), 100);
+            up = __uint_as_float((unsigned)(127 + 13 - e) << 23);
+            q_factor = __uint_as_float((unsigned)(127 - 13 + e) << 23);
+        }
+        for (int i = warp; i < 2 * KC; i += kWarps) {
+            const float4 y = *reinterpret_cast<const float4 *>(q + 32 * (i >> 1) + 4 * (i & 1));
+            uint4 f;
+            if constexpr (TYPE == kBF16) {
+                uint2 low;
+                split_bf16(y.x, y.y, f.x, f.y, low.x);
+                split_bf16(y.z, y.w, f.z, f.w, low.y);
+                sh.q_low[i][lane] = low;
+            } else {
+                split_f16(y.x * up, y.y * up, f.x, f.y);
+                split_f16(y.z * up, y.w * up, f.z, f.w);
             }
-#pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                if (c % kWarps != warp) continue;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint4 f;
-                    const float *y = &x[c][4 * h];
-                    if constexpr (TYPE == kBF16) {
-                        uint2 low;
-                        split_bf16(y[0], y[1], f.x, f.y, low.x);
-                        split_bf16(y[2], y[3], f.z, f.w, low.y);
-                        q_low[2 * c + h][lane] = low;
-                    } else {
-                        split_f16(y[0], y[1], f.x, f.y);
-                        split_f16(y[2], y[3], f.z, f.w);
-                    }
-                    q_frag[2 * c + h][lane] = f;
-                }
-            }
+            sh.q_frag[i][lane] = f;
         }
         __syncthreads();
-
-        const bool capped = a.softcap > 0.0f;
         // score factor: to base 2 at once, or to the score itself when capped
         const float s_factor = q_factor * a.scale * (capped ? 1.0f : kLog2e);
-        const float inv_cap = capped ? 1.0f / a.softcap : 0.0f;
 
         float o[NJ][2];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = 0.0f;
         float m = -INFINITY, l = 0.0f;  // head g: maximum (base 2) and this lane's part of the sum
+        int unit_exp = -30;             // q8: the sums of p v are in units of 2^unit_exp
 
-        int tok = from + warp * kAttnTile;
-        if (!bad && tok < to) {
-            const size_t head_off = (size_t)kvh * a.head_bytes;
-            auto page_at = [&](int token) {
-                const int p = __ldcg(table + token / a.page_size);
-                if ((unsigned)p < (unsigned)a.n_pages) return p;
-                bad = true;
-                return 0;
-            };
-            Tile<TYPE, D> r;
-            int page = page_at(tok), slot = tok % a.page_size;
-            load_k<TYPE, D>(r, a.k_pages + page * a.page_stride + head_off, slot, a.page_size, g, t);
-            load_v<TYPE, D>(r, a.v_pages + page * a.page_stride + head_off, slot, a.page_size, g, t, first - tok, n - tok);
-            int next = tok + kRound;
-            int page_next = next < to ? page_at(next) : 0;
-            for (;;) {
+        for (int r = 0; r < at.take; ++r) {
+            if (r > 0) copies_wait<NS - 1>();
+            __syncwarp();
+            const int tok = from + r * kRound;
+            if (tok < to) {
+                const uint8_t *kt = sh.ring[warp][stage], *vt = kt + S::matrix;
+                bad = bad || (missing >> stage & 1);
                 // scores of 16 tokens: s[j][e] is token 8 j + 2 t + e, head g
                 float s[2][2];
+                if constexpr (TYPE == kQ8) {
+                    alignas(16) __half ks[4][KC];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if constexpr (TYPE == kQ8) {
-                        s[j][0] = s[j][1] = 0.0f;
+                    for (int i = 0; i < 4; ++i)
+                        load_scales<KC>(ks[i], vt + S::matrix + (8 * (i >> 1) + 2 * t + (i & 1)) * (KC * 2));
+                    s[0][0] = s[0][1] = s[1][0] = s[1][1] = 0.0f;
 #pragma unroll
-                        for (int c = 0; c < KC; ++c) {
-                            const uint32_t w[2] = {r.k[j][c].x ^ 0x80808080u, r.k[j][c].y ^ 0x80808080u};
+                    for (int c = 0; c < KC; ++c) {
+                        const uint4 f0 = sh.q_frag[2 * c][lane], f1 = sh.q_frag[2 * c + 1][lane];
+                        const uint32_t q0[4] = {f0.x, f0.y, f0.z, f0.w}, q1[4] = {f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint2 w = *reinterpret_cast<const uint2 *>(kt + (8 * j + g) * S::pitch +
+                                                                       (((2 * c + (t >> 1)) ^ k_key<TYPE>(g)) << 4) + (t & 1) * 8);
+                            w.x ^= 0x80808080u, w.y ^= 0x80808080u;
                             float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint4 f = q_frag[2 * c + h][lane];
-                                const uint32_t qa[4] = {f.x, f.y, f.z, f.w};
-                                mma_f16(acc, qa, codes_f16(w[h], 0x4140), codes_f16(w[h], 0x4342));
-                            }
-                            s[j][0] = fmaf(acc[0] + acc[2], __half2float(r.ks[2 * j][c]), s[j][0]);
-                            s[j][1] = fmaf(acc[1] + acc[3], __half2float(r.ks[2 * j + 1][c]), s[j][1]);
+                            mma_f16(acc, q0, codes_f16(w.x, 0x4140), codes_f16(w.x, 0x4342));
+                            mma_f16(acc, q1, codes_f16(w.y, 0x4140), codes_f16(w.y, 0x4342));
+                            s[j][0] = fmaf(acc[0] + acc[2], __half2float(ks[2 * j][c]), s[j][0]);
+                            s[j][1] = fmaf(acc[1] + acc[3], __half2float(ks[2 * j + 1][c]), s[j][1]);
                         }
-                    } else {
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    }
+                } else {
+                    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-                        for (int c = 0; c < KC; ++c) {
+                    for (int c = 0; c < KC; ++c) {
+                        uint4 k[2];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint4 f = q_frag[2 * c + h][lane];
-                                const uint32_t qa[4] = {f.x, f.y, f.z, f.w};
-                                const uint32_t b0 = h ? r.k[j][c].z : r.k[j][c].x, b1 = h ? r.k[j][c].w : r.k[j][c].y;
+                        for (int j = 0; j < 2; ++j)
+                            k[j] = *reinterpret_cast<const uint4 *>(kt + (8 * j + g) * S::pitch +
+                                                                    (((4 * c + t) ^ k_key<TYPE>(g)) << 4));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 f = sh.q_frag[2 * c + h][lane];
+                            const uint32_t qa[4] = {f.x, f.y, f.z, f.w};
+                            uint32_t ql[4] = {0, 0, 0, 0};
+                            if constexpr (TYPE == kBF16) {
+                                const uint2 low = sh.q_low[2 * c + h][lane];
+                                ql[0] = low.x, ql[2] = low.y;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t b0 = h ? k[j].z : k[j].x, b1 = h ? k[j].w : k[j].y;
                                 if constexpr (TYPE == kBF16) {
-                                    mma_bf16(acc, qa, b0, b1);
-                                    const uint2 low = q_low[2 * c + h][lane];
-                                    const uint32_t ql[4] = {low.x, 0u, low.y, 0u};
-                                    mma_bf16(acc, ql, b0, b1);
+                                    mma_bf16(acc[j], qa, b0, b1);
+                                    mma_bf16(acc[j], ql, b0, b1);
                                 } else {
-                                    mma_f16(acc, qa, b0, b1);
+                                    mma_f16(acc[j], qa, b0, b1);
                                 }
                             }
                         }
-                        s[j][0] = acc[0] + acc[2];
-                        s[j][1] = acc[1] + acc[3];
                     }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) s[j][0] = acc[j][0] + acc[j][2], s[j][1] = acc[j][1] + acc[j][3];
                 }
-                const bool more = next < to;
-                // the next tile's K is on its way while this one's probabilities are formed
-                if (more) {
-                    slot = next % a.page_size;
-                    load_k<TYPE, D>(r, a.k_pages + page_next * a.page_stride + head_off, slot, a.page_size, g, t);
-                }
+                const bool full = tok >= first && tok + kAttnTile <= n;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -472,14 +507,14 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::ctas) attn_decode
                         float x = s[j][e] * s_factor;
                         if (capped) x = a.softcap * tanhf(x * inv_cap) * kLog2e;
                         const int tk = tok + 8 * j + 2 * t + e;
-                        s[j][e] = tk >= first && tk < n ? x : -INFINITY;
+                        s[j][e] = full || (tk >= first && tk < n) ? x : -INFINITY;
                     }
                 float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
                 const float m_new = fmaxf(m, mx);
                 const float m_use = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every p is 0
-                const float alpha = exp2f(m - m_use);
+                float alpha = exp2f(m - m_use);
                 m = m_new;
                 float p[4];
 #pragma unroll
@@ -487,39 +522,54 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::ctas) attn_decode
                 l = fmaf(l, alpha, (p[0] + p[1]) + (p[2] + p[3]));
 
                 if constexpr (TYPE == kQ8) {
-                    // the tile's largest V scale to [1/2, 1): 2^shift
+                    alignas(16) __half vs[4][KC];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = 8 * (i >> 1) + 2 * t + (i & 1);
+                        load_scales<KC>(vs[i], vt + S::matrix + S::scales + row * (KC * 2));
+                        if (!full && (tok + row < first || tok + row >= n)) {
+#pragma unroll
+                            for (int c = 0; c < KC; ++c) vs[i][c] = __ushort_as_half(0);
+                        }
+                    }
+                    // the largest scale met: below 2^unit_exp
                     __half2 big = __half2half2(__ushort_as_half(0));
 #pragma unroll
                     for (int i = 0; i < 4; i += 2)
 #pragma unroll
-                        for (int c = 0; c < KC; ++c) big = __hmax2(big, __habs2(__halves2half2(r.vs[i][c], r.vs[i + 1][c])));
+                        for (int c = 0; c < KC; ++c) big = __hmax2(big, __habs2(__halves2half2(vs[i][c], vs[i + 1][c])));
                     float bm = fmaxf(__low2float(big), __high2float(big));
                     bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 1));
                     bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 2));
-                    const int e = (int)(__float_as_uint(bm) >> 23) - 126;  // bm < 2^e
-                    const float up = __uint_as_float((unsigned)(127 + min(max(-e, -30), 30)) << 23);
-                    const float down = __uint_as_float((unsigned)(127 - min(max(-e, -30), 30)) << 23);
+                    const int e = max(unit_exp, min((int)(__float_as_uint(bm) >> 23) - 126, 30));
+                    alpha *= __uint_as_float((unsigned)(127 + unit_exp - e) << 23);
+                    unit_exp = e;
+                    const float up_p = kPScale * __uint_as_float((unsigned)(127 - e) << 23);
                     float ps[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ps[i] = p[i] * (kPScale * up);
+                    for (int i = 0; i < 4; ++i) ps[i] = p[i] * up_p;
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
                         uint32_t pa[4];
-                        split_f16(ps[0] * __half2float(r.vs[0][c]), ps[1] * __half2float(r.vs[1][c]), pa[0], pa[1]);
-                        split_f16(ps[2] * __half2float(r.vs[2][c]), ps[3] * __half2float(r.vs[3][c]), pa[2], pa[3]);
+                        split_f16(ps[0] * __half2float(vs[0][c]), ps[1] * __half2float(vs[1][c]), pa[0], pa[1]);
+                        split_f16(ps[2] * __half2float(vs[2][c]), ps[3] * __half2float(vs[3][c]), pa[2], pa[3]);
+                        uint32_t x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] = 0x80808080u ^ *reinterpret_cast<const uint32_t *>(
+                                                     vt + (8 * (i >> 1) + 2 * t + (i & 1)) * S::pitch +
+                                                     (((2 * c + (g >> 2)) ^ v_key<TYPE>(2 * t)) << 4) + (g & 3) * 4);
                         // bytes of two tokens side by side
-                        const uint32_t x0 = r.v[0][c] ^ 0x80808080u, x1 = r.v[1][c] ^ 0x80808080u;
-                        const uint32_t x2 = r.v[2][c] ^ 0x80808080u, x3 = r.v[3][c] ^ 0x80808080u;
-                        const uint32_t lo[2] = {__byte_perm(x0, x1, 0x5140), __byte_perm(x0, x1, 0x7362)};
-                        const uint32_t hi[2] = {__byte_perm(x2, x3, 0x5140), __byte_perm(x2, x3, 0x7362)};
+                        const uint32_t lo[2] = {__byte_perm(x[0], x[1], 0x5140), __byte_perm(x[0], x[1], 0x7362)};
+                        const uint32_t hi[2] = {__byte_perm(x[2], x[3], 0x5140), __byte_perm(x[2], x[3], 0x7362)};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t sel = (i & 1) ? 0x4342 : 0x4140;
                             float acc[4] = {0.f, 0.f, 0.f, 0.f};
                             mma_f16(acc, pa, codes_f16(lo[i >> 1], sel), codes_f16(hi[i >> 1], sel));
                             const int j = 4 * c + i;
-                            o[j][0] = fmaf(o[j][0], alpha, (acc[0] + acc[2]) * down);
-                            o[j][1] = fmaf(o[j][1], alpha, (acc[1] + acc[3]) * down);
+                            o[j][0] = fmaf(o[j][0], alpha, acc[0] + acc[2]);
+                            o[j][1] = fmaf(o[j][1], alpha, acc[1] + acc[3]);
                         }
                     }
                 } else {
@@ -532,11 +582,13 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::ctas) attn_decode
                         split_f16(p[2] * kPScale, p[3] * kPScale, pa[2], pa[3]);
                     }
 #pragma unroll
-                    for (int c = 0; c < Tile<TYPE, D>::VC; ++c) {
-                        const uint32_t *v0 = reinterpret_cast<const uint32_t *>(&r.v[0][c]);
-                        const uint32_t *v1 = reinterpret_cast<const uint32_t *>(&r.v[1][c]);
-                        const uint32_t *v2 = reinterpret_cast<const uint32_t *>(&r.v[2][c]);
-                        const uint32_t *v3 = reinterpret_cast<const uint32_t *>(&r.v[3][c]);
+                    for (int c = 0; c < VC; ++c) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = *reinterpret_cast<const uint4 *>(vt + (8 * (i >> 1) + 2 * t + (i & 1)) * S::pitch +
+                                                                    ((8 * c + (g ^ v_key<TYPE>(2 * t + (i & 1)))) << 4));
+                        const uint32_t *v0 = reinterpret_cast<const uint32_t *>(&v[0]), *v1 = v0 + 4, *v2 = v0 + 8, *v3 = v0 + 12;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const uint32_t sel = (i & 1) ? 0x7632 : 0x5410;
@@ -555,13 +607,10 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::ctas) attn_decode
                         }
                     }
                 }
-                if (!more) break;
-                load_v<TYPE, D>(r, a.v_pages + page_next * a.page_stride + head_off, slot, a.page_size, g, t, first - next,
-                                n - next);
-                tok = next;
-                next += kRound;
-                if (next < to) page_next = page_at(next);
             }
+            __syncwarp();  // the stage has been read
+            issue(stage);
+            stage = stage + 1 == NS ? 0 : stage + 1;
         }
         l += __shfl_xor_sync(kFull, l, 1);
         l += __shfl_xor_sync(kFull, l, 2);
@@ -571,21 +620,24 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::ctas) attn_decode
         }
 
         // the warps meet
+        const float o_unit = TYPE == kBF16 ? 1.0f : (1.0f / kPScale) * (TYPE == kQ8 ? __uint_as_float((unsigned)(127 + unit_exp) << 23) : 1.0f);
         if (t == 0) sh.x_m[warp][g] = m, sh.x_l[warp][g] = l;
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int d = value_of<TYPE>(j, e, t);
-                if (d < D) sh.x_o[warp][g][d] = o[j][e];
+                if (d < D) sh.x_o[warp][g][d] = o[j][e] * o_unit;
             }
-        __syncthreads();
-        const float o_scale = TYPE == kBF16 ? 1.0f : 1.0f / kPScale;
         // a cut unit: CTAs cta0 .. cta0 + pieces - 1 have a part of it; every CTA has room for the
         // part of a unit that began before its share (0) and of one that goes on behind it (1)
-        const int cta0 = whole ? 0 : (int)(unit_at / share);
-        const int pieces = whole ? 1 : (int)((unit_at + rounds - 1) / share) - cta0 + 1;
+        const int unit_at = at.pos - at.round;
+        const int cta0 = whole ? 0 : unit_at / share;
+        const int pieces = whole ? 1 : (unit_at + at.rounds - 1) / share - cta0 + 1;
+        const int row = at.row;
         auto part_of = [&](int p) { return a.ws_part + (size_t)(2 * (cta0 + p) + (p == 0 ? 1 : 0)) * part; };
+        __syncthreads();
+        // what each warp's sums are multiplied by
         float *const mine = whole ? nullptr : part_of((int)blockIdx.x - cta0);
 
         float4 done[kPer];
@@ -612,12 +664,13 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::ctas) attn_decode
                 __stcg(reinterpret_cast<float4 *>(mine + 2 * kAttnHeads) + idx, v);
                 if (d == 0) __stcg(mine + h, M), __stcg(mine + kAttnHeads + h, L);
             } else {
-                const float inv = L == 0.0f ? 0.0f : o_scale / L;
+                const float inv = L == 0.0f ? 0.0f : 1.0f / L;
                 done[i] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
             }
         }
-        __syncthreads();  // the exchange may be used again; the parts are written
+        bool joined = whole;
         if (!whole) {
+            __syncthreads();  // the parts are written; the exchange has been read
             if (tid == 0) {
                 __threadfence();  // all of this CTA's part, before it is counted
                 const unsigned arrived = atomicAdd(a.ws_cnt + cta0, 1u);
@@ -626,7 +679,9 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::ctas) attn_decode
                 __threadfence();  // and the others' parts after the count
             }
             __syncthreads();
-            if (!sh.last) continue;
+            joined = sh.last;
+        }
+        if (!whole && joined) {
             // weights of the pieces: a warp a head
             for (int i = tid; i < pieces * kAttnHeads; i += kThreads)
                 sh.weight[i / kAttnHeads][i % kAttnHeads] = __ldcg(part_of(i / kAttnHeads) + i % kAttnHeads);
@@ -661,24 +716,28 @@ __global__ void __launch_bounds__(Shape<D>::threads, Shape<D>::ctas) attn_decode
                     v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
                 }
                 const float L = sh.total[h];
-                const float inv = L == 0.0f ? 0.0f : o_scale / L;
+                const float inv = L == 0.0f ? 0.0f : 1.0f / L;
                 done[i] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
             }
-            __syncthreads();  // the weights have been read
         }
-        // rows of out, and their q8 blocks (8 lanes each; every lane joins the shuffles)
+        if (joined) {
+            // rows of out, and their q8 blocks (8 lanes each; every lane joins the shuffles)
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int idx = tid + i * kThreads;
-            const int h = idx / (D / 4);
-            const bool valid = idx < kSlots && h < heads;
-            const float4 v = valid ? done[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-            if (valid)
-                *reinterpret_cast<float4 *>(a.out + row * a.out_stride + (size_t)head0 * D + (size_t)idx * 4) = v;
-            if (a.q8)
-                quantize4(v, valid, (long long)head0 * (D / 4) + idx, a.q8 + (size_t)row * a.q8_stride, a.q8_d_off,
-                          a.q8_sum_off);
+            for (int i = 0; i < kPer; ++i) {
+                const int idx = tid + i * kThreads;
+                const int h = idx / (D / 4);
+                const bool valid = idx < kSlots && h < heads;
+                const float4 v = valid ? done[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (valid)
+                    *reinterpret_cast<float4 *>(a.out + row * a.out_stride + (size_t)head0 * D + (size_t)idx * 4) = v;
+                if (a.q8)
+                    quantize4(v, valid, (long long)head0 * (D / 4) + idx, a.q8 + (size_t)row * a.q8_stride, a.q8_d_off,
+                              a.q8_sum_off);
+            }
         }
+        leave(at);
+        if (!enter(at)) break;
+        // the barrier at the next unit's start keeps the exchange until every thread has read it
     }
 }
 
@@ -690,7 +749,7 @@ cudaError_t launch_dim(const AttnLaunch &a, int pdl, cudaStream_t st)
     static std::atomic<bool> opted[kMaxDevices];
     const auto kernel = attn_decode_kernel<TYPE, D>;
     constexpr size_t smem = sizeof(Smem<TYPE, D>);
-    static_assert(smem * Shape<D>::ctas <= 220 * 1024, "the CTAs of an SM share 228 KB, 1 KB of each reserved");
+    static_assert(smem <= 227 * 1024, "what a CTA may have");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -699,7 +758,7 @@ cudaError_t launch_dim(const AttnLaunch &a, int pdl, cudaStream_t st)
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDevices) opted[dev].store(true, std::memory_order_release);
     }
-    return launch_maybe_pdl(kernel, dim3((unsigned)a.ctas), dim3(Shape<D>::threads), smem, pdl, st, a);
+    return launch_maybe_pdl(kernel, dim3((unsigned)a.ctas), dim3(Shape<TYPE, D>::threads), smem, pdl, st, a);
 }
 
 template <int TYPE>

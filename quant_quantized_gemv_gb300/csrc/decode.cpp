@@ -42,40 +42,30 @@ int kv_check(const mq_kv_cache *kv, size_t *page_stride, size_t *head_bytes)
 // heads of one kv head) of up to `span` tokens each: one resident wave, or fewer
 // when there are fewer rounds of tokens than that.  Beyond kAttnMaxRows rows: a
 // CTA per unit.
-int attn_wave(int sms, int head_dim)
-{
-    const int n = sms * attn_ctas(head_dim);
-    return n < kAttnMaxCtas ? n : kAttnMaxCtas;
-}
+int attn_wave(int sms) { return sms < kAttnMaxCtas ? sms : kAttnMaxCtas; }
 
-long long attn_rounds(long long span, int head_dim)
+long long attn_rounds(long long span, int type, int head_dim)
 {
-    const int round = attn_warps(head_dim) * kAttnTile;
+    const int round = attn_warps(type, head_dim) * kAttnTile;
     return (span + round - 1) / round;
 }
 
-long long attn_grid(long long units, long long span, int nt, int sms, int head_dim)
+long long attn_grid(long long units, long long rounds, int nt, int sms)
 {
     if (nt > kAttnMaxRows) return units;
-    const long long rounds = units * attn_rounds(span, head_dim);
-    const long long wave = attn_wave(sms, head_dim);
-    return rounds < wave ? rounds : wave;
+    return units * rounds < attn_wave(sms) ? units * rounds : attn_wave(sms);
 }
 
 // Workspace of a call: a counter and two partial results for each CTA that
 // shares out the work, in places that no call changes (a workspace may serve
 // calls of different sizes, and every counter must be zero before each).  None
 // for rows so short that no unit is cut.
-size_t attn_count_bytes(int sms, int head_dim)
-{
-    return ((size_t)attn_wave(sms, head_dim) * 4 + 15) & ~(size_t)15;
-}
+size_t attn_count_bytes(int sms) { return ((size_t)attn_wave(sms) * 4 + 15) & ~(size_t)15; }
 
-size_t attn_ws_bytes(int max_len, int sms, int head_dim)
+size_t attn_ws_bytes(const mq_kv_cache *kv, int max_len, int sms)
 {
-    if (attn_rounds((long long)max_len + kAttnTile - 1, head_dim) <= kAttnWhole) return 0;
-    return attn_count_bytes(sms, head_dim) +
-           (size_t)attn_wave(sms, head_dim) * 2 * attn_part_floats(head_dim) * 4;
+    if (attn_rounds((long long)max_len + kAttnTile - 1, kv->type, kv->head_dim) <= kAttnWhole) return 0;
+    return attn_count_bytes(sms) + (size_t)attn_wave(sms) * 2 * attn_part_floats(kv->head_dim) * 4;
 }
 
 bool attn_shape_ok(const mq_kv_cache *kv, int n_heads, int nt, int max_len)
@@ -83,10 +73,10 @@ bool attn_shape_ok(const mq_kv_cache *kv, int n_heads, int nt, int max_len)
     if (mq_kv_page_bytes(kv->type, kv->n_kv_heads, kv->page_size, kv->head_dim) == 0) return false;
     if (nt < 1 || n_heads < 1 || n_heads % kv->n_kv_heads != 0 || max_len < 1) return false;
     if (max_len > 0x7fffffff - 4096) return false;
-    // the grid and the rounds of a row and of all rows; a q8 plane's values
-    const long long rounds = attn_rounds((long long)max_len + kAttnTile - 1, kv->head_dim);
+    // the grid, a q8 plane's values and the rounds of all rows
+    const long long rounds = attn_rounds((long long)max_len + kAttnTile - 1, kv->type, kv->head_dim);
     return (long long)nt * n_heads < (1LL << 24) && (long long)n_heads * kv->head_dim < (1LL << 30) &&
-           n_heads * rounds < (1LL << 31) && nt * rounds < (1LL << 31);
+           (long long)nt * n_heads * rounds < (1LL << 31);
 }
 
 long long attn_units(const mq_kv_cache *kv, int n_heads, int nt)
@@ -173,7 +163,7 @@ size_t mq_attn_workspace_bytes(const mq_kv_cache *kv, int n_heads, int nt, int m
     if (!kv || !attn_shape_ok(kv, n_heads, nt, max_len)) return 0;
     const int sms = mq_device_sms();
     if (sms <= 0) return 0;
-    return nt > kAttnMaxRows ? 0 : attn_ws_bytes(max_len, sms, kv->head_dim);
+    return nt > kAttnMaxRows ? 0 : attn_ws_bytes(kv, max_len, sms);
 }
 
 int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *a, void *stream)
@@ -202,13 +192,14 @@ int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *a, void *stream)
     // a window starts inside a tile of its own
     long long span = a->max_len;
     if (a->window > 0 && (long long)a->window + kAttnTile - 1 < span) span = (long long)a->window + kAttnTile - 1;
-    r.ctas = (int)attn_grid(units, span, a->nt, sms, D);
-    if (a->nt <= kAttnMaxRows && attn_rounds(span, D) > kAttnWhole) {
+    const long long rounds = attn_rounds(span, kv->type, D);
+    r.ctas = (int)attn_grid(units, rounds, a->nt, sms);
+    if (a->nt <= kAttnMaxRows && rounds > kAttnWhole) {
         if (!a->ws) return MQ_ERR_NULL;
-        if (a->ws_bytes < attn_count_bytes(sms, D) + (size_t)r.ctas * 2 * attn_part_floats(D) * 4)
+        if (a->ws_bytes < attn_count_bytes(sms) + (size_t)r.ctas * 2 * attn_part_floats(D) * 4)
             return MQ_ERR_WORKSPACE;
         r.ws_cnt = (unsigned *)a->ws;
-        r.ws_part = (float *)((uint8_t *)a->ws + attn_count_bytes(sms, D));
+        r.ws_part = (float *)((uint8_t *)a->ws + attn_count_bytes(sms));
     }
     r.q = a->q, r.out = a->out, r.q_stride = a->q_stride, r.out_stride = a->out_stride;
     r.q8 = (uint8_t *)a->q8;

@@ -224,11 +224,15 @@ cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_
 constexpr int kAttnHeads = 8;        // query heads of a CTA (rows of its matrix products)
 constexpr int kAttnTile = 16;        // tokens a warp takes at a time
 constexpr int kAttnMaxRows = 1024;
-constexpr int kAttnMaxCtas = 512;    // CTAs that share out the work
+constexpr int kAttnMaxCtas = 256;    // CTAs that share out the work
 constexpr int kAttnWhole = 2;        // units of so many rounds or less are not cut
-// Warps of a CTA and CTAs of an SM for a head size (what a tile's registers allow).
-__host__ __device__ constexpr int attn_warps(int head_dim) { return head_dim <= 128 ? 12 : 8; }
-__host__ __device__ constexpr int attn_ctas(int head_dim) { return 1; }
+// Warps of a CTA (one CTA an SM) and stages of a warp, by cache type (MQ_KV_*) and head size: what
+// fits 227 KB, a stage being 16 tokens' K and V.
+__host__ __device__ constexpr int attn_warps(int type, int head_dim)
+{
+    return type == 3 ? (head_dim <= 128 ? 12 : 6) : head_dim == 64 ? 12 : head_dim <= 128 ? 8 : 4;
+}
+__host__ __device__ constexpr int attn_stages(int type, int head_dim) { return head_dim == 64 ? 3 : 2; }
 constexpr int attn_part_floats(int head_dim) { return kAttnHeads * (head_dim + 2); }
 
 struct AttnLaunch {
