@@ -141,6 +141,7 @@ template <int TYPE, int D>
 struct Shape {
     static constexpr int warps = attn_warps(TYPE, D), threads = warps * 32, round = warps * kAttnTile;
     static constexpr int stages = attn_stages(TYPE, D);
+    static constexpr int meet = attn_meet_heads(TYPE, D);            // heads the warps exchange at a time
     static constexpr int KC = D / 32;
     static constexpr int row = TYPE == kQ8 ? D : 2 * D;              // bytes of a token's K or V
     static constexpr int pitch = row < 128 ? 128 : row == 192 ? 256 : row;  // the same in a stage: room for the permutation
@@ -172,8 +173,10 @@ struct Smem {
     uint4 q_frag[2 * S::KC][32];                           // q's parts as the products take them
     uint2 q_low[TYPE == kBF16 ? 2 * S::KC : 1][32];        // bf16's third part
     union {
-        float x_o[S::warps][kAttnHeads][D + 4];            // the warps' exchange
-        float weight[kAttnMaxCtas][kAttnHeads];            // the join
+        float x_o[S::warps][S::meet][D + 4];               // the warps' exchange
+        struct {
+            float weight[kAttnMaxCtas][kAttnHeads], mass[kAttnMaxCtas][kAttnHeads];  // the join
+        };
     };
     float x_m[S::warps][kAttnHeads], x_l[S::warps][kAttnHeads];
     float total[kAttnHeads];
@@ -184,7 +187,7 @@ struct Smem {
 
 // A place in the line of rounds: a unit, or the part of it that falls to this CTA.
 struct Segment {
-    int pos;                 // of its first round
+    int pos;                 // of its first round in the line
     int row, unit;           // unit of the row
     int rounds, round, take; // of the unit; the first one here; how many here
 };
@@ -197,7 +200,6 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
     constexpr int NJ = TYPE == kQ8 ? D / 8 : VC * 8;             // accumulator pairs a lane
     constexpr int kWarps = S::warps, kThreads = S::threads, kRound = S::round;
     constexpr int kSlots = kAttnHeads * D / 4;                   // float4s of a unit's output
-    constexpr int kPer = (kSlots + kThreads - 1) / kThreads;
     constexpr size_t part = kAttnHeads * (D + 2);                // attn_part_floats(D)
     extern __shared__ __align__(128) unsigned char raw[];
     Smem<TYPE, D> &sh = *reinterpret_cast<Smem<TYPE, D> *>(raw);
@@ -206,23 +208,49 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     griddep_wait();  // queries, lengths, tables and the cache may come from the preceding kernels
 
-    // first cached token and rounds of a row of n tokens (n < 0: padding, none; nothing to read: one)
+    // The page tables and queries to L2 while the lengths are fetched: they lie on the way to the first
+    // tile, one behind the other, and a long context's stream leaves nothing of them there.
+    {
+        const unsigned i = blockIdx.x * kThreads + tid;  // 128 bytes a thread
+        if ((size_t)i * 32 < (size_t)a.n_seqs * a.pages_stride)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.pages + (size_t)i * 32));
+        const unsigned lines = a.n_heads * (D / 32), r = i / lines;
+        if (r < (unsigned)a.nt)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + r * a.q_stride + (size_t)(i - r * lines) * 32));
+    }
+    // first cached token and rounds of a row of n tokens (n < 0: padding, none; nothing to read: one).
+    // In the line a unit has kAttnUnitCost rounds more, in front: what its beginning and end cost.
     auto first_of = [&](int n) { return a.window > 0 ? max(0, n - a.window) : 0; };
     auto start_of = [&](int n) { return first_of(n) & ~(kAttnTile - 1); };
     auto too_long = [&](int n) { return n > a.max_len || (long long)n > (long long)a.pages_stride * a.page_size; };
     auto rounds_of = [&](int n) { return n < 0 ? 0 : n == 0 || too_long(n) ? 1 : (n - start_of(n) + kRound - 1) / kRound; };
+
+    auto line_of = [&](int n) { return n < 0 ? 0 : rounds_of(n) + kAttnUnitCost; };
 
     const int units = a.n_kv_heads * a.subgroups;  // of a row
     const bool shared_out = a.nt <= kAttnMaxRows;  // else a CTA per unit
     int end, share = 0, single_n = 0;
     Segment load_at;
     if (shared_out) {
-        // rounds of the rows before each row
+        // rounds of the rows before each row: up to 32 rows by every warp for itself
         int before = 0;
-        for (int r0 = 0; r0 < a.nt; r0 += kThreads) {
+        if (a.nt <= 32) {
+            const int n = lane < a.nt ? __ldcg(a.lens + lane) : -1;
+            const int mine = line_of(n);
+            int s = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(kFull, s, o);
+                if (lane >= o) s += v;
+            }
+            before = __shfl_sync(kFull, s, 31);
+            sh.rounds[lane] = s - mine;  // every warp writes the same
+            if (lane < a.nt) sh.lens[lane] = n;
+            __syncwarp();
+        } else for (int r0 = 0; r0 < a.nt; r0 += kThreads) {
             const int r = r0 + tid;
             const int n = r < a.nt ? __ldcg(a.lens + r) : -1;
-            const int mine = rounds_of(n);
+            const int mine = line_of(n);
             int s = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -241,8 +269,13 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
             before += all;
             if (r0 + kThreads < a.nt) __syncthreads();
         }
-        if (tid == 0) sh.rounds[a.nt] = before;
-        __syncthreads();
+        if (a.nt > 32) {
+            if (tid == 0) sh.rounds[a.nt] = before;
+            __syncthreads();
+        } else if (lane == 0) {
+            sh.rounds[a.nt] = before;
+        }
+        __syncwarp();
         const int all = before * units;
         share = max((int)((all + gridDim.x - 1) / gridDim.x), 1);
         load_at.pos = blockIdx.x * share;
@@ -264,19 +297,30 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
         load_at.unit = blockIdx.x - load_at.row * units;
         load_at.pos = load_at.round = 0;
         single_n = __ldcg(a.lens + load_at.row);
-        end = rounds_of(single_n);
+        end = line_of(single_n);
     }
     auto n_of = [&](int row) { return shared_out ? sh.lens[row] : single_n; };
-    // completes a segment that begins where its fields say; false: none is left
+    // completes a segment that begins where its fields say (its round counted with the unit's cost; from
+    // then on without); false: none is left
     auto enter = [&](Segment &s) {
         for (;;) {
             if (s.pos >= end) return false;
             s.rounds = shared_out ? sh.rounds[s.row + 1] - sh.rounds[s.row] : end;
             s.take = min(s.rounds - s.round, end - s.pos);
-            if (s.rounds > kAttnWhole) return true;
+            if (s.rounds > kAttnWhole + kAttnUnitCost) {
+                if (s.round + s.take <= kAttnUnitCost) return false;  // nothing but the cost: the next CTA begins it
+                // to the tokens' rounds
+                const int cost = max(kAttnUnitCost - s.round, 0);
+                s.pos += cost, s.round += cost, s.take -= cost;
+                s.round -= kAttnUnitCost, s.rounds -= kAttnUnitCost;
+                return true;
+            }
             // not cut: it belongs to the share in which it begins
-            s.take = s.rounds;
-            if (s.round == 0) return true;
+            if (s.round == 0) {
+                s.pos += kAttnUnitCost;
+                s.take = s.rounds -= kAttnUnitCost;
+                return true;
+            }
             s.take = s.rounds - s.round;
             s.pos += s.take, s.round = 0;
             if (++s.unit == units) {
@@ -301,7 +345,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
     if (!load_live) return;
     Segment at = load_at;  // the working side
     int load_round = 0, load_count = 0;              // round of the segment; segments begun
-    int l_first = 0, l_n = 0, l_from = 0, l_to = 0, l_page = -1;
+    int l_first = 0, l_n = 0, l_from = 0, l_to = 0, l_pages = -1;  // l_pages: a lane a round, 32 at a time
     const int *l_table = nullptr;
     size_t l_head = 0;
     auto open_load = [&]() {
@@ -314,11 +358,12 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
         l_table = a.pages + (bad ? 0 : (size_t)seq * a.pages_stride);
         l_head = (size_t)(load_at.unit / a.subgroups) * a.head_bytes;
     };
-    auto ask_page = [&]() {
-        if (l_from < l_to) l_page = __ldcg(l_table + l_from / a.page_size);
+    auto ask_pages = [&]() {
+        const int tok = l_from + lane * kRound;
+        if (tok < l_to) l_pages = __ldcg(l_table + tok / a.page_size);
     };
     open_load();
-    ask_page();
+    ask_pages();
     unsigned missing = 0;  // stages whose page is not there
     auto issue = [&](int stage) {
         if (load_live) {
@@ -330,6 +375,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                 for (int i = tid; i < kSlots; i += kThreads)
                     copy16(dst + i * 16, i < heads * (D / 4) ? src + i * 4 : src, i < heads * (D / 4) ? 16 : 0);
             }
+            const int l_page = __shfl_sync(kFull, l_pages, load_round & 31);
             if (l_from < l_to) {
                 const bool there = (unsigned)l_page < (unsigned)a.n_pages;
                 missing = there ? missing & ~(1u << stage) : missing | 1u << stage;
@@ -365,9 +411,13 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                 leave(load_at);
                 load_live = enter(load_at);
                 load_round = 0, ++load_count;
-                if (load_live) open_load();
+                if (load_live) {
+                    open_load();
+                    ask_pages();
+                }
+            } else if ((load_round & 31) == 0) {
+                ask_pages();
             }
-            if (load_live) ask_page();
         }
         copies_commit();
     };
@@ -468,6 +518,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                     }
                 } else {
                     float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                    float low_acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
                         uint4 k[2];
@@ -489,7 +540,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                                 const uint32_t b0 = h ? k[j].z : k[j].x, b1 = h ? k[j].w : k[j].y;
                                 if constexpr (TYPE == kBF16) {
                                     mma_bf16(acc[j], qa, b0, b1);
-                                    mma_bf16(acc[j], ql, b0, b1);
+                                    mma_bf16(low_acc[j], ql, b0, b1);
                                 } else {
                                     mma_f16(acc[j], qa, b0, b1);
                                 }
@@ -497,7 +548,10 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                         }
                     }
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) s[j][0] = acc[j][0] + acc[j][2], s[j][1] = acc[j][1] + acc[j][3];
+                    for (int j = 0; j < 2; ++j) {
+                        s[j][0] = acc[j][0] + (acc[j][2] + low_acc[j][0]);
+                        s[j][1] = acc[j][1] + (acc[j][3] + low_acc[j][1]);
+                    }
                 }
                 const bool full = tok >= first && tok + kAttnTile <= n;
 #pragma unroll
@@ -619,56 +673,70 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
             if (a.status && lane == 0) atomicOr(a.status, 1);
         }
 
-        // the warps meet
+        // the warps meet, S::meet heads at a time
         const float o_unit = TYPE == kBF16 ? 1.0f : (1.0f / kPScale) * (TYPE == kQ8 ? __uint_as_float((unsigned)(127 + unit_exp) << 23) : 1.0f);
         if (t == 0) sh.x_m[warp][g] = m, sh.x_l[warp][g] = l;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int d = value_of<TYPE>(j, e, t);
-                if (d < D) sh.x_o[warp][g][d] = o[j][e] * o_unit;
-            }
         // a cut unit: CTAs cta0 .. cta0 + pieces - 1 have a part of it; every CTA has room for the
         // part of a unit that began before its share (0) and of one that goes on behind it (1)
-        const int unit_at = at.pos - at.round;
+        const int unit_at = at.pos - at.round;  // of the unit's first tokens
         const int cta0 = whole ? 0 : unit_at / share;
         const int pieces = whole ? 1 : (unit_at + at.rounds - 1) / share - cta0 + 1;
         const int row = at.row;
         auto part_of = [&](int p) { return a.ws_part + (size_t)(2 * (cta0 + p) + (p == 0 ? 1 : 0)) * part; };
-        __syncthreads();
-        // what each warp's sums are multiplied by
         float *const mine = whole ? nullptr : part_of((int)blockIdx.x - cta0);
-
-        float4 done[kPer];
+        // four values of out, and their share of a q8 block (8 lanes; every lane joins the shuffles)
+        auto emit = [&](int idx, bool in_range, float4 v) {
+            const bool valid = in_range && idx / (D / 4) < heads;
+            if (valid)
+                *reinterpret_cast<float4 *>(a.out + row * a.out_stride + (size_t)head0 * D + (size_t)idx * 4) = v;
+            if (a.q8)
+                quantize4(valid ? v : make_float4(0.f, 0.f, 0.f, 0.f), valid, (long long)head0 * (D / 4) + idx,
+                          a.q8 + (size_t)row * a.q8_stride, a.q8_d_off, a.q8_sum_off);
+        };
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int idx = tid + i * kThreads;
-            if (idx >= kSlots) continue;
-            const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
-            float M = sh.x_m[0][h];
+        for (int h0 = 0; h0 < kAttnHeads; h0 += S::meet) {
+            if (h0 > 0) __syncthreads();  // the heads before have been read
+            if (g >= h0 && g < h0 + S::meet) {
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sh.x_m[w][h]);
-            const float M_use = M == -INFINITY ? 0.0f : M;
-            float L = 0.0f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2f(sh.x_m[w][h] - M_use);
-                const float4 u = *reinterpret_cast<const float4 *>(&sh.x_o[w][h][d]);
-                L = fmaf(sh.x_l[w][h], f, L);
-                v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y);
-                v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
+                    for (int e = 0; e < 2; ++e) {
+                        const int d = value_of<TYPE>(j, e, t);
+                        if (d < D) sh.x_o[warp][g - h0][d] = o[j][e] * o_unit;
+                    }
             }
-            if (!whole) {
-                __stcg(reinterpret_cast<float4 *>(mine + 2 * kAttnHeads) + idx, v);
-                if (d == 0) __stcg(mine + h, M), __stcg(mine + kAttnHeads + h, L);
-            } else {
-                const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-                done[i] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            __syncthreads();
+            constexpr int kMeet = S::meet * D / 4;  // float4s of these heads
+#pragma unroll 1
+            for (int i0 = 0; i0 < kMeet; i0 += kThreads) {
+                const int i = i0 + tid, hh = i / (D / 4), d = (i - hh * (D / 4)) * 4, h = h0 + hh;
+                const bool in_range = i < kMeet;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (in_range) {
+                    float M = sh.x_m[0][h];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sh.x_m[w][h]);
+                    const float M_use = M == -INFINITY ? 0.0f : M;
+                    float L = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float f = exp2f(sh.x_m[w][h] - M_use);
+                        const float4 u = *reinterpret_cast<const float4 *>(&sh.x_o[w][hh][d]);
+                        L = fmaf(sh.x_l[w][h], f, L);
+                        v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y);
+                        v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
+                    }
+                    if (!whole) {
+                        __stcg(reinterpret_cast<float4 *>(mine + 2 * kAttnHeads) + h0 * (D / 4) + i, v);
+                        if (d == 0) __stcg(mine + h, M), __stcg(mine + kAttnHeads + h, L);
+                    } else {
+                        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                        v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    }
+                }
+                if (whole) emit(h0 * (D / 4) + i, in_range, v);
             }
         }
-        bool joined = whole;
         if (!whole) {
             __syncthreads();  // the parts are written; the exchange has been read
             if (tid == 0) {
@@ -679,60 +747,58 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                 __threadfence();  // and the others' parts after the count
             }
             __syncthreads();
-            joined = sh.last;
-        }
-        if (!whole && joined) {
-            // weights of the pieces: a warp a head
-            for (int i = tid; i < pieces * kAttnHeads; i += kThreads)
-                sh.weight[i / kAttnHeads][i % kAttnHeads] = __ldcg(part_of(i / kAttnHeads) + i % kAttnHeads);
-            __syncthreads();
-            for (int h = warp; h < kAttnHeads; h += kWarps) {
-                float M = -INFINITY, L = 0.0f;
-                for (int p = lane; p < pieces; p += 32) M = fmaxf(M, sh.weight[p][h]);
+            if (sh.last) {
+                // the pieces' values are asked for before their weights are known: kAhead at a time
+                constexpr int kAhead = 8;
+                float4 u[kAhead];
+                auto ask = [&](int idx, int p0) {
 #pragma unroll
-                for (int o2 = 16; o2 > 0; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o2));
-                const float M_use = M == -INFINITY ? 0.0f : M;
-                for (int p = lane; p < pieces; p += 32) {
-                    const float f = exp2f(sh.weight[p][h] - M_use);
-                    L = fmaf(__ldcg(part_of(p) + kAttnHeads + h), f, L);
-                    sh.weight[p][h] = f;
+                    for (int k = 0; k < kAhead; ++k) {
+                        u[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (idx < kSlots && p0 + k < pieces)
+                            u[k] = __ldcg(reinterpret_cast<const float4 *>(part_of(p0 + k) + 2 * kAttnHeads) + idx);
+                    }
+                };
+                ask(tid, 0);
+                // weights of the pieces: a warp a head
+                for (int h = warp; h < kAttnHeads; h += kWarps) {
+                    float M = -INFINITY, L = 0.0f;
+                    for (int p = lane; p < pieces; p += 32) {
+                        sh.weight[p][h] = __ldcg(part_of(p) + h);
+                        sh.mass[p][h] = __ldcg(part_of(p) + kAttnHeads + h);
+                        M = fmaxf(M, sh.weight[p][h]);
+                    }
+#pragma unroll
+                    for (int o2 = 16; o2 > 0; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o2));
+                    const float M_use = M == -INFINITY ? 0.0f : M;
+                    for (int p = lane; p < pieces; p += 32) {
+                        const float f = exp2f(sh.weight[p][h] - M_use);
+                        L = fmaf(sh.mass[p][h], f, L);
+                        sh.weight[p][h] = f;
+                    }
+#pragma unroll
+                    for (int o2 = 16; o2 > 0; o2 >>= 1) L += __shfl_xor_sync(kFull, L, o2);
+                    if (lane == 0) sh.total[h] = L;
                 }
+                __syncthreads();
+#pragma unroll 1
+                for (int i0 = 0; i0 < kSlots; i0 += kThreads) {
+                    const int idx = i0 + tid, h = min(idx / (D / 4), kAttnHeads - 1);
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int p0 = 0; p0 < pieces; p0 += kAhead) {
+                        if (i0 + p0 > 0) ask(idx, p0);
 #pragma unroll
-                for (int o2 = 16; o2 > 0; o2 >>= 1) L += __shfl_xor_sync(kFull, L, o2);
-                if (lane == 0) sh.total[h] = L;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int idx = tid + i * kThreads;
-                if (idx >= kSlots) continue;
-                const int h = idx / (D / 4);
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                for (int p = 0; p < pieces; ++p) {
-                    const float4 u = __ldcg(reinterpret_cast<const float4 *>(part_of(p) + 2 * kAttnHeads) + idx);
-                    const float f = sh.weight[p][h];
-                    v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y);
-                    v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
+                        for (int k = 0; k < kAhead; ++k) {
+                            if (p0 + k >= pieces) break;
+                            const float f = sh.weight[p0 + k][h];
+                            v.x = fmaf(u[k].x, f, v.x), v.y = fmaf(u[k].y, f, v.y);
+                            v.z = fmaf(u[k].z, f, v.z), v.w = fmaf(u[k].w, f, v.w);
+                        }
+                    }
+                    const float L = sh.total[h];
+                    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                    emit(idx, idx < kSlots, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                 }
-                const float L = sh.total[h];
-                const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-                done[i] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            }
-        }
-        if (joined) {
-            // rows of out, and their q8 blocks (8 lanes each; every lane joins the shuffles)
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int idx = tid + i * kThreads;
-                const int h = idx / (D / 4);
-                const bool valid = idx < kSlots && h < heads;
-                const float4 v = valid ? done[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-                if (valid)
-                    *reinterpret_cast<float4 *>(a.out + row * a.out_stride + (size_t)head0 * D + (size_t)idx * 4) = v;
-                if (a.q8)
-                    quantize4(v, valid, (long long)head0 * (D / 4) + idx, a.q8 + (size_t)row * a.q8_stride, a.q8_d_off,
-                              a.q8_sum_off);
             }
         }
         leave(at);

@@ -76,7 +76,7 @@ bool attn_shape_ok(const mq_kv_cache *kv, int n_heads, int nt, int max_len)
     // the grid, a q8 plane's values and the rounds of all rows
     const long long rounds = attn_rounds((long long)max_len + kAttnTile - 1, kv->type, kv->head_dim);
     return (long long)nt * n_heads < (1LL << 24) && (long long)n_heads * kv->head_dim < (1LL << 30) &&
-           (long long)nt * n_heads * rounds < (1LL << 31);
+           (long long)nt * n_heads * (rounds + kAttnUnitCost) < (1LL << 31);
 }
 
 long long attn_units(const mq_kv_cache *kv, int n_heads, int nt)

@@ -226,6 +226,7 @@ constexpr int kAttnTile = 16;        // tokens a warp takes at a time
 constexpr int kAttnMaxRows = 1024;
 constexpr int kAttnMaxCtas = 256;    // CTAs that share out the work
 constexpr int kAttnWhole = 2;        // units of so many rounds or less are not cut
+constexpr int kAttnUnitCost = 2;     // rounds that the beginning and end of a unit are worth
 // Warps of a CTA (one CTA an SM) and stages of a warp, by cache type (MQ_KV_*) and head size: what
 // fits 227 KB, a stage being 16 tokens' K and V.
 __host__ __device__ constexpr int attn_warps(int type, int head_dim)
@@ -233,6 +234,8 @@ __host__ __device__ constexpr int attn_warps(int type, int head_dim)
     return type == 3 ? (head_dim <= 128 ? 12 : 6) : head_dim == 64 ? 12 : head_dim <= 128 ? 8 : 4;
 }
 __host__ __device__ constexpr int attn_stages(int type, int head_dim) { return head_dim == 64 ? 3 : 2; }
+// Heads that a CTA's warps exchange at a time at the end of a unit (shared memory again).
+__host__ __device__ constexpr int attn_meet_heads(int type, int head_dim) { return 8; }
 constexpr int attn_part_floats(int head_dim) { return kAttnHeads * (head_dim + 2); }
 
 struct AttnLaunch {
