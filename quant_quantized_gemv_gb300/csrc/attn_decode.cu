@@ -54,6 +54,7 @@
 
 #include <atomic>
 
+#include "f32x2.cuh"
 #include "kernels.h"
 #include "q8_block.cuh"
 
@@ -82,6 +83,14 @@ __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<u
 __device__ __forceinline__ uint32_t bits(__nv_bfloat162 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ __half2 half2_of(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
 
+// 2^x, to 2 ulp; below 2^-126 it is 0.
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // x, y as fp16 parts: hi rounds the value, lo the rest.
 __device__ __forceinline__ void split_f16(float x, float y, uint32_t &hi, uint32_t &lo)
 {
@@ -89,6 +98,17 @@ __device__ __forceinline__ void split_f16(float x, float y, uint32_t &hi, uint32
     const float2 f = __half22float2(h);
     hi = bits(h);
     lo = bits(__floats2half2_rn(x - f.x, y - f.y));
+}
+
+__device__ __forceinline__ void split_f16(Two x, uint32_t &hi, uint32_t &lo)
+{
+    float a, b;
+    split(x, a, b);
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    split(fma2(two(f.x, f.y), two(-1.0f, -1.0f), x), a, b);
+    hi = bits(h);
+    lo = bits(__floats2half2_rn(a, b));
 }
 
 // x, y as three bf16 parts.
@@ -345,7 +365,8 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
     if (!load_live) return;
     Segment at = load_at;  // the working side
     int load_round = 0, load_count = 0;              // round of the segment; segments begun
-    int l_first = 0, l_n = 0, l_from = 0, l_to = 0, l_pages = -1;  // l_pages: a lane a round, 32 at a time
+    int l_first = 0, l_n = 0, l_from = 0, l_to = 0;
+    int l_pages = -1, l_slots = 0;                   // pages and places in them: a lane a round, 32 at a time
     const int *l_table = nullptr;
     size_t l_head = 0;
     auto open_load = [&]() {
@@ -360,7 +381,11 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
     };
     auto ask_pages = [&]() {
         const int tok = l_from + lane * kRound;
-        if (tok < l_to) l_pages = __ldcg(l_table + tok / a.page_size);
+        if (tok < l_to) {
+            const int i = tok / a.page_size;
+            l_slots = tok - i * a.page_size;
+            l_pages = __ldcg(l_table + i);
+        }
     };
     open_load();
     ask_pages();
@@ -376,26 +401,34 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                     copy16(dst + i * 16, i < heads * (D / 4) ? src + i * 4 : src, i < heads * (D / 4) ? 16 : 0);
             }
             const int l_page = __shfl_sync(kFull, l_pages, load_round & 31);
+            const int slot = __shfl_sync(kFull, l_slots, load_round & 31);
             if (l_from < l_to) {
                 const bool there = (unsigned)l_page < (unsigned)a.n_pages;
                 missing = there ? missing & ~(1u << stage) : missing | 1u << stage;
                 const size_t page = (size_t)(there ? l_page : 0) * a.page_stride + l_head;
-                const int slot = l_from % a.page_size;
                 const uint8_t *k = a.k_pages + page + (size_t)slot * S::row, *v = a.v_pages + page + (size_t)slot * S::row;
                 const uint32_t to = shared_address(sh.ring[warp][stage]);
-                const int lo = l_first - l_from, hi = l_n - l_from;  // rows [lo, hi) are seen
                 constexpr int kChunks = S::row / 16;
 #pragma unroll
                 for (int j = 0; j < kAttnTile * kChunks / 32; ++j) {
                     const int i = lane + 32 * j, r = i / kChunks, c = i % kChunks;
                     copy16(to + r * S::pitch + ((c ^ k_key<TYPE>(r)) << 4), k + i * 16, 16);
                 }
+                // V's rows outside [lo, hi) are zeros: p is 0 there, whatever the cache holds
+                const int lo = l_first - l_from, hi = l_n - l_from;
+                if (lo <= 0 && hi >= kAttnTile) {
 #pragma unroll
-                for (int j = 0; j < kAttnTile * kChunks / 32; ++j) {
-                    const int i = lane + 32 * j, r = i / kChunks, c = i % kChunks;
-                    // V's other rows are zeros: p is 0 there, whatever the cache holds
-                    copy16(to + S::matrix + r * S::pitch + ((c ^ v_key<TYPE>(r)) << 4), v + i * 16,
-                           r >= lo && r < hi ? 16 : 0);
+                    for (int j = 0; j < kAttnTile * kChunks / 32; ++j) {
+                        const int i = lane + 32 * j, r = i / kChunks, c = i % kChunks;
+                        copy16(to + S::matrix + r * S::pitch + ((c ^ v_key<TYPE>(r)) << 4), v + i * 16, 16);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kAttnTile * kChunks / 32; ++j) {
+                        const int i = lane + 32 * j, r = i / kChunks, c = i % kChunks;
+                        copy16(to + S::matrix + r * S::pitch + ((c ^ v_key<TYPE>(r)) << 4), v + i * 16,
+                               r >= lo && r < hi ? 16 : 0);
+                    }
                 }
                 if constexpr (TYPE == kQ8) {
                     const size_t scales = (size_t)a.page_size * D + (size_t)slot * (KC * 2);
@@ -479,9 +512,9 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
         // score factor: to base 2 at once, or to the score itself when capped
         const float s_factor = q_factor * a.scale * (capped ? 1.0f : kLog2e);
 
-        float o[NJ][2];
+        Two o[NJ];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = 0.0f;
+        for (int j = 0; j < NJ; ++j) o[j] = two(0.0f, 0.0f);
         float m = -INFINITY, l = 0.0f;  // head g: maximum (base 2) and this lane's part of the sum
         int unit_exp = -30;             // q8: the sums of p v are in units of 2^unit_exp
 
@@ -499,7 +532,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         load_scales<KC>(ks[i], vt + S::matrix + (8 * (i >> 1) + 2 * t + (i & 1)) * (KC * 2));
-                    s[0][0] = s[0][1] = s[1][0] = s[1][1] = 0.0f;
+                    Two sum[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)};
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
                         const uint4 f0 = sh.q_frag[2 * c][lane], f1 = sh.q_frag[2 * c + 1][lane];
@@ -512,10 +545,12 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                             float acc[4] = {0.f, 0.f, 0.f, 0.f};
                             mma_f16(acc, q0, codes_f16(w.x, 0x4140), codes_f16(w.x, 0x4342));
                             mma_f16(acc, q1, codes_f16(w.y, 0x4140), codes_f16(w.y, 0x4342));
-                            s[j][0] = fmaf(acc[0] + acc[2], __half2float(ks[2 * j][c]), s[j][0]);
-                            s[j][1] = fmaf(acc[1] + acc[3], __half2float(ks[2 * j + 1][c]), s[j][1]);
+                            sum[j] = fma2(add2(two(acc[0], acc[1]), two(acc[2], acc[3])),
+                                          two(__half2float(ks[2 * j][c]), __half2float(ks[2 * j + 1][c])), sum[j]);
                         }
                     }
+                    split(sum[0], s[0][0], s[0][1]);
+                    split(sum[1], s[1][0], s[1][1]);
                 } else {
                     float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
                     float low_acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -560,19 +595,27 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                     for (int e = 0; e < 2; ++e) {
                         float x = s[j][e] * s_factor;
                         if (capped) x = a.softcap * tanhf(x * inv_cap) * kLog2e;
-                        const int tk = tok + 8 * j + 2 * t + e;
-                        s[j][e] = full || (tk >= first && tk < n) ? x : -INFINITY;
+                        s[j][e] = x;
                     }
+                if (!full) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int tk = tok + 8 * j + 2 * t + e;
+                            if (tk < first || tk >= n) s[j][e] = -INFINITY;
+                        }
+                }
                 float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
                 const float m_new = fmaxf(m, mx);
                 const float m_use = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every p is 0
-                float alpha = exp2f(m - m_use);
+                float alpha = ex2(m - m_use);
                 m = m_new;
                 float p[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = exp2f(s[i >> 1][i & 1] - m_use);
+                for (int i = 0; i < 4; ++i) p[i] = ex2(s[i >> 1][i & 1] - m_use);
                 l = fmaf(l, alpha, (p[0] + p[1]) + (p[2] + p[3]));
 
                 if constexpr (TYPE == kQ8) {
@@ -589,24 +632,26 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                     // the largest scale met: below 2^unit_exp
                     __half2 big = __half2half2(__ushort_as_half(0));
 #pragma unroll
-                    for (int i = 0; i < 4; i += 2)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int c = 0; c < KC; ++c) big = __hmax2(big, __habs2(__halves2half2(vs[i][c], vs[i + 1][c])));
+                        for (int c = 0; c < KC; c += 2)
+                            big = __hmax2(big, __habs2(__halves2half2(vs[i][c], vs[i][c + 1 < KC ? c + 1 : c])));
                     float bm = fmaxf(__low2float(big), __high2float(big));
                     bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 1));
                     bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 2));
                     const int e = max(unit_exp, min((int)(__float_as_uint(bm) >> 23) - 126, 30));
                     alpha *= __uint_as_float((unsigned)(127 + unit_exp - e) << 23);
                     unit_exp = e;
+                    const Two alpha2 = two(alpha, alpha);
                     const float up_p = kPScale * __uint_as_float((unsigned)(127 - e) << 23);
-                    float ps[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) ps[i] = p[i] * up_p;
+                    const Two ps[2] = {mul2(two(p[0], p[1]), two(up_p, up_p)), mul2(two(p[2], p[3]), two(up_p, up_p))};
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
                         uint32_t pa[4];
-                        split_f16(ps[0] * __half2float(vs[0][c]), ps[1] * __half2float(vs[1][c]), pa[0], pa[1]);
-                        split_f16(ps[2] * __half2float(vs[2][c]), ps[3] * __half2float(vs[3][c]), pa[2], pa[3]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            split_f16(mul2(ps[i], two(__half2float(vs[2 * i][c]), __half2float(vs[2 * i + 1][c]))), pa[2 * i],
+                                      pa[2 * i + 1]);
                         uint32_t x[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -622,11 +667,11 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                             float acc[4] = {0.f, 0.f, 0.f, 0.f};
                             mma_f16(acc, pa, codes_f16(lo[i >> 1], sel), codes_f16(hi[i >> 1], sel));
                             const int j = 4 * c + i;
-                            o[j][0] = fmaf(o[j][0], alpha, acc[0] + acc[2]);
-                            o[j][1] = fmaf(o[j][1], alpha, acc[1] + acc[3]);
+                            o[j] = fma2(o[j], alpha2, add2(two(acc[0], acc[1]), two(acc[2], acc[3])));
                         }
                     }
                 } else {
+                    const Two alpha2 = two(alpha, alpha);
                     uint32_t pa[4], pl[4] = {0, 0, 0, 0};
                     if constexpr (TYPE == kBF16) {
                         split_bf16(p[0], p[1], pa[0], pa[1], pl[0]);
@@ -656,8 +701,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                                 mma_f16(acc, pa, b0, b1);
                             }
                             const int j = 8 * c + i;
-                            o[j][0] = fmaf(o[j][0], alpha, acc[0] + acc[2]);
-                            o[j][1] = fmaf(o[j][1], alpha, acc[1] + acc[3]);
+                            o[j] = fma2(o[j], alpha2, add2(two(acc[0], acc[1]), two(acc[2], acc[3])));
                         }
                     }
                 }
@@ -698,12 +742,15 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
             if (h0 > 0) __syncthreads();  // the heads before have been read
             if (g >= h0 && g < h0 + S::meet) {
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
+                for (int j = 0; j < NJ; ++j) {
+                    float x[2];
+                    split(mul2(o[j], two(o_unit, o_unit)), x[0], x[1]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int d = value_of<TYPE>(j, e, t);
-                        if (d < D) sh.x_o[warp][g - h0][d] = o[j][e] * o_unit;
+                        if (d < D) sh.x_o[warp][g - h0][d] = x[e];
                     }
+                }
             }
             __syncthreads();
             constexpr int kMeet = S::meet * D / 4;  // float4s of these heads
@@ -720,7 +767,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                     float L = 0.0f;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
-                        const float f = exp2f(sh.x_m[w][h] - M_use);
+                        const float f = ex2(sh.x_m[w][h] - M_use);
                         const float4 u = *reinterpret_cast<const float4 *>(&sh.x_o[w][hh][d]);
                         L = fmaf(sh.x_l[w][h], f, L);
                         v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y);
@@ -772,7 +819,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                     for (int o2 = 16; o2 > 0; o2 >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o2));
                     const float M_use = M == -INFINITY ? 0.0f : M;
                     for (int p = lane; p < pieces; p += 32) {
-                        const float f = exp2f(sh.weight[p][h] - M_use);
+                        const float f = ex2(sh.weight[p][h] - M_use);
                         L = fmaf(sh.mass[p][h], f, L);
                         sh.weight[p][h] = f;
                     }

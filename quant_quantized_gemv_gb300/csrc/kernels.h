@@ -231,11 +231,11 @@ constexpr int kAttnUnitCost = 2;     // rounds that the beginning and end of a u
 // fits 227 KB, a stage being 16 tokens' K and V.
 __host__ __device__ constexpr int attn_warps(int type, int head_dim)
 {
-    return type == 3 ? (head_dim <= 128 ? 12 : 6) : head_dim == 64 ? 12 : head_dim <= 128 ? 8 : 4;
+    return type == 3 ? (head_dim <= 128 ? 12 : 8) : head_dim == 64 ? 12 : head_dim <= 128 ? 8 : 4;
 }
 __host__ __device__ constexpr int attn_stages(int type, int head_dim) { return head_dim == 64 ? 3 : 2; }
 // Heads that a CTA's warps exchange at a time at the end of a unit (shared memory again).
-__host__ __device__ constexpr int attn_meet_heads(int type, int head_dim) { return 8; }
+__host__ __device__ constexpr int attn_meet_heads(int type, int head_dim) { return type == 3 && head_dim > 128 ? 4 : 8; }
 constexpr int attn_part_floats(int head_dim) { return kAttnHeads * (head_dim + 2); }
 
 struct AttnLaunch {

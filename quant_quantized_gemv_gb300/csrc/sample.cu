@@ -51,6 +51,7 @@
 #include <atomic>
 #include <utility>
 
+#include "f32x2.cuh"
 #include "kernels.h"
 
 namespace mq {
@@ -126,36 +127,6 @@ __device__ __forceinline__ u64 place_of(float x, int index)
 }
 
 constexpr float kMagic = 12582912.0f;  // 1.5 x 2^23: a float + this has the rounded integer in its low bits
-
-// Two floats an instruction (each rounded as its scalar form).
-struct Two {
-    u64 v;
-};
-__device__ __forceinline__ Two two(float a, float b)
-{
-    Two r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void split(Two x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c)
-{
-    Two r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ Two add2(Two a, Two b)
-{
-    Two r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Two mul2(Two a, Two b)
-{
-    Two r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
 
 struct Weight {
     float top, c_hi, c_lo;  // the row's maximum; log2(e) / temperature in two parts
