@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
         single_n = __ldcg(a.lens + load_at.row);
         end = line_of(single_n);
     }
+    auto kv_head = [&](int unit) { return a.subgroups == 1 ? unit : unit / a.subgroups; };
     auto n_of = [&](int row) { return shared_out ? sh.lens[row] : single_n; };
     // completes a segment that begins where its fields say (its round counted with the unit's cost; from
     // then on without); false: none is left
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
         l_from = start_of(l_n) + load_at.round * kRound + warp * kAttnTile;
         l_to = bad ? 0 : min(l_n, start_of(l_n) + (load_at.round + load_at.take) * kRound);
         l_table = a.pages + (bad ? 0 : (size_t)seq * a.pages_stride);
-        l_head = (size_t)(load_at.unit / a.subgroups) * a.head_bytes;
+        l_head = (size_t)kv_head(load_at.unit) * a.head_bytes;
     };
     auto ask_pages = [&]() {
         const int tok = l_from + lane * kRound;
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
     auto issue = [&](int stage) {
         if (load_live) {
             if (load_round == 0) {  // the unit's queries
-                const int sg = load_at.unit % a.subgroups, kvh = load_at.unit / a.subgroups;
+                const int kvh = kv_head(load_at.unit), sg = load_at.unit - kvh * a.subgroups;
                 const int head0 = kvh * a.group + sg * kAttnHeads, heads = min(kAttnHeads, a.group - sg * kAttnHeads);
                 const float *src = a.q + load_at.row * a.q_stride + (size_t)head0 * D;
                 const uint32_t dst = shared_address(sh.q[load_count % (NS + 1)]);
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
     const float inv_cap = capped ? 1.0f / a.softcap : 0.0f;
     int stage = 0;
     for (int count = 0;; ++count) {
-        const int sg = at.unit % a.subgroups, kvh = at.unit / a.subgroups;
+        const int kvh = kv_head(at.unit), sg = at.unit - kvh * a.subgroups;
         const int head0 = kvh * a.group + sg * kAttnHeads, heads = min(kAttnHeads, a.group - sg * kAttnHeads);
         const int n = n_of(at.row), first = first_of(n);
         const int from = start_of(n) + at.round * kRound + warp * kAttnTile;
@@ -787,16 +788,16 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
         if (!whole) {
             __syncthreads();  // the parts are written; the exchange has been read
             if (tid == 0) {
-                __threadfence();  // all of this CTA's part, before it is counted
-                const unsigned arrived = atomicAdd(a.ws_cnt + cta0, 1u);
+                // this CTA's part (all of it: the barrier) before the count, the others' after it
+                unsigned arrived;
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(arrived) : "l"(a.ws_cnt + cta0) : "memory");
                 sh.last = arrived + 1 == (unsigned)pieces;
                 if (sh.last) a.ws_cnt[cta0] = 0;  // as the next call expects it
-                __threadfence();  // and the others' parts after the count
             }
             __syncthreads();
             if (sh.last) {
                 // the pieces' values are asked for before their weights are known: kAhead at a time
-                constexpr int kAhead = 8;
+                constexpr int kAhead = 16;
                 float4 u[kAhead];
                 auto ask = [&](int idx, int p0) {
 #pragma unroll
