@@ -948,8 +948,9 @@ def mq_attn_decode(kv: MQKVCache, q, lens, pages, scale: float, out=None, q8=Non
         _vec(q8, q8.numel(), torch.uint8, dev, "q8")
         if q8.numel() < nt * mq_q8_bytes(nq):
             raise ValueError(f"q8: smaller than {nt} planes of {nq} values")
-    if ws is None:
-        ws = mq_attn_workspace(kv, nq // d, nt, max_len)
+    if ws is None and mq_attn_workspace_bytes(kv, nq // d, nt, max_len):
+        with torch.cuda.stream(stream):  # zeroed, used and freed in the launch's order (None: the current stream)
+            ws = mq_attn_workspace(kv, nq // d, nt, max_len)
     wsb = 0 if ws is None else ws.numel()
     qp, qs = _rows(q, nt, nq, f32, dev, "q")
     op, os_ = _rows(out, nt, nq, f32, dev, "out")

@@ -163,7 +163,7 @@ size_t mq_attn_workspace_bytes(const mq_kv_cache *kv, int n_heads, int nt, int m
     if (!kv || !attn_shape_ok(kv, n_heads, nt, max_len)) return 0;
     const int sms = mq_device_sms();
     if (sms <= 0) return 0;
-    return nt > kAttnMaxRows ? 0 : attn_ws_bytes(kv, max_len, sms);
+    return attn_ws_bytes(kv, max_len, sms);
 }
 
 int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *a, void *stream)

@@ -44,6 +44,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4;
 constexpr int kUnits = 7;  // groups of heads a warp takes when there are many rows
 constexpr int kMaxGroups = kWarps * kUnits;
+static_assert(kWarps * 32 >= 128, "a thread for each of the up to 128 angles");
 
 template <int EPL>
 struct Vals {

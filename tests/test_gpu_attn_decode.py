@@ -147,6 +147,32 @@ def test_many_rows(mq):
     c.check(c.run(), rows=list(range(0, 70, 9)))
 
 
+@pytest.mark.parametrize("window", [0, 100])
+def test_more_rows_than_are_shared_out(mq, window):
+    """Past 1024 rows every unit has a CTA of its own (no workspace, no cut)."""
+    lens = [(i * 37) % 700 - (1 if i % 11 == 0 else 0) for i in range(1100)]
+    c = Case(mq, "f16", 64, 4, 2, 16, lens)
+    out = c.run(window=window)
+    rows = [i for i in range(0, 1100, 97) if lens[i] > window] + [0, 1099]
+    c.check(out, rows=rows, window=window)
+    for i in np.flatnonzero(c.lens < 0):
+        assert (out[i] == 7.0).all()
+
+
+def test_exactly_the_rows_that_are_shared_out(mq):
+    """1024 rows, the most of one shared launch: empty, padded, short and long ones."""
+    lens = [0 if i % 5 == 0 else -1 if i % 7 == 0 else 1 + (i * 131) % 300 for i in range(1023)] + [5000]
+    c = Case(mq, "q8", 64, 2, 1, 16, lens)
+    out = c.run()
+    c.check(out, rows=list(range(0, 1024, 61)) + [1023])
+    assert (out[c.lens == 0] == 0).all() and (out[c.lens < 0] == 7.0).all() and torch_finite(out[c.lens > 0])
+
+
+def torch_finite(t):
+    import torch
+    return bool(torch.isfinite(t).all())
+
+
 @pytest.mark.parametrize("kv", ["f16", "q8"])
 @pytest.mark.parametrize("window", [1, 15, 16, 17, 100, 1024, 5000])
 def test_windows(mq, kv, window):
@@ -307,6 +333,12 @@ def test_captured_replayed_and_on_another_stream(mq):
     import torch
     c = Case(mq, "bf16", 128, 8, 2, 16, [3000, 17, 500])
     want = c.run(max_len=4000)
+    # without a workspace: one is made, zeroed and used in the stream's order
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    free = mq.mq_attn_decode(c.cache, dev(c.q), dev(c.lens), dev(c.table), c.scale, max_len=4000, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(free, want)
     ws = mq.mq_attn_workspace(c.cache, 8, 3, 4000)
     q, lens, table = torch.zeros_like(dev(c.q)), torch.zeros(3, dtype=torch.int32, device="cuda"), dev(c.table)
     out = torch.zeros_like(q)
