@@ -22,18 +22,23 @@
 //
 // Work: a row's heads, queries | keys | values, in groups of what a warp's lanes
 // hold, are shared by the CTAs of the row.  A CTA first writes down where each
-// of its groups is read and what becomes of it, then all its loads are under way
-// while it finds the row's page and one thread per pair computes an angle.
+// of its groups is read and what becomes of it; then its first loads are under
+// way while one thread per pair computes an angle and the row's page is found,
+// which only the cache entries wait for.
 //
 // What bounds it: few rows, the launch and three dependent loads (2.9 us a call
-// in a captured chain).  Many rows, latency and instructions before HBM: 4096
-// rows of the 14B shape (40 + 8 + 8 heads of 128) take 53 us, 4.1 TB/s, where
-// their 218 MB take 33; 28 groups a CTA of 4 warps (56 in 8 warps: 55, one load
-// ahead and every warp its own angles: 57 to 65, one group a warp: 123).
+// in a captured chain).  Many rows, instructions and the latency of a CTA's
+// beginning, before HBM: 4096 rows of the 14B shape (40 + 8 + 8 heads of 128)
+// take 48 us, 4.5 TB/s, where their 218 MB take 33 (127 instructions a group with
+// 28 groups a CTA of 4 warps: 54 us; 56 groups, as here, spread the beginning
+// over twice as many; more loads in flight a lane cost registers, 8: 52 us; one
+// group a warp: 123 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "kernels.h"
 
@@ -42,8 +47,10 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4;
-constexpr int kUnits = 7;  // groups of heads a warp takes when there are many rows
+constexpr int kUnits = 14;  // groups of heads a warp takes when there are many rows
+constexpr int kLoads = 4;  // float4 loads of a lane in flight
 constexpr int kMaxGroups = kWarps * kUnits;
+constexpr int kGridRows = 32768;  // rows along the grid's y
 static_assert(kWarps * 32 >= 128, "a thread for each of the up to 128 angles");
 
 template <int EPL>
@@ -100,12 +107,12 @@ struct alignas(16) Group {
 template <int EPL>
 __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppendLaunch a)
 {
-    constexpr int kBatch = EPL == 4 ? kUnits : (kUnits + 1) / 2;  // groups a warp loads at a time
+    constexpr int kBatch = kLoads * 4 / EPL;  // groups a warp loads at a time
     __shared__ Group groups[kMaxGroups];
     __shared__ float cosine[128], sine[128];
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, D = a.head_dim;
-    const int lph = a.lanes_per_head, hpw = 32 / lph;  // lanes of a head: 16 or 32
+    const int two = a.two_heads, lph = 32 >> two;  // lanes of a head: 16 (two heads a group) or 32
     const int half = a.rope_dims >> 1;
     const int sub = lane >= lph ? 1 : 0, e = (lane & (lph - 1)) * EPL;  // this lane's head of a group, first value
     const bool in_head = e < D, rotated = e < a.rope_dims;
@@ -113,19 +120,20 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppe
     const int from = (lane + (rotated ? (upper ? -half : half) / EPL : 0)) & 31;
 
     // this CTA's row and groups
-    const int t = blockIdx.x / a.ctas_per_row, c = blockIdx.x - t * a.ctas_per_row;
-    const int gq = (a.n_heads + hpw - 1) / hpw, gk = (a.n_kv_heads + hpw - 1) / hpw;
+    const int t = blockIdx.y + blockIdx.z * kGridRows, c = blockIdx.x;
+    if (t >= a.nt) return;
+    const int gq = (a.n_heads + two) >> two, gk = (a.n_kv_heads + two) >> two;
     const int first = c * a.groups_per_cta, n = min(a.groups_per_cta, gq + 2 * gk - first);
     for (int i = tid; i < n; i += kWarps * 32) {
         const int gr = first + i, kind = gr < gq ? 0 : gr < gq + gk ? 1 : 2;
-        const int h = (kind == 0 ? gr : kind == 1 ? gr - gq : gr - gq - gk) * hpw;
+        const int h = (kind == 0 ? gr : kind == 1 ? gr - gq : gr - gq - gk) << two;
         const float *bias = kind == 0 ? a.q_bias : kind == 1 ? a.k_bias : a.v_bias;
         Group &g = groups[i];
         g.src = (kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride) + h * D;
         g.bias = bias ? bias + h * D : nullptr;
         g.dst = a.q_out + t * a.q_out_stride + h * D;
         g.kind = kind, g.head = h;
-        g.heads = min(hpw, (kind == 0 ? a.n_heads : a.n_kv_heads) - h);
+        g.heads = min(1 + two, (kind == 0 ? a.n_heads : a.n_kv_heads) - h);
     }
     const unsigned long long step = tid < half ? __ldg(a.rope_table + tid) : 0;  // no preceding kernel writes it
     __syncthreads();
@@ -150,13 +158,12 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppe
         const float h = __ll2float_rn((long long)((unsigned long long)pos * step)) * 0x1p-63f;
         sincospif(h, &sine[tid], &cosine[tid]);
     }
-    // the row's page; a row that names none writes nothing but NaN queries
+    // the row's page; a row that names none writes nothing but NaN queries, at the end
     const int seq = a.seq ? __ldcg(a.seq + t) : t;
-    const int pi = pos / a.page_size, slot = pos - pi * a.page_size;
+    const int pi = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size, slot = pos - pi * a.page_size;
     const bool named = (unsigned)seq < (unsigned)a.n_seqs && pi < a.pages_stride;
     const int page = named ? __ldcg(a.pages + (size_t)seq * a.pages_stride + pi) : -1;
     const bool ok = (unsigned)page < (unsigned)a.n_pages;
-    if (!ok && a.status && c == 0 && tid == 0) atomicOr(a.status, 1);
     const size_t page_at = (size_t)(ok ? page : 0) * a.page_stride, slot_at = (size_t)slot * D + e;
     __syncthreads();
     float cs[EPL], sn[EPL];
@@ -212,10 +219,6 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppe
                     }
                 }
                 if (kind == 0) {
-                    if (!ok) {
-#pragma unroll
-                        for (int j = 0; j < EPL; ++j) x[k].v[j] = __int_as_float(0x7fc00000);
-                    }
                     if (valid) {
                         float *dst = g.dst + sub * D + e;
 #pragma unroll
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppe
                 }
             }
             uint8_t *base = (kind == 1 ? a.k_pages : a.v_pages) + page_at + (size_t)(g.head + sub) * a.head_bytes;
-            const bool cached = valid && ok;
+            const bool cached = valid && ok;  // the first use of the page: the queries do not wait for it
             if (a.type == 1) {
                 if (cached) store16<EPL, __half>(base + slot_at * 2, x[k]);
             } else if (a.type == 2) {
@@ -255,23 +258,34 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppe
             }
         }
     }
+    if (!ok) {  // the row names no page: its queries become NaN
+        for (int i = warp; i < n; i += kWarps) {
+            const Group &g = groups[i];
+            if (g.kind != 0 || !in_head || sub >= g.heads) continue;
+            const float nan = __int_as_float(0x7fc00000);
+#pragma unroll
+            for (int j = 0; j < EPL; j += 4)
+                *reinterpret_cast<float4 *>(g.dst + sub * D + e + j) = make_float4(nan, nan, nan, nan);
+        }
+        if (a.status && c == 0 && tid == 0) atomicOr(a.status, 1);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_t st)
 {
-    a.lanes_per_head = a.head_dim <= 64 ? 16 : 32;
-    const int hpw = 32 / a.lanes_per_head;
-    const int groups = (a.n_heads + hpw - 1) / hpw + 2 * ((a.n_kv_heads + hpw - 1) / hpw);
+    a.two_heads = a.head_dim <= 64 ? 1 : 0;
+    a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
+    const int groups = ((a.n_heads + a.two_heads) >> a.two_heads) + 2 * ((a.n_kv_heads + a.two_heads) >> a.two_heads);
     // Few rows: a group a warp, for latency.  More: up to kUnits groups a warp, which share the
     // row's angles and its page.
     const long long wave = (long long)sms * 32;  // warps
     long long units = ((long long)a.nt * groups + wave - 1) / wave;
     units = units < 1 ? 1 : units > kUnits ? kUnits : units;
     a.groups_per_cta = (int)units * kWarps;
-    a.ctas_per_row = (groups + a.groups_per_cta - 1) / a.groups_per_cta;
-    const dim3 grid((unsigned)((long long)a.nt * a.ctas_per_row));
+    const int ctas = (groups + a.groups_per_cta - 1) / a.groups_per_cta;
+    const dim3 grid((unsigned)ctas, (unsigned)std::min(a.nt, kGridRows), (unsigned)((a.nt + kGridRows - 1) / kGridRows));
     const auto kernel = a.head_dim <= 128 ? rope_append_kernel<4> : rope_append_kernel<8>;
     return launch_maybe_pdl(kernel, grid, dim3(kWarps * 32), 0, pdl, st, a);
 }
