@@ -65,18 +65,30 @@ constexpr int kF16 = 1, kBF16 = 2, kQ8 = 3;  // MQ_KV_*
 constexpr float kPScale = 16384.0f;          // p's factor in fp16 parts: 2^14
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+// c = a b, or c += a b; bf16 or fp16 operands.
+template <bool BF16>
+__device__ __forceinline__ void product(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
-
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+template <bool BF16>
+__device__ __forceinline__ void add_product(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
@@ -543,9 +555,9 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                             uint2 w = *reinterpret_cast<const uint2 *>(kt + (8 * j + g) * S::pitch +
                                                                        (((2 * c + (t >> 1)) ^ k_key<TYPE>(g)) << 4) + (t & 1) * 8);
                             w.x ^= 0x80808080u, w.y ^= 0x80808080u;
-                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma_f16(acc, q0, codes_f16(w.x, 0x4140), codes_f16(w.x, 0x4342));
-                            mma_f16(acc, q1, codes_f16(w.y, 0x4140), codes_f16(w.y, 0x4342));
+                            float acc[4];
+                            product<false>(acc, q0, codes_f16(w.x, 0x4140), codes_f16(w.x, 0x4342));
+                            add_product<false>(acc, q1, codes_f16(w.y, 0x4140), codes_f16(w.y, 0x4342));
                             sum[j] = fma2(add2(two(acc[0], acc[1]), two(acc[2], acc[3])),
                                           two(__half2float(ks[2 * j][c]), __half2float(ks[2 * j + 1][c])), sum[j]);
                         }
@@ -553,8 +565,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                     split(sum[0], s[0][0], s[0][1]);
                     split(sum[1], s[1][0], s[1][1]);
                 } else {
-                    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                    float low_acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                    float acc[2][4], low_acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
                         uint4 k[2];
@@ -574,19 +585,20 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const uint32_t b0 = h ? k[j].z : k[j].x, b1 = h ? k[j].w : k[j].y;
-                                if constexpr (TYPE == kBF16) {
-                                    mma_bf16(acc[j], qa, b0, b1);
-                                    mma_bf16(low_acc[j], ql, b0, b1);
+                                if (c + h == 0) {
+                                    product<TYPE == kBF16>(acc[j], qa, b0, b1);
+                                    if constexpr (TYPE == kBF16) product<true>(low_acc[j], ql, b0, b1);
                                 } else {
-                                    mma_f16(acc[j], qa, b0, b1);
+                                    add_product<TYPE == kBF16>(acc[j], qa, b0, b1);
+                                    if constexpr (TYPE == kBF16) add_product<true>(low_acc[j], ql, b0, b1);
                                 }
                             }
                         }
                     }
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        s[j][0] = acc[j][0] + (acc[j][2] + low_acc[j][0]);
-                        s[j][1] = acc[j][1] + (acc[j][3] + low_acc[j][1]);
+                        s[j][0] = TYPE == kBF16 ? acc[j][0] + (acc[j][2] + low_acc[j][0]) : acc[j][0] + acc[j][2];
+                        s[j][1] = TYPE == kBF16 ? acc[j][1] + (acc[j][3] + low_acc[j][1]) : acc[j][1] + acc[j][3];
                     }
                 }
                 const bool full = tok >= first && tok + kAttnTile <= n;
@@ -665,8 +677,8 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t sel = (i & 1) ? 0x4342 : 0x4140;
-                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma_f16(acc, pa, codes_f16(lo[i >> 1], sel), codes_f16(hi[i >> 1], sel));
+                            float acc[4];
+                            product<false>(acc, pa, codes_f16(lo[i >> 1], sel), codes_f16(hi[i >> 1], sel));
                             const int j = 4 * c + i;
                             o[j] = fma2(o[j], alpha2, add2(two(acc[0], acc[1]), two(acc[2], acc[3])));
                         }
@@ -694,12 +706,12 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                             const uint32_t sel = (i & 1) ? 0x7632 : 0x5410;
                             const uint32_t b0 = __byte_perm(v0[i >> 1], v1[i >> 1], sel);
                             const uint32_t b1 = __byte_perm(v2[i >> 1], v3[i >> 1], sel);
-                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                            float acc[4];
                             if constexpr (TYPE == kBF16) {
-                                mma_bf16(acc, pl, b0, b1);
-                                mma_bf16(acc, pa, b0, b1);
+                                product<true>(acc, pl, b0, b1);
+                                add_product<true>(acc, pa, b0, b1);
                             } else {
-                                mma_f16(acc, pa, b0, b1);
+                                product<false>(acc, pa, b0, b1);
                             }
                             const int j = 8 * c + i;
                             o[j] = fma2(o[j], alpha2, add2(two(acc[0], acc[1]), two(acc[2], acc[3])));
