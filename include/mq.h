@@ -641,18 +641,24 @@ int mq_rope_append(const mq_kv_cache *kv, const mq_rope_append_args *args, void 
  * Products with the cache are exact to f32 (queries and probabilities go
  * through the tensor cores in two fp16 or three bf16 parts); statistics and
  * sums are f32.  The result does not depend on the run (the order is fixed).
- *   max_len: no row is longer; the launch and its split are sized by it.  A
- *     longer row is out of range (see above).
+ * The work is shared out on the device, by the rows' lengths: a batch of very
+ * different lengths keeps the GPU as busy as one of equal ones.  Past 1024 rows
+ * each row's heads have a CTA of their own instead.
+ *   max_len: no row is longer; the launch is sized by it.  A longer row is out
+ *     of range (see above).
  *   q, out: rows of n_heads * head_dim f32, strides in values, multiples of 4.
+ *     out may be q (the same rows).
  *   q8: NULL, or nt planes of n_heads * head_dim values back to back
  *     (mq_q8_bytes each): out's quantization, what mq_quantize_q8_batch gives.
- *   ws: mq_attn_workspace_bytes(kv, n_heads, nt, max_len) bytes or more (a
- *     workspace sized for larger nt and max_len serves), device, 16-byte aligned,
+ *   ws: mq_attn_workspace_bytes(kv, n_heads, nt, max_len) bytes or more (0 when
+ *     max_len is short, else a size that depends on the device and head_dim alone,
+ *     so one workspace serves calls of every size), device, 16-byte aligned,
  *     zero-filled before its first use; every completed call leaves its counters
  *     zero.  NULL when 0 bytes are needed.  Calls that share a workspace,
  *     replayed graphs among them, must be ordered on one stream.
  * Shapes: n_heads a multiple of n_kv_heads; max_len >= 1; window >= 0;
- *   softcap >= 0; scale and softcap finite.
+ *   softcap >= 0; scale and softcap finite; nt * n_heads * (max_len / 64 + 4)
+ *   below 2^31 and nt * n_heads below 2^24.
  * Errors: MQ_ERR_NULL, MQ_ERR_SHAPE, MQ_ERR_ALIGN, MQ_ERR_WORKSPACE,
  *         MQ_ERR_CUDA.
  * ------------------------------------------------------------------------ */

@@ -293,6 +293,17 @@ def test_strided_rows_and_pages(mq):
     assert torch.equal(out[:, 1024:], want) and (out[:, :1024] == 7.0).all()
 
 
+@pytest.mark.parametrize("kv,hq,hkv", [("f16", 8, 2), ("bf16", 20, 2), ("q8", 8, 8)])
+def test_in_place(mq, kv, hq, hkv):
+    """out is q: rows that are cut over many CTAs, and head groups of one kv head."""
+    import torch
+    c = Case(mq, kv, 128, hq, hkv, 16, [9000, 3, 0, 700, 4000])
+    want = c.run()
+    q = dev(c.q)
+    c.run(q=q, out=q)
+    assert torch.equal(q, want)
+
+
 def test_cache_beyond_32_bits(mq):
     """Pages past 4 GB: their offsets need 64 bits."""
     import torch

@@ -156,6 +156,31 @@ def test_infinities_and_nan(mq):
         check(x, u, got, **f)
 
 
+@pytest.mark.parametrize("t", [np.inf, 1e-38, 1e-45, -1.0, np.nan])
+def test_temperatures_at_the_ends(mq, t):
+    """Infinite: every finite logit weighs the same.  Vanishing, negative and
+    NaN: the largest (equal ones share the draw where the temperature is positive)."""
+    x, u = rows("ends", 6, 900, 2.0)
+    x[2, 40:] = -np.inf
+    x[4, [7, 300]] = 20.0
+    for f in (dict(), dict(k=30), dict(p=0.5), dict(m=0.5)):
+        got = run(mq, x, u, t=t, **f)
+        if np.isinf(t):
+            kept = np.isfinite(x)
+            if "k" in f or "p" in f:
+                order = np.argsort(-x, kind="stable", axis=1)
+                n = np.full(6, f["k"]) if "k" in f else np.ceil(kept.sum(1) * 0.5).astype(int)
+                kept = np.zeros_like(kept)
+                for i in range(6):
+                    kept[i, order[i, :n[i]]] = True
+            for i in range(6):
+                at = np.flatnonzero(kept[i])
+                assert got[0][i] == at[int(np.float64(np.float32(u[i])) * len(at))]
+                assert abs(got[1][i] * len(at) - 1) < 2.0 ** -22
+        else:
+            check(x, u, got, t=t if t > 0 else 0.0, **f)
+
+
 def test_u_outside_its_range(mq):
     x, _ = rows("u", 4, 700)
     u = np.array([-1.0, 1.0, 2.0, np.nan], np.float32)
