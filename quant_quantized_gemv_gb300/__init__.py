@@ -811,17 +811,24 @@ class MQKVCache:
         self._ref = ctypes.byref(self._struct)
 
 
-def _on_current(index: int):
-    """The calls below run on the current device; its index, if it is `index`."""
+_torch = None
+
+
+def _bind_torch():
+    """torch, imported once: an import statement in every call of the functions below would cost more
+    than their checks."""
+    global _torch
     import torch
-    if torch._C._cuda_getDevice() != index:
+    _torch = torch
+    return torch
+
+
+def _launch_stream(stream, index: int) -> int:
+    """The stream of a launch on cuda:`index`, which must be the current device."""
+    c = _torch._C
+    if c._cuda_getDevice() != index:
         raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
-    return index
-
-
-def _raw_stream(stream, index: int) -> int:
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return c._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _bad_tensor(t, shape, dtype, index, what):
@@ -881,10 +888,10 @@ def mq_rope_append(kv: MQKVCache, q, k, v, positions, pages, q_out=None, rope=No
     row (row t is sequence t when None); rope: mq_rope_table's steps (None:
     no rotation); style: "half" or "pairs"; status: int32 [1], gets 1 OR-ed
     in when a row names no valid page."""
-    import torch
+    torch = _torch or _bind_torch()
     f32, i32 = torch.float32, torch.int32
     dev, d, hkv = kv.device_index, kv.head_dim, kv.n_kv_heads
-    _on_current(dev)
+    st = _launch_stream(stream, dev)
     nt, nq = q.shape
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=f32, device=q.device)
@@ -903,9 +910,9 @@ def mq_rope_append(kv: MQKVCache, q, k, v, positions, pages, q_out=None, rope=No
         _vec(k_gain, d, f32, dev, "k_gain"), _vec(rope, half, torch.int64, dev, "rope"),
         _vec(positions, nt, i32, dev, "positions"), _vec(seq, nt, i32, dev, "seq"),
         _vec(pages, n_seqs * per_seq, i32, dev, "pages"), n_seqs, per_seq, _vec(status, 1, i32, dev, "status"))
-    st = (_lib or lib()).mq_rope_append(kv._ref, ctypes.byref(args), _raw_stream(stream, dev))
-    if st:
-        raise MQError(st, "mq_rope_append")
+    err = _lib.mq_rope_append(kv._ref, ctypes.byref(args), st)
+    if err:
+        raise MQError(err, "mq_rope_append")
     return q_out
 
 
@@ -932,10 +939,10 @@ def mq_attn_decode(kv: MQKVCache, q, lens, pages, scale: float, out=None, q8=Non
     mq_rope_append; max_len: no row is longer (None: what the page table
     holds); q8: a uint8 tensor that gets nt q8 planes of out; ws: from
     mq_attn_workspace (made for this call when None and one is needed)."""
-    import torch
+    torch = _torch or _bind_torch()
     f32, i32 = torch.float32, torch.int32
     dev, d = kv.device_index, kv.head_dim
-    _on_current(dev)
+    st = _launch_stream(stream, dev)
     nt, nq = q.shape
     if out is None:
         out = torch.empty(q.shape, dtype=f32, device=q.device)
@@ -959,9 +966,9 @@ def mq_attn_decode(kv: MQKVCache, q, lens, pages, scale: float, out=None, q8=Non
         None if q8 is None else q8.data_ptr(), _vec(lens, nt, i32, dev, "lens"), _vec(seq, nt, i32, dev, "seq"),
         _vec(pages, n_seqs * per_seq, i32, dev, "pages"), n_seqs, per_seq, _vec(ws, wsb, torch.uint8, dev, "ws"), wsb,
         _vec(status, 1, i32, dev, "status"))
-    st = (_lib or lib()).mq_attn_decode(kv._ref, ctypes.byref(args), _raw_stream(stream, dev))
-    if st:
-        raise MQError(st, "mq_attn_decode")
+    err = _lib.mq_attn_decode(kv._ref, ctypes.byref(args), st)
+    if err:
+        raise MQError(err, "mq_attn_decode")
     return out
 
 
@@ -974,9 +981,10 @@ def mq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     filter out (temperature 1).  temperature 0 is the most likely token.
     prob: an f32 tensor [nt] that gets the token's probability among those
     kept.  A row without a finite logit gives -1."""
-    import torch
+    torch = _torch or _bind_torch()
     f32, i32 = torch.float32, torch.int32
-    dev = _on_current(logits.get_device())
+    dev = logits.get_device()
+    st = _launch_stream(stream, dev)
     nt, vocab = logits.shape
     if token is None:
         token = torch.empty(nt, dtype=i32, device=logits.device)
@@ -985,7 +993,7 @@ def mq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
         nt, vocab, lp, ls, _vec(u, nt, f32, dev, "u"), _vec(temperature, nt, f32, dev, "temperature"),
         _vec(top_p, nt, f32, dev, "top_p"), _vec(min_p, nt, f32, dev, "min_p"), _vec(top_k, nt, i32, dev, "top_k"),
         _vec(token, nt, i32, dev, "token"), _vec(prob, nt, f32, dev, "prob"))
-    st = (_lib or lib()).mq_sample(ctypes.byref(args), _raw_stream(stream, dev))
-    if st:
-        raise MQError(st, "mq_sample")
+    err = (_lib or lib()).mq_sample(ctypes.byref(args), st)
+    if err:
+        raise MQError(err, "mq_sample")
     return token

@@ -47,6 +47,13 @@
 // is joined through the workspace: its CTAs leave their partial results, and the
 // last to arrive (an atomic count; nobody waits) adds them in order.  Units of
 // kAttnWhole rounds or less are not cut: the join costs more than they do.
+//
+// Measured (GB300, captured): 16 rows of 16384 tokens, 40 and 8 heads of 128:
+// f16 and bf16 159 us, 6.68 TB/s of the cache, the rate of a plain copy; q8 116
+// us, 4.9 TB/s, bound by 650 instructions a tile (f16: 350), a quarter of them
+// to turn codes into fp16.  One row of 32768 tokens: 28.5 us, where the bytes
+// take 20; of the rest 3 us pass before the first copy (length, page, launch)
+// and 3 in the join.  One row of 117 tokens: 5.1 us, all of it latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
