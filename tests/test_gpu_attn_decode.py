@@ -208,7 +208,7 @@ def test_windows(mq, kv, window):
 @pytest.mark.parametrize("kv,d", [("f16", 128), ("bf16", 256), ("q8", 96)])
 @pytest.mark.parametrize("cap,window", [(30.0, 0), (50.0, 700), (0.5, 0)])
 def test_capped_scores(mq, kv, d, cap, window):
-    c = Case(mq, kv, d, 12, 4, 16, [1, 40, 777, 2500], q_std=6.0)
+    c = Case(mq, kv, d, 8, 4, 16, [1, 40, 777, 2500], q_std=6.0)
     c.check(c.run(softcap=cap, window=window), softcap=cap, window=window)
 
 
