@@ -656,12 +656,14 @@ int mq_rope_append(const mq_kv_cache *kv, const mq_rope_append_args *args, void 
  *     zero-filled before its first use; every completed call leaves its counters
  *     zero.  NULL when 0 bytes are needed.  Calls that share a workspace,
  *     replayed graphs among them, must be ordered on one stream.
- * Shapes: n_heads a multiple of n_kv_heads; max_len >= 1; window >= 0;
- *   softcap >= 0; scale and softcap finite; nt * n_heads * (max_len / 64 + 4)
- *   below 2^31 and nt * n_heads below 2^24.
+ * Shapes: n_heads a multiple of n_kv_heads; 1 <= max_len <=
+ *   MQ_ATTN_MAX_LEN; window >= 0; softcap >= 0; scale and softcap finite;
+ *   nt * n_heads * (max_len / 64 + 4) below 2^30 and nt * n_heads below 2^24.
  * Errors: MQ_ERR_NULL, MQ_ERR_SHAPE, MQ_ERR_ALIGN, MQ_ERR_WORKSPACE,
  *         MQ_ERR_CUDA.
  * ------------------------------------------------------------------------ */
+#define MQ_ATTN_MAX_LEN (1 << 30)
+
 typedef struct {
     int nt, n_heads;               /* rows; query heads                    */
     int max_len, window;

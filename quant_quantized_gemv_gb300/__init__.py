@@ -720,9 +720,11 @@ def mq_gemv_q5k_q8_subdots(Wp, q8, rows: int, cols: int, stream=None):
 
 
 # ------------------------------------------------------------------ around the GEMVs of a decode step
+# An output that a call makes (none given) is allocated on the call's stream, as if that were current.
 KV_TYPES = {"f16": 1, "bf16": 2, "q8": 3}
 ROPE_STYLES = {"half": 0, "pairs": 1}
 MQ_SAMPLE_MAX_VOCAB = 655360
+MQ_ATTN_MAX_LEN = 1 << 30
 
 
 class _KVStruct(ctypes.Structure):
@@ -806,6 +808,8 @@ class MQKVCache:
         self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
         self.device_index = k.get_device()
         stride = k.stride(0) * k.element_size() if n_pages > 1 else 0
+        if n_pages > 1 and stride < page:
+            raise ValueError("pages must not overlap")
         self._struct = _KVStruct(KV_TYPES[kv_type], n_pages, page_size, n_kv_heads, head_dim,
                                  k.data_ptr(), v.data_ptr(), stride)
         self._ref = ctypes.byref(self._struct)
@@ -829,6 +833,14 @@ def _launch_stream(stream, index: int) -> int:
     if c._cuda_getDevice() != index:
         raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
     return c._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _made(like, shape, dtype, stream):
+    """A tensor for a launch's output: from the memory of the stream that writes it."""
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=like.device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _bad_tensor(t, shape, dtype, index, what):
@@ -894,7 +906,7 @@ def mq_rope_append(kv: MQKVCache, q, k, v, positions, pages, q_out=None, rope=No
     st = _launch_stream(stream, dev)
     nt, nq = q.shape
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=f32, device=q.device)
+        q_out = _made(q, q.shape, f32, stream)
     n_seqs, per_seq = _page_table(pages, nt, seq)
     if nq % d != 0:
         raise ValueError(f"q: {nq} columns are no whole heads of {d}")
@@ -917,7 +929,10 @@ def mq_rope_append(kv: MQKVCache, q, k, v, positions, pages, q_out=None, rope=No
 
 
 def mq_attn_workspace_bytes(kv: MQKVCache, n_heads: int, nt: int, max_len: int) -> int:
-    """Workspace bytes of mq_attn_decode for up to nt rows of up to max_len cached tokens."""
+    """Workspace bytes of mq_attn_decode for up to nt rows of up to max_len cached tokens (0: none are
+    needed, or a bad shape)."""
+    if max_len > MQ_ATTN_MAX_LEN:  # before it becomes a C integer
+        return 0
     return lib().mq_attn_workspace_bytes(kv._ref, n_heads, nt, max_len)
 
 
@@ -945,12 +960,14 @@ def mq_attn_decode(kv: MQKVCache, q, lens, pages, scale: float, out=None, q8=Non
     st = _launch_stream(stream, dev)
     nt, nq = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=f32, device=q.device)
+        out = _made(q, q.shape, f32, stream)
     n_seqs, per_seq = _page_table(pages, nt, seq)
     if nq % d != 0:
         raise ValueError(f"q: {nq} columns are no whole heads of {d}")
     if max_len is None:
         max_len = per_seq * kv.page_size
+    if max_len > MQ_ATTN_MAX_LEN or not 0 <= window < 2 ** 31:  # before they become C integers
+        raise MQError(MQ_ERR_SHAPE, "mq_attn_decode")
     if q8 is not None:
         _vec(q8, q8.numel(), torch.uint8, dev, "q8")
         if q8.numel() < nt * mq_q8_bytes(nq):
@@ -987,7 +1004,7 @@ def mq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     st = _launch_stream(stream, dev)
     nt, vocab = logits.shape
     if token is None:
-        token = torch.empty(nt, dtype=i32, device=logits.device)
+        token = _made(logits, (nt,), i32, stream)
     lp, ls = _rows(logits, nt, vocab, f32, dev, "logits")
     args = _SampleStruct(
         nt, vocab, lp, ls, _vec(u, nt, f32, dev, "u"), _vec(temperature, nt, f32, dev, "temperature"),

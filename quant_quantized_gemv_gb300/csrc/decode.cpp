@@ -72,11 +72,11 @@ bool attn_shape_ok(const mq_kv_cache *kv, int n_heads, int nt, int max_len)
 {
     if (mq_kv_page_bytes(kv->type, kv->n_kv_heads, kv->page_size, kv->head_dim) == 0) return false;
     if (nt < 1 || n_heads < 1 || n_heads % kv->n_kv_heads != 0 || max_len < 1) return false;
-    if (max_len > 0x7fffffff - 4096) return false;
-    // the grid, a q8 plane's values and the rounds of all rows
+    if (max_len > MQ_ATTN_MAX_LEN) return false;  // places in 32 bits, of rounds asked for ahead too
+    // the grid, a q8 plane's values and the rounds of all rows (a CTA's share ends up to its length behind them)
     const long long rounds = attn_rounds((long long)max_len + kAttnTile - 1, kv->type, kv->head_dim);
     return (long long)nt * n_heads < (1LL << 24) && (long long)n_heads * kv->head_dim < (1LL << 30) &&
-           (long long)nt * n_heads * (rounds + kAttnUnitCost) < (1LL << 31);
+           (long long)nt * n_heads * (rounds + kAttnUnitCost) < (1LL << 30);
 }
 
 long long attn_units(const mq_kv_cache *kv, int n_heads, int nt)

@@ -148,6 +148,7 @@ def test_attention_refuses_a_bad_cache(mq, bad, status):
 @pytest.mark.parametrize("bad,status", [
     (dict(nt=0), "SHAPE"), (dict(n_heads=0), "SHAPE"), (dict(n_heads=5), "SHAPE"), (dict(nt=1 << 24), "SHAPE"),
     (dict(max_len=0), "SHAPE"), (dict(max_len=-1), "SHAPE"), (dict(max_len=2 ** 31 - 1), "SHAPE"),
+    (dict(max_len=2 ** 30 + 1), "SHAPE"), (dict(max_len=2 ** 30, n_heads=256, q_stride=1 << 15, out_stride=1 << 15), "SHAPE"),
     (dict(window=-1), "SHAPE"), (dict(scale=math.inf), "SHAPE"), (dict(scale=math.nan), "SHAPE"),
     (dict(softcap=-2.0), "SHAPE"), (dict(softcap=math.nan), "SHAPE"), (dict(q_stride=508), "SHAPE"),
     (dict(out_stride=-512), "SHAPE"), (dict(n_seqs=0), "SHAPE"), (dict(pages_stride=0), "SHAPE"),

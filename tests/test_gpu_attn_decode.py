@@ -344,12 +344,14 @@ def test_captured_replayed_and_on_another_stream(mq):
     import torch
     c = Case(mq, "bf16", 128, 8, 2, 16, [3000, 17, 500])
     want = c.run(max_len=4000)
-    # without a workspace: one is made, zeroed and used in the stream's order
+    # without a workspace: one is made, zeroed and used in the stream's order; out is of its memory too, not
+    # of what the current stream has just given back
     side = torch.cuda.Stream()
+    given_back = torch.empty_like(want).data_ptr()
     torch.cuda.synchronize()
     free = mq.mq_attn_decode(c.cache, dev(c.q), dev(c.lens), dev(c.table), c.scale, max_len=4000, stream=side)
     torch.cuda.synchronize()
-    assert torch.equal(free, want)
+    assert torch.equal(free, want) and free.data_ptr() != given_back
     ws = mq.mq_attn_workspace(c.cache, 8, 3, 4000)
     q, lens, table = torch.zeros_like(dev(c.q)), torch.zeros(3, dtype=torch.int32, device="cuda"), dev(c.table)
     out = torch.zeros_like(q)
@@ -394,6 +396,9 @@ def test_refusals(mq):
             call(**bad)
     for bad, status in ((dict(q=torch.zeros(1, 3 * 128, device="cuda")), mq.MQ_ERR_SHAPE),
                         (dict(window=-1), mq.MQ_ERR_SHAPE), (dict(max_len=0), mq.MQ_ERR_SHAPE),
+                        (dict(max_len=2 ** 30 + 1), mq.MQ_ERR_SHAPE), (dict(max_len=2 ** 32 + 3000), mq.MQ_ERR_SHAPE),
+                        (dict(max_len=2 ** 32 + 3000, ws=None), mq.MQ_ERR_SHAPE),
+                        (dict(window=2 ** 32), mq.MQ_ERR_SHAPE), (dict(window=2 ** 31), mq.MQ_ERR_SHAPE),
                         (dict(scale=math.nan), mq.MQ_ERR_SHAPE), (dict(softcap=-1.0), mq.MQ_ERR_SHAPE),
                         (dict(softcap=math.inf), mq.MQ_ERR_SHAPE),
                         (dict(ws=ok[:64]), mq.MQ_ERR_WORKSPACE), (dict(ws=ok[8:]), mq.MQ_ERR_ALIGN)):

@@ -288,3 +288,33 @@ def test_refusals(mq):
         mq.MQKVCache("f16", 4, 24, 2, 128)
     with pytest.raises(mq.MQError):
         mq.MQKVCache("f16", 4, 16, 2, 80)
+
+
+def test_pages_that_overlap_are_refused(mq):
+    """A stride of 0 between pages would read as pages back to back."""
+    import torch
+    for kv, dtype, page in (("f16", torch.float16, (2, 16, 64)), ("q8", torch.uint8, (2, 16 * 68))):
+        one, four = (torch.zeros(n, *page, dtype=dtype, device="cuda") for n in (1, 4))
+        pages = one.expand(4, *page)
+        with pytest.raises(ValueError):
+            mq.MQKVCache(kv, 4, 16, 2, 64, k=pages, v=pages)
+        with pytest.raises(ValueError):
+            mq.MQKVCache(kv, 4, 16, 2, 64, k=four, v=pages)
+        halves = torch.as_strided(four, (4, *page), (four.stride(0) // 2, *four.stride()[1:]))
+        with pytest.raises(ValueError):
+            mq.MQKVCache(kv, 4, 16, 2, 64, k=halves, v=halves)
+        assert mq.MQKVCache(kv, 1, 16, 2, 64, k=pages[:1], v=four[:1])._struct.page_stride == 0
+
+
+def test_queries_made_for_another_stream_are_of_its_memory(mq):
+    """Not of what the current stream has just given back, which its kernels may still use."""
+    import torch
+    kv = mq.MQKVCache("f16", 4, 16, 2, 128)
+    q, k, v = (torch.ones(1, w * 128, device="cuda") for w in (4, 2, 2))
+    pos, table = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    given_back = torch.empty_like(q).data_ptr()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = mq.mq_rope_append(kv, q, k, v, pos, table, stream=st)
+    st.synchronize()
+    assert out.data_ptr() != given_back and torch.equal(out, q)

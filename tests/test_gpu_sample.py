@@ -272,3 +272,15 @@ def test_refusals(mq):
     with pytest.raises(mq.MQError) as e:
         mq.mq_sample(wide, u[:1])
     assert e.value.status == mq.MQ_ERR_SHAPE
+
+
+def test_a_token_made_for_another_stream_is_of_its_memory(mq):
+    """Not of what the current stream has just given back, which its kernels may still use."""
+    import torch
+    x, u = torch.zeros(2, 100, device="cuda"), torch.zeros(2, device="cuda")
+    given_back = torch.empty(2, dtype=torch.int32, device="cuda").data_ptr()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    token = mq.mq_sample(x, u, stream=st)
+    st.synchronize()
+    assert token.data_ptr() != given_back and token.tolist() == [0, 0]
