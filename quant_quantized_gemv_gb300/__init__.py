@@ -21,6 +21,7 @@ import numpy as np
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _SO = os.path.join(_PKG, "_build", "libmq.so")
+_BINDING = os.path.join(_PKG, "_build", "mq_binding.so")
 _lib = None
 
 (MQ_OK, MQ_ERR_SHAPE, MQ_ERR_ALIGN, MQ_ERR_NULL, MQ_ERR_COVERAGE, MQ_ERR_WORKSPACE, MQ_ERR_CUDA,
@@ -734,36 +735,6 @@ class _KVStruct(ctypes.Structure):
                 + [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_longlong)])
 
 
-class _RopeAppendStruct(ctypes.Structure):
-    """mq_rope_append_args of include/mq.h"""
-    _fields_ = ([(n, ctypes.c_int) for n in ("nt", "n_heads", "rope_dims", "rope_style")]
-                + [("eps", ctypes.c_float)]
-                + [(n, ctypes.c_void_p) for n in ("q", "k", "v")]
-                + [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "v_stride")]
-                + [("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_longlong)]
-                + [(n, ctypes.c_void_p) for n in ("q_bias", "k_bias", "v_bias", "q_gain", "k_gain",
-                                                  "rope_table", "positions", "seq", "pages")]
-                + [("n_seqs", ctypes.c_int), ("pages_stride", ctypes.c_int), ("status", ctypes.c_void_p)])
-
-
-class _AttnStruct(ctypes.Structure):
-    """mq_attn_args of include/mq.h"""
-    _fields_ = ([(n, ctypes.c_int) for n in ("nt", "n_heads", "max_len", "window")]
-                + [(n, ctypes.c_float) for n in ("scale", "softcap")]
-                + [("q", ctypes.c_void_p), ("out", ctypes.c_void_p)]
-                + [("q_stride", ctypes.c_longlong), ("out_stride", ctypes.c_longlong)]
-                + [(n, ctypes.c_void_p) for n in ("q8", "lens", "seq", "pages")]
-                + [("n_seqs", ctypes.c_int), ("pages_stride", ctypes.c_int)]
-                + [("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p)])
-
-
-class _SampleStruct(ctypes.Structure):
-    """mq_sample_args of include/mq.h"""
-    _fields_ = ([("nt", ctypes.c_int), ("vocab", ctypes.c_int), ("logits", ctypes.c_void_p),
-                 ("stride", ctypes.c_longlong)]
-                + [(n, ctypes.c_void_p) for n in ("u", "temperature", "top_p", "min_p", "top_k", "token", "prob")])
-
-
 def mq_kv_page_bytes(kv_type: str, n_kv_heads: int, page_size: int, head_dim: int) -> int:
     """Bytes of one cache page (0 on a bad shape)."""
     return lib().mq_kv_page_bytes(KV_TYPES[kv_type], n_kv_heads, page_size, head_dim)
@@ -812,70 +783,43 @@ class MQKVCache:
             raise ValueError("pages must not overlap")
         self._struct = _KVStruct(KV_TYPES[kv_type], n_pages, page_size, n_kv_heads, head_dim,
                                  k.data_ptr(), v.data_ptr(), stride)
-        self._ref = ctypes.byref(self._struct)
+        self._address = ctypes.addressof(self._struct)
 
 
-_torch = None
+_calls = None
 
 
-def _bind_torch():
-    """torch, imported once: an import statement in every call of the functions below would cost more
-    than their checks."""
-    global _torch
-    import torch
-    _torch = torch
-    return torch
-
-
-def _launch_stream(stream, index: int) -> int:
-    """The stream of a launch on cuda:`index`, which must be the current device."""
-    c = _torch._C
-    if c._cuda_getDevice() != index:
-        raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
-    return c._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+def _bind():
+    """The compiled calls (csrc/binding.cpp), loaded at the first use of the functions below."""
+    global _calls
+    import torch  # noqa: F401  (its libraries must be loaded first)
+    from importlib.machinery import ExtensionFileLoader
+    from importlib.util import module_from_spec, spec_from_file_location
+    L = lib()
+    if not os.path.exists(_BINDING):
+        raise FileNotFoundError(f"{_BINDING} is missing: run build()")
+    spec = spec_from_file_location("mq_binding", _BINDING, loader=ExtensionFileLoader("mq_binding", _BINDING))
+    m = module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.setup(*(ctypes.cast(f, ctypes.c_void_p).value
+              for f in (L.mq_rope_append, L.mq_attn_decode, L.mq_sample, L.mq_q8_bytes)), MQError, _bad_tensor)
+    _calls = m
+    return m
 
 
 def _made(like, shape, dtype, stream):
     """A tensor for a launch's output: from the memory of the stream that writes it."""
+    import torch
     if stream is None:
-        return _torch.empty(shape, dtype=dtype, device=like.device)
-    with _torch.cuda.stream(stream):
-        return _torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _bad_tensor(t, shape, dtype, index, what):
-    if t.dtype is not dtype or t.get_device() != index:
-        raise TypeError(f"{what}: expected {dtype} on cuda:{index}, got {t.dtype} on {t.device}")
+def _bad_tensor(t, shape, dtype, index, what, is_shape):
+    if not is_shape:
+        raise TypeError(f"{what}: expected torch.{dtype} on cuda:{index}, got {t.dtype} on {t.device}")
     raise ValueError(f"{what}: expected {shape}, got {tuple(t.shape)} with strides {t.stride()}")
-
-
-def _rows(t, nt, cols, dtype, index, what):
-    """The address of a [nt, cols] CUDA tensor whose rows are contiguous, and its row stride."""
-    if t.dtype is not dtype or t.get_device() != index or t.shape != (nt, cols):
-        _bad_tensor(t, f"[{nt}, {cols}] with contiguous rows", dtype, index, what)
-    if t.is_contiguous():
-        return t.data_ptr(), cols
-    if cols > 1 and t.stride(1) != 1:
-        _bad_tensor(t, f"[{nt}, {cols}] with contiguous rows", dtype, index, what)
-    return t.data_ptr(), t.stride(0)
-
-
-def _vec(t, n, dtype, index, what):
-    """The address of a contiguous CUDA tensor of n values; None for None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.numel() != n or t.get_device() != index or not t.is_contiguous():
-        _bad_tensor(t, f"{n} contiguous values", dtype, index, what)
-    return t.data_ptr()
-
-
-def _page_table(pages, nt, seq):
-    if pages.dim() != 2:
-        raise ValueError("pages: expected [sequences, pages per sequence]")
-    n_seqs, per_seq = pages.shape
-    if seq is None and n_seqs < nt:
-        raise ValueError(f"pages: {nt} rows but {n_seqs} sequences")
-    return n_seqs, per_seq
 
 
 def mq_rope_table(freqs, device=None):
@@ -900,32 +844,11 @@ def mq_rope_append(kv: MQKVCache, q, k, v, positions, pages, q_out=None, rope=No
     row (row t is sequence t when None); rope: mq_rope_table's steps (None:
     no rotation); style: "half" or "pairs"; status: int32 [1], gets 1 OR-ed
     in when a row names no valid page."""
-    torch = _torch or _bind_torch()
-    f32, i32 = torch.float32, torch.int32
-    dev, d, hkv = kv.device_index, kv.head_dim, kv.n_kv_heads
-    st = _launch_stream(stream, dev)
-    nt, nq = q.shape
     if q_out is None:
-        q_out = _made(q, q.shape, f32, stream)
-    n_seqs, per_seq = _page_table(pages, nt, seq)
-    if nq % d != 0:
-        raise ValueError(f"q: {nq} columns are no whole heads of {d}")
-    half, nk = 0 if rope is None else rope.numel(), hkv * d
-    qp, qs = _rows(q, nt, nq, f32, dev, "q")
-    kp, ks = _rows(k, nt, nk, f32, dev, "k")
-    vp, vs = _rows(v, nt, nk, f32, dev, "v")
-    op, os_ = _rows(q_out, nt, nq, f32, dev, "q_out")
-    args = _RopeAppendStruct(
-        nt, nq // d, 2 * half, ROPE_STYLES[style], eps, qp, kp, vp, qs, ks, vs, op, os_,
-        _vec(q_bias, nq, f32, dev, "q_bias"), _vec(k_bias, nk, f32, dev, "k_bias"),
-        _vec(v_bias, nk, f32, dev, "v_bias"), _vec(q_gain, d, f32, dev, "q_gain"),
-        _vec(k_gain, d, f32, dev, "k_gain"), _vec(rope, half, torch.int64, dev, "rope"),
-        _vec(positions, nt, i32, dev, "positions"), _vec(seq, nt, i32, dev, "seq"),
-        _vec(pages, n_seqs * per_seq, i32, dev, "pages"), n_seqs, per_seq, _vec(status, 1, i32, dev, "status"))
-    err = _lib.mq_rope_append(kv._ref, ctypes.byref(args), st)
-    if err:
-        raise MQError(err, "mq_rope_append")
-    return q_out
+        q_out = _made(q, q.shape, q.dtype, stream)
+    return (_calls or _bind()).rope_append(
+        kv._address, kv.device_index, q, k, v, positions, pages, q_out, rope, ROPE_STYLES[style], q_bias, k_bias,
+        v_bias, q_gain, k_gain, eps, seq, status, None if stream is None else stream.cuda_stream)
 
 
 def mq_attn_workspace_bytes(kv: MQKVCache, n_heads: int, nt: int, max_len: int) -> int:
@@ -933,7 +856,7 @@ def mq_attn_workspace_bytes(kv: MQKVCache, n_heads: int, nt: int, max_len: int) 
     needed, or a bad shape)."""
     if max_len > MQ_ATTN_MAX_LEN:  # before it becomes a C integer
         return 0
-    return lib().mq_attn_workspace_bytes(kv._ref, n_heads, nt, max_len)
+    return lib().mq_attn_workspace_bytes(kv._address, n_heads, nt, max_len)
 
 
 def mq_attn_workspace(kv: MQKVCache, n_heads: int, nt: int, max_len: int):
@@ -954,39 +877,18 @@ def mq_attn_decode(kv: MQKVCache, q, lens, pages, scale: float, out=None, q8=Non
     mq_rope_append; max_len: no row is longer (None: what the page table
     holds); q8: a uint8 tensor that gets nt q8 planes of out; ws: from
     mq_attn_workspace (made for this call when None and one is needed)."""
-    torch = _torch or _bind_torch()
-    f32, i32 = torch.float32, torch.int32
-    dev, d = kv.device_index, kv.head_dim
-    st = _launch_stream(stream, dev)
-    nt, nq = q.shape
     if out is None:
-        out = _made(q, q.shape, f32, stream)
-    n_seqs, per_seq = _page_table(pages, nt, seq)
-    if nq % d != 0:
-        raise ValueError(f"q: {nq} columns are no whole heads of {d}")
-    if max_len is None:
-        max_len = per_seq * kv.page_size
-    if max_len > MQ_ATTN_MAX_LEN or not 0 <= window < 2 ** 31:  # before they become C integers
-        raise MQError(MQ_ERR_SHAPE, "mq_attn_decode")
-    if q8 is not None:
-        _vec(q8, q8.numel(), torch.uint8, dev, "q8")
-        if q8.numel() < nt * mq_q8_bytes(nq):
-            raise ValueError(f"q8: smaller than {nt} planes of {nq} values")
-    if ws is None and mq_attn_workspace_bytes(kv, nq // d, nt, max_len):
-        with torch.cuda.stream(stream):  # zeroed, used and freed in the launch's order (None: the current stream)
-            ws = mq_attn_workspace(kv, nq // d, nt, max_len)
-    wsb = 0 if ws is None else ws.numel()
-    qp, qs = _rows(q, nt, nq, f32, dev, "q")
-    op, os_ = _rows(out, nt, nq, f32, dev, "out")
-    args = _AttnStruct(
-        nt, nq // d, max_len, window, scale, softcap, qp, op, qs, os_,
-        None if q8 is None else q8.data_ptr(), _vec(lens, nt, i32, dev, "lens"), _vec(seq, nt, i32, dev, "seq"),
-        _vec(pages, n_seqs * per_seq, i32, dev, "pages"), n_seqs, per_seq, _vec(ws, wsb, torch.uint8, dev, "ws"), wsb,
-        _vec(status, 1, i32, dev, "status"))
-    err = _lib.mq_attn_decode(kv._ref, ctypes.byref(args), st)
-    if err:
-        raise MQError(err, "mq_attn_decode")
-    return out
+        out = _made(q, q.shape, q.dtype, stream)
+    if ws is None:
+        nt, nq = q.shape
+        most = pages.shape[-1] * kv.page_size if max_len is None else max_len
+        if mq_attn_workspace_bytes(kv, nq // kv.head_dim, nt, most):
+            import torch
+            with torch.cuda.stream(stream):  # zeroed, used and freed in the launch's order (None: the current stream)
+                ws = mq_attn_workspace(kv, nq // kv.head_dim, nt, most)
+    return (_calls or _bind()).attn_decode(
+        kv._address, kv.device_index, q, lens, pages, scale, out, q8, ws, softcap, window, max_len, seq, status,
+        None if stream is None else stream.cuda_stream)
 
 
 def mq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, token=None, prob=None,
@@ -998,19 +900,8 @@ def mq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     filter out (temperature 1).  temperature 0 is the most likely token.
     prob: an f32 tensor [nt] that gets the token's probability among those
     kept.  A row without a finite logit gives -1."""
-    torch = _torch or _bind_torch()
-    f32, i32 = torch.float32, torch.int32
-    dev = logits.get_device()
-    st = _launch_stream(stream, dev)
-    nt, vocab = logits.shape
     if token is None:
-        token = _made(logits, (nt,), i32, stream)
-    lp, ls = _rows(logits, nt, vocab, f32, dev, "logits")
-    args = _SampleStruct(
-        nt, vocab, lp, ls, _vec(u, nt, f32, dev, "u"), _vec(temperature, nt, f32, dev, "temperature"),
-        _vec(top_p, nt, f32, dev, "top_p"), _vec(min_p, nt, f32, dev, "min_p"), _vec(top_k, nt, i32, dev, "top_k"),
-        _vec(token, nt, i32, dev, "token"), _vec(prob, nt, f32, dev, "prob"))
-    err = (_lib or lib()).mq_sample(ctypes.byref(args), st)
-    if err:
-        raise MQError(err, "mq_sample")
-    return token
+        import torch
+        token = _made(logits, logits.shape[:1], torch.int32, stream)
+    return (_calls or _bind()).sample(logits, u, temperature, top_k, top_p, min_p, token, prob,
+                                      None if stream is None else stream.cuda_stream)

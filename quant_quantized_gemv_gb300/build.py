@@ -4,13 +4,17 @@ nvcc compiles every translation unit of csrc/ in parallel (one -gencode,
 sm_103a only, no fast-math so that the producers' IEEE division, reciprocal
 and rounding match the definition), then links a shared library against the
 shared CUDA runtime.  Output: quant_quantized_gemv_gb300/_build/libmq.so.
+Beside it _build/mq_binding.so, a Python module over torch's headers, with the
+calls of the operators that name many tensors (csrc/binding.cpp).
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+from importlib.util import find_spec
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 SO = os.path.join(BUILD, "libmq.so")
+BINDING = os.path.join(BUILD, "mq_binding.so")
 SOURCES = ["gemv.cu", "gemv_batch.cu", "gemv_gateup.cu", "gemv_f32.cu", "producers.cu", "noalloc.cu",
            "readfloor.cu", "copy.cu", "repack_device.cu", "rope_append.cu", "attn_decode.cu", "sample.cu",
            "api.cpp", "repack.cpp", "decode.cpp"]
@@ -29,10 +34,14 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else (shutil.which("nvcc") or "nvcc")
 
 
+def _torch() -> str:
+    return find_spec("torch").submodule_search_locations[0]
+
+
 def _stale() -> bool:
-    if not os.path.exists(SO):
+    if not os.path.exists(SO) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(SO)
+    t = min(os.path.getmtime(SO), os.path.getmtime(BINDING))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "mq.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -42,12 +51,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return SO
     os.makedirs(BUILD, exist_ok=True)
     common = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
+    torch = _torch()
+    headers = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, src + ".o")
         cmd = [nvcc(), *common, "-c", os.path.join(CSRC, src), "-o", obj]
         if src.endswith(".cu"):
             cmd[1:1] = [*ARCH, "-lineinfo", "-Xptxas", "-v" if verbose else "-O3"]
+        if src == "binding.cpp":
+            cmd[1:1] = [x for h in headers for x in ("-I", h)]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
@@ -55,14 +69,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
-    tmp = SO + f".{os.getpid()}.tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, SO)
+    def link(so: str, objs: list, libs: list):
+        tmp = so + f".{os.getpid()}.tmp"
+        cmd = [nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs, *libs]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, so)
+
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        *objs, binding = ex.map(compile_one, SOURCES + ["binding.cpp"])
+    link(SO, objs, [])
+    lib = os.path.join(torch, "lib")
+    link(BINDING, [binding], ["-L", lib, "-Xlinker", "-rpath", "-Xlinker", lib, "-ltorch_python", "-ltorch_cpu",
+                              "-lc10_cuda", "-lc10"])
     return SO
 
 

@@ -10,6 +10,36 @@ NO_GPU = pytest.mark.skipif(__import__("torch").cuda.is_available(),
                             reason="fake device pointers are only passed where no GPU exists")
 
 
+class RopeAppend(ctypes.Structure):
+    """mq_rope_append_args of include/mq.h"""
+    _fields_ = ([(n, ctypes.c_int) for n in ("nt", "n_heads", "rope_dims", "rope_style")]
+                + [("eps", ctypes.c_float)]
+                + [(n, ctypes.c_void_p) for n in ("q", "k", "v")]
+                + [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "v_stride")]
+                + [("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("q_bias", "k_bias", "v_bias", "q_gain", "k_gain",
+                                                  "rope_table", "positions", "seq", "pages")]
+                + [("n_seqs", ctypes.c_int), ("pages_stride", ctypes.c_int), ("status", ctypes.c_void_p)])
+
+
+class Attn(ctypes.Structure):
+    """mq_attn_args of include/mq.h"""
+    _fields_ = ([(n, ctypes.c_int) for n in ("nt", "n_heads", "max_len", "window")]
+                + [(n, ctypes.c_float) for n in ("scale", "softcap")]
+                + [("q", ctypes.c_void_p), ("out", ctypes.c_void_p)]
+                + [("q_stride", ctypes.c_longlong), ("out_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("q8", "lens", "seq", "pages")]
+                + [("n_seqs", ctypes.c_int), ("pages_stride", ctypes.c_int)]
+                + [("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p)])
+
+
+class Sample(ctypes.Structure):
+    """mq_sample_args of include/mq.h"""
+    _fields_ = ([("nt", ctypes.c_int), ("vocab", ctypes.c_int), ("logits", ctypes.c_void_p),
+                 ("stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("u", "temperature", "top_p", "min_p", "top_k", "token", "prob")])
+
+
 @pytest.fixture(scope="module")
 def mq():
     from quant_quantized_gemv_gb300 import build
@@ -93,7 +123,7 @@ def append_args(mq, **kw):
              q_stride=512, k_stride=256, v_stride=256, q_out=0x60000, q_out_stride=512, rope_table=0x70000,
              positions=0x80000, pages=0x90000, n_seqs=1, pages_stride=4)
     a.update(kw)
-    return mq._RopeAppendStruct(**a)
+    return RopeAppend(**a)
 
 
 @NO_GPU
@@ -134,7 +164,7 @@ def attn_args(mq, **kw):
              q_stride=512, out_stride=512, lens=0x50000, pages=0x60000, n_seqs=1, pages_stride=64, ws=0x70000,
              ws_bytes=1 << 30)
     a.update(kw)
-    return mq._AttnStruct(**a)
+    return Attn(**a)
 
 
 @NO_GPU
@@ -180,13 +210,47 @@ def test_attention_refuses_null_structs(mq):
 def test_sample_refuses_bad_arguments(mq, bad, status):
     a = dict(nt=1, vocab=100, logits=0x10000, stride=100, u=0x20000, token=0x30000)
     a.update(bad)
-    st = mq.lib().mq_sample(ctypes.byref(mq._SampleStruct(**a)), None)
+    st = mq.lib().mq_sample(ctypes.byref(Sample(**a)), None)
     assert st == getattr(mq, "MQ_ERR_" + status)
 
 
 @NO_GPU
 def test_sample_refuses_null_arguments(mq):
     assert mq.lib().mq_sample(None, None) == mq.MQ_ERR_NULL
+
+
+class Described:
+    """What the calls read of a cache, without one on a GPU."""
+
+    def __init__(self, mq):
+        self._struct = cache(mq)
+        self._address, self.device_index, self.page_size, self.head_dim = ctypes.addressof(self._struct), 0, 16, 128
+
+
+def test_calls_refuse_what_is_no_cuda_tensor(mq):
+    """Without a launch: the checks of the compiled calls, up to the first that fails."""
+    import torch
+    x = torch.zeros(2, 100)
+    for bad in (x, x[0], 3, None, "x", x.to_sparse(), x.double()):
+        with pytest.raises(TypeError):
+            mq.mq_sample(bad, x[:, 0], token=x)
+    b = mq._calls
+    for f in (b.rope_append, b.attn_decode, b.sample, b.setup):
+        with pytest.raises(TypeError):
+            f(1, 2)
+        with pytest.raises(TypeError):
+            f()
+
+
+@pytest.mark.skipif(__import__("torch").cuda.is_available(), reason="there is a current device")
+def test_calls_without_a_device_raise(mq):
+    """The device's own error, as an exception."""
+    import torch
+    kv, x, i = Described(mq), torch.zeros(1, 512), torch.zeros(1, 1, dtype=torch.int32)
+    with pytest.raises((RuntimeError, ValueError, TypeError)):
+        mq.mq_rope_append(kv, x, x, x, i[0], i)
+    with pytest.raises((RuntimeError, ValueError, TypeError)):
+        mq.mq_attn_decode(kv, x, i[0], i, 0.1, ws=x)
 
 
 # the references against what they can be checked with on paper
