@@ -6,6 +6,11 @@
 // into shared memory, and everything after that happens there and in the
 // cluster's distributed shared memory: one launch, no workspace, no sort of
 // the vocabulary.
+//   0. a short top-k (up to 48 with 16 CTAs a row, 96 with 8, 192, then 256): every CTA
+//      sends the first top_k tokens of its slice, by bins as in 2, to rank 0, which
+//      narrows them to few more than top_k, applies every filter and draws: one
+//      exchange instead of four (one row of 152064, top-k 40: 12.6 -> 10.5 us). What does
+//      not fit its room (long ties) goes on with
 //   1. the row's maximum;
 //   2. if top-k or top-p is on: the tokens are counted in bins of
 //      (max - logit) / temperature, 64 to a factor of two, and the bins summed
@@ -66,6 +71,9 @@ constexpr int kGroups = 64;      // groups of as many bins
 constexpr float kBinsPerOctave = 64.0f;
 constexpr int kList = 512;       // tokens that rank 0 ranks at once
 constexpr int kMine = 1024;      // tokens that a CTA sets aside
+constexpr int kSent = 1024;      // tokens that rank 0 chooses from, in equal rooms for the CTAs
+constexpr int kMostSmall = 256;  // the largest top-k that is chosen so
+constexpr int kFew = 128;        // tokens that rank 0 ranks without narrowing them first
 constexpr int kMaxCluster = 16;  // CTAs of a row (over 8: the non-portable size)
 constexpr int kFixBits = 42;     // a weight of 1 is 2^42
 constexpr int kWindow = 25;      // bins whose weights are summed one by one
@@ -99,10 +107,11 @@ struct alignas(16) Shared {
     u64 group_w[kGroups], groups_w[kGroups];     // estimated weights of the groups: this CTA's, the row's
     unsigned group_n[kGroups], groups_n[kGroups];
     unsigned bins_n[kGroups];                    // the row's bins of one group
+    u64 sent[kSent];                             // rank 0: every CTA's first tokens
     u64 octave[64];                              // 2^30 2^(-b / 64)
     u64 warp_sums[kThreads / 32];
     float maxes[kMaxCluster];
-    int argmax[kMaxCluster];
+    int argmax[kMaxCluster], sent_n[kMaxCluster];
     u64 totals[kMaxCluster];
     u64 boundary, narrow_left;
     unsigned list_n, mine_n, at, at_n, narrow_n, narrow_digit;
@@ -294,16 +303,234 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
         xs[tid] = clean(p >= lo && p < hi ? __ldcg(src + p) : -INFINITY);
     }
 
-    // the row's maximum
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     if (lane == 0) sh.warp_sums[warp] = __float_as_uint(mx);
     __syncthreads();
+    float own = -INFINITY;  // this CTA's maximum
+    for (int w = 0; w < kThreads / 32; ++w) own = fmaxf(own, __uint_as_float((unsigned)sh.warp_sums[w]));
     cluster.barrier_wait(std::move(started));  // every CTA of the row runs
-    if (tid < ranks) {
-        float m = -INFINITY;
-        for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, __uint_as_float((unsigned)sh.warp_sums[w]));
-        cluster.map_shared_rank(&sh, tid)->maxes[rank] = m;
+    const bool single = !(temperature > 0.0f) || top_k == 1 || top_p <= 0.0f || min_p > 1.0f;  // one token is kept
+
+    // log2(e) / temperature in two parts: the quotient, and what its product leaves
+    Weight weight;
+    weight.c_hi = fminf(1.44269502f / temperature, 1e30f);
+    weight.c_lo = (fmaf(-weight.c_hi, temperature, 1.44269502f) + 1.92596299e-8f) / temperature;
+    if (!(fabsf(weight.c_lo) < weight.c_hi)) weight.c_lo = 0.0f;  // clamped, or an infinite temperature
+    const u64 floor_w = min_p > 0.0f ? __float2ull_ru(min_p * (float)(1ull << kFixBits)) : 0;
+    const bool by_count = top_k > 0 && top_k < a.vocab, by_weight = top_p < 1.0f;
+    const int first = tid * a.seg;  // this thread's values, in the order of the vocabulary
+    auto index_of = [&](int i) { return base + i - shift; };
+    auto place = [&](int i) { return place_of(xs[i], index_of(i)); };
+    // a share s < 1 of a sum: its floor, by the 64 bits behind the point
+    auto share_of = [](float s, u64 all, bool up) {
+        const u64 f = __float2ull_rz(s * 18446744073709551616.0f);
+        return __umul64hi(f, all) + (up && f * all != 0 ? 1 : 0);
+    };
+    auto drawn_at = [&](u64 all) { return u > 0.0f ? (u < 1.0f ? share_of(u, all, false) : all - 1) : 0; };
+    auto wanted = [&](u64 all) { return max(share_of(top_p, all, true), (u64)1); };  // top-p of a sum
+    auto share_f32 = [](u64 w, u64 all) {  // w / all: the quotient and one correction
+        const float wh = __ull2float_rn(w), ah = __ull2float_rn(all);
+        const float wl = __ll2float_rn((long long)(w - __float2ull_rn(wh)));
+        const float al = __ll2float_rn((long long)(all - __float2ull_rn(ah)));
+        const float q = wh / ah;
+        return q + ((fmaf(-q, ah, wh) + wl) - q * al) / ah;
+    };
+
+    // Ranks the tokens [from, to) of a list of n.  body(i, tokens before i, weights before i) runs in
+    // one thread for each of them; several threads share the comparisons of one token.
+    auto rank_list = [&](int n, int from, int to, auto &&body) {
+        for (int i = tid; i < n; i += kThreads) sh.weight[i] = weight(logit_of((unsigned)(sh.list[i] >> 32)));
+        __syncthreads();
+        int by = 1;
+        while (by < 32 && (to - from) * by * 2 <= kThreads) by *= 2;
+        const int i = from + tid / by, sub = tid & (by - 1);
+        int before = 0;
+        u64 w_before = 0;
+        if (i < to) {
+            const u64 p = sh.list[i];
+            for (int j = sub; j < n; j += by)
+                if (sh.list[j] > p) ++before, w_before += sh.weight[j];
+        }
+        for (int o = 1; o < by; o <<= 1) {
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+            w_before += __shfl_xor_sync(0xffffffffu, w_before, o);
+        }
+        if (i < to && sub == 0) body(i, before, w_before);
+    };
+    // The draw from a list in rank 0 that holds whatever top-k may keep.
+    auto draw_from_list = [&](int n) {
+        bool in = false;
+        int my_i = 0;
+        u64 my_w = 0, my_before = 0, all;
+        rank_list(n, 0, n, [&](int i, int before_i, u64 w_before) {
+            in = before_i < top_k;
+            my_i = i, my_before = w_before;
+            my_w = in ? sh.weight[i] : 0;
+        });
+        if (by_weight) {
+            block_scan(my_w, sh.warp_sums, &all);
+            in = in && my_before < wanted(all);
+        }
+        in = in && my_w >= floor_w && my_w > 0;
+        const u64 kept_w = in ? my_w : 0;
+        block_scan(kept_w, sh.warp_sums, &all);
+        // in the order of the vocabulary: what is kept before each token
+        if (tid < n) sh.weight[tid] = 0;
+        __syncthreads();
+        if (in) sh.weight[my_i] = kept_w;
+        __syncthreads();
+        const u64 target = drawn_at(all);
+        if (in) {
+            const unsigned mine_low = (unsigned)sh.list[my_i];
+            u64 sum = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j)
+                if ((unsigned)sh.list[j] > mine_low) sum += sh.weight[j];  // a lower index
+            if (sum <= target && target < sum + kept_w) {
+                a.token[row] = (int)~mine_low;
+                if (a.prob) a.prob[row] = share_f32(kept_w, all);
+            }
+        }
+    };
+
+    // A short top-k: every CTA sends its own first top_k tokens, and all of their bin, to rank 0, which
+    // chooses and draws. The others leave after one barrier. (Infinities and long ties: below.)
+    const int room = kSent / ranks;  // a power of two
+    if (!single && by_count && top_k <= min(room / 4 * 3, kMostSmall)) {
+        int sent = 0;
+        if (own == INFINITY) sent = kSent + 1;
+        else if (own != -INFINITY) {
+            weight.top = own;
+#pragma unroll 2
+            for (int i = tid * 2; i < a.seg * kThreads; i += 2 * kThreads) {
+                const float2 x = *reinterpret_cast<const float2 *>(xs + i);
+                int b0, b1;
+                weight.bins(x.x, x.y, b0, b1);
+                if (x.x != -INFINITY) atomicAdd(&sh.cnt[b0], 1u);
+                if (x.y != -INFINITY) atomicAdd(&sh.cnt[b1], 1u);
+            }
+            __syncthreads();
+            unsigned n = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) n += sh.cnt[(tid >> 3) * 64 + j * 8 + (tid & 7)];
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            if ((tid & 7) == 0) sh.group_n[tid >> 3] = n;
+            __syncthreads();
+            u64 before, all, in_group;
+            const int group = reach(sh.group_n[2 * lane], sh.group_n[2 * lane + 1], (u64)top_k, &before, &all);
+            int last_bin = kBins - 1;
+            sent = (int)all;
+            if (all > (u64)top_k) {
+                const unsigned *bins = sh.cnt + group * 64;
+                const int at = reach(bins[2 * lane], bins[2 * lane + 1], (u64)top_k - before, &in_group, &all);
+                last_bin = group * 64 + at;
+                sent = (int)(before + in_group) + (int)bins[at];
+            }
+            if (sent <= room) {
+                u64 *to = root.sent + rank * room;
+                auto look = [&](float x, int b, int i) {
+                    if (b <= last_bin && x != -INFINITY) to[atomicAdd(&sh.mine_n, 1u)] = place(i);
+                };
+#pragma unroll 2
+                for (int i = tid * 2; i < a.seg * kThreads; i += 2 * kThreads) {
+                    const float2 x = *reinterpret_cast<const float2 *>(xs + i);
+                    int b0, b1;
+                    weight.bins(x.x, x.y, b0, b1);
+                    look(x.x, b0, i);
+                    look(x.y, b1, i + 1);
+                }
+            }
+        }
+        if (tid < ranks) {
+            Shared &o = *cluster.map_shared_rank(&sh, tid);
+            o.sent_n[rank] = sent;
+            o.maxes[rank] = own;
+        }
+        cluster.sync();
+        int total = 0;
+        bool fits = true;
+        float top = -INFINITY;
+        for (int r = 0; r < ranks; ++r) {
+            fits = fits && sh.sent_n[r] <= room;
+            total += sh.sent_n[r];
+            top = fmaxf(top, sh.maxes[r]);
+        }
+        if (fits) {
+            if (rank != 0) return;
+            if (total == 0) {  // nothing to draw from
+                if (tid == 0) {
+                    a.token[row] = -1;
+                    if (a.prob) a.prob[row] = 0.0f;
+                }
+                return;
+            }
+            weight.top = top;
+            if (tid == 0) sh.mine_n = 0;
+            static_assert(kSent == 2 * kThreads, "two tokens a thread");
+            u64 p[2];
+            int coarse[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int e = tid + j * kThreads;
+                p[j] = (e & (room - 1)) < sh.sent_n[e / room] ? sh.sent[e] : 0;
+                coarse[j] = weight.bin(logit_of((unsigned)(p[j] >> 32))) / (kBins / kDigits);
+            }
+            // To few: by the coarse bin of the last token kept, then by its place in it, 8 bits at a time.
+            const int few = max(kFew, top_k);
+            int last_coarse = kDigits - 1, bits = -8, kept = total, left = top_k;
+            u64 prefix = 0;
+            for (; kept > few && bits < 64; bits += 8) {
+                __syncthreads();
+                if (tid < kDigits) sh.digit_n[tid] = 0;
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (!p[j] || (bits >= 0 && (coarse[j] != last_coarse || (bits > 0 && p[j] >> (64 - bits) != prefix)))) continue;
+                    const int digit = bits < 0 ? coarse[j] : kDigits - 1 - ((int)(p[j] >> (56 - bits)) & (kDigits - 1));
+                    atomicAdd(&sh.digit_n[digit], 1u);
+                }
+                __syncthreads();
+                unsigned n[8], sum = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum += n[j] = sh.digit_n[8 * lane + j];
+                unsigned to = sum;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned t = __shfl_up_sync(0xffffffffu, to, o);
+                    if (lane >= o) to += t;
+                }
+                const int at = __ffs(__ballot_sync(0xffffffffu, to >= (unsigned)left)) - 1;  // left <= the sum of all
+                int digit = 8 * lane, before = (int)(to - sum), here = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (here == 0) {
+                        if (before + (int)n[j] >= left) here = (int)n[j], digit += j;
+                        else before += (int)n[j];
+                    }
+                digit = __shfl_sync(0xffffffffu, digit, at);
+                before = __shfl_sync(0xffffffffu, before, at);
+                here = __shfl_sync(0xffffffffu, here, at);
+                left -= before;
+                kept = top_k - left + here;
+                if (bits < 0) last_coarse = digit;
+                else prefix = prefix << 8 | (u64)(kDigits - 1 - digit);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (p[j] && (coarse[j] < last_coarse || (coarse[j] == last_coarse && (bits <= 0 || p[j] >> (64 - bits) >= prefix))))
+                    sh.list[atomicAdd(&sh.mine_n, 1u)] = p[j];
+            __syncthreads();
+            draw_from_list((int)sh.mine_n);
+            return;
+        }
+        // the long way begins again
+        for (int i = tid; i < kBins; i += kThreads) sh.cnt[i] = 0;
     }
+
+    // the row's maximum
+    if (tid < ranks) cluster.map_shared_rank(&sh, tid)->maxes[rank] = own;
     cluster.sync();
     mx = sh.maxes[0];
     for (int r = 1; r < ranks; ++r) mx = fmaxf(mx, sh.maxes[r]);
@@ -315,8 +542,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
         }
         return;
     }
-    if (!(temperature > 0.0f) || top_k == 1 || top_p <= 0.0f || min_p > 1.0f) {
-        // one token is kept: the lowest index of the largest logit
+    if (single) {  // the lowest index of the largest logit
         int best = 0x7fffffff;
         for (int i = tid; i < a.slice; i += kThreads)
             if (xs[i] == mx) {
@@ -345,31 +571,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
         __syncthreads();
     }
 
-    // log2(e) / temperature in two parts: the quotient, and what its product leaves
-    Weight weight;
     weight.top = mx;
-    weight.c_hi = fminf(1.44269502f / temperature, 1e30f);
-    weight.c_lo = (fmaf(-weight.c_hi, temperature, 1.44269502f) + 1.92596299e-8f) / temperature;
-    if (!(fabsf(weight.c_lo) < weight.c_hi)) weight.c_lo = 0.0f;  // clamped, or an infinite temperature
-    const u64 floor_w = min_p > 0.0f ? __float2ull_ru(min_p * (float)(1ull << kFixBits)) : 0;
-    const bool by_count = top_k > 0 && top_k < a.vocab, by_weight = top_p < 1.0f;
-    const int first = tid * a.seg;  // this thread's values, in the order of the vocabulary
-    auto index_of = [&](int i) { return base + i - shift; };
-    auto place = [&](int i) { return place_of(xs[i], index_of(i)); };
-    // a share s < 1 of a sum: its floor, by the 64 bits behind the point
-    auto share_of = [](float s, u64 all, bool up) {
-        const u64 f = __float2ull_rz(s * 18446744073709551616.0f);
-        return __umul64hi(f, all) + (up && f * all != 0 ? 1 : 0);
-    };
-    auto drawn_at = [&](u64 all) { return u > 0.0f ? (u < 1.0f ? share_of(u, all, false) : all - 1) : 0; };
-    auto wanted = [&](u64 all) { return max(share_of(top_p, all, true), (u64)1); };  // top-p of a sum
-    auto share_f32 = [](u64 w, u64 all) {  // w / all: the quotient and one correction
-        const float wh = __ull2float_rn(w), ah = __ull2float_rn(all);
-        const float wl = __ll2float_rn((long long)(w - __float2ull_rn(wh)));
-        const float al = __ll2float_rn((long long)(all - __float2ull_rn(ah)));
-        const float q = wh / ah;
-        return q + ((fmaf(-q, ah, wh) + wl) - q * al) / ah;
-    };
 
     // The filters' last token: logit and index (no filter: every finite logit passes).
     float last_x = -INFINITY;
@@ -421,27 +623,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
         cluster.sync();
     };
     static_assert(kList <= kThreads, "one token a thread");
-    // Ranks the tokens [from, to) of a list of n.  body(i, tokens before i, weights before i) runs in
-    // one thread for each of them; several threads share the comparisons of one token.
-    auto rank_list = [&](int n, int from, int to, auto &&body) {
-        for (int i = tid; i < n; i += kThreads) sh.weight[i] = weight(logit_of((unsigned)(sh.list[i] >> 32)));
-        __syncthreads();
-        int by = 1;
-        while (by < 32 && (to - from) * by * 2 <= kThreads) by *= 2;
-        const int i = from + tid / by, sub = tid & (by - 1);
-        int before = 0;
-        u64 w_before = 0;
-        if (i < to) {
-            const u64 p = sh.list[i];
-            for (int j = sub; j < n; j += by)
-                if (sh.list[j] > p) ++before, w_before += sh.weight[j];
-        }
-        for (int o = 1; o < by; o <<= 1) {
-            before += __shfl_xor_sync(0xffffffffu, before, o);
-            w_before += __shfl_xor_sync(0xffffffffu, w_before, o);
-        }
-        if (i < to && sub == 0) body(i, before, w_before);
-    };
     // The last token of a list (in every CTA) whose order is followed until `left` counts or weights
     // are reached: the CTA that sent it finds it and tells the others.
     auto end_of_list = [&](int n, bool counts, u64 left) {
@@ -574,40 +755,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
                 if (cut_to <= kList) {
                     // everything that can be kept, in one list; rank 0 alone goes on
                     gather(0, cut_bin, 0, 0, false);
-                    if (rank != 0) return;
-                    const int n = min((int)sh.list_n, kList);
-                    bool in = false;
-                    int my_i = 0;
-                    u64 my_w = 0, my_before = 0, all;
-                    rank_list(n, 0, n, [&](int i, int before_i, u64 w_before) {
-                        in = before_i < top_k;
-                        my_i = i, my_before = w_before;
-                        my_w = in ? sh.weight[i] : 0;
-                    });
-                    if (by_weight) {
-                        block_scan(my_w, sh.warp_sums, &all);
-                        in = in && my_before < wanted(all);
-                    }
-                    in = in && my_w >= floor_w && my_w > 0;
-                    const u64 kept_w = in ? my_w : 0;
-                    block_scan(kept_w, sh.warp_sums, &all);
-                    // in the order of the vocabulary: what is kept before each token
-                    if (tid < n) sh.weight[tid] = 0;
-                    __syncthreads();
-                    if (in) sh.weight[my_i] = kept_w;
-                    __syncthreads();
-                    const u64 target = drawn_at(all);
-                    if (in) {
-                        const unsigned mine_low = (unsigned)sh.list[my_i];
-                        u64 sum = 0;
-#pragma unroll 4
-                        for (int j = 0; j < n; ++j)
-                            if ((unsigned)sh.list[j] > mine_low) sum += sh.weight[j];  // a lower index
-                        if (sum <= target && target < sum + kept_w) {
-                            a.token[row] = (int)~mine_low;
-                            if (a.prob) a.prob[row] = share_f32(kept_w, all);
-                        }
-                    }
+                    if (rank == 0) draw_from_list(min((int)sh.list_n, kList));
                     return;
                 }
                 // the estimate of what top-k keeps, while the bins are at hand
@@ -850,7 +998,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
 // more, or 8192 for the step to 16, whose barriers cost more.  Captured, us, top-k 40 + top-p / top-p
 // 0.9 of flat logits, C = 4, 8, 16: 152064 tokens, 1 row: -, 13.6 / 29.0, 13.0 / 23.0; 12 rows: -, 14.6 /
 // 29.6, 17.4 / 32.1; 50257 tokens, 1 row: 12.3 / 22.4, 11.2 / 18.4, 11.9 / 18.4; 64 rows: 16.8 / 32.5, 26.6 /
-// 50.6, 57 / 103.
+// 50.6, 57 / 103 (the top-k of these by step 3).
 int cluster_for(int nt, int vocab, int sms)
 {
     int c = 1;

@@ -284,3 +284,34 @@ def test_a_token_made_for_another_stream_is_of_its_memory(mq):
     token = mq.mq_sample(x, u, stream=st)
     st.synchronize()
     assert token.data_ptr() != given_back and token.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("kind", ["spread", "ties", "many ties", "near", "one place", "few finite", "infinite"])
+@pytest.mark.parametrize("v", [700, 4100, 9001, 20011, 152064])
+def test_short_top_k(mq, v, kind):
+    """Top-k small enough to be chosen from what each part of a row sends, up to and past its limits:
+    parts with nothing, ties within and across parts, fewer tokens than k."""
+    ks = [2, 3, 40, 47, 48, 49, 95, 96, 97, 191, 192, 193, 255, 256, 257, 300, 600, v - 1]
+    x, u = rows("short " + kind, len(ks), v)
+    g = synth.rng("short", kind, v)
+    if kind == "ties":                       # some 55 equal ones in every sixteenth, places differ alone
+        x[:, :: max(v // 880, 1)] = 20.0
+    elif kind == "many ties":                # more than any part may send
+        x[:, ::5] = 20.0
+    elif kind == "near":                     # the order lies in the last bits
+        at = g.choice(v, min(v, 800), replace=False)
+        x[:, at] = 20.0 + g.integers(0, 3, (len(ks), len(at))) * np.float32(2.0 ** -19)
+    elif kind == "one place":                # all of them in one part
+        x[:, v // 2:v // 2 + 300] += 30.0
+    elif kind == "few finite":
+        keep = g.choice(v, 37, replace=False)
+        y = np.full_like(x, -np.inf)
+        y[:, keep] = x[:, keep]
+        x = y
+    elif kind == "infinite":
+        x[:, g.choice(v, 3, replace=False)] = np.inf
+    for more in (dict(), dict(p=0.9, m=0.05, t=0.7)):
+        for a in range(0, len(ks), 6):       # 6 rows: the widest split of each
+            s = slice(a, a + 6)
+            check(x[s], u[s], run(mq, x[s], u[s], k=ks[s], **more), k=ks[s], **more)
+    check(x[:1], u[:1], run(mq, x[:1], u[:1], k=40, p=0.95), k=40, p=0.95)
