@@ -13,12 +13,13 @@
 // f32 product would be off by 2^-24 of the whole angle: 0.06 radian at
 // position 10^6.
 //
-// Layout: a lane holds EPL consecutive values of a head (4, or 8 above 128
-// values a head), so 16 lanes (head_dim <= 64) or 32 hold a head, loads and
-// f32 stores are float4, and the partner of a value under MQ_ROPE_HALF is
-// rope_dims / 2 values away in another lane at the same place (rope_dims a
-// multiple of 2 EPL): one shuffle per value.  A q8 block is 32 / EPL lanes: max
-// and codes as in the q8 producers.
+// Layout: a lane holds EPL consecutive values of a head, so 16 or 32 lanes hold
+// a head, loads and f32 stores are float4, and the partner of a value under
+// MQ_ROPE_HALF is rope_dims / 2 values away in another lane at the same place
+// (rope_dims a multiple of 2 EPL): one shuffle per value.  EPL is 4 (two heads a
+// warp up to 64 values, else one), or 8 (one head above 128 values; and two heads
+// of 65 to 128 where rows are many: less to do per value, but fewer warps).  A q8
+// block is 32 / EPL lanes: max and codes as in the q8 producers.
 //
 // Work: a row's heads, queries | keys | values, in groups of what a warp's lanes
 // hold, are shared by the CTAs of the row.  A CTA first writes down where each
@@ -26,13 +27,12 @@
 // way while one thread per pair computes an angle and the row's page is found,
 // which only the cache entries wait for.
 //
-// What bounds it: few rows, the launch and three dependent loads (2.9 us a call
-// in a captured chain).  Many rows, instructions and the latency of a CTA's
-// beginning, before HBM: 4096 rows of the 14B shape (40 + 8 + 8 heads of 128)
-// take 48 us, 4.5 TB/s, where their 218 MB take 33 (127 instructions a group with
-// 28 groups a CTA of 4 warps: 54 us; 56 groups, as here, spread the beginning
-// over twice as many; more loads in flight a lane cost registers, 8: 52 us; one
-// group a warp: 123 us).
+// What bounds it: few rows, the launch and three dependent loads (2.7 us a call
+// in a captured chain).  Many rows, the latency of a CTA's loads, one batch after
+// another, before HBM.  4096 rows of 40 + 8 + 8 heads of 128, 218 MB, which take 33
+// us: f16 38 us (5.7 TB/s), with biases 43, q8 with norms 45.  EPL 4: 40, 47 and
+// 55.  28 groups of EPL 4 a CTA: 45 instead of 40; biases fetched with the values
+// cost registers, so warps: 44 instead of 43; one group a warp: 66.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -47,7 +47,8 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4;
-constexpr int kUnits = 14;  // groups of heads a warp takes when there are many rows
+constexpr int kUnits = 14;  // groups of heads (of 4 values a lane) a warp takes when there are many rows
+constexpr int kResident = 9;  // CTAs an SM holds, by registers
 constexpr int kLoads = 4;  // float4 loads of a lane in flight
 constexpr int kMaxGroups = kWarps * kUnits;
 constexpr int kGridRows = 32768;  // rows along the grid's y
@@ -105,7 +106,7 @@ struct alignas(16) Group {
 };
 
 template <int EPL>
-__global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppendLaunch a)
+__global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(const RopeAppendLaunch a)
 {
     constexpr int kBatch = kLoads * 4 / EPL;  // groups a warp loads at a time
     __shared__ Group groups[kMaxGroups];
@@ -275,18 +276,24 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppe
 
 cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_t st)
 {
-    a.two_heads = a.head_dim <= 64 ? 1 : 0;
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
+    // 8 values a lane where the warps are enough all the same (40 + 8 + 8 heads of 128, EPL 4 and 8: 1 row 2.7
+    // and 3.0 us, 16 rows 3.3 and 3.3, 64 rows 4.6 and 3.9, 256 rows 5.2 and 6.0, 1024 rows 16.9 and 16.5,
+    // 4096 rows 47 and 43)
+    const long long heads = a.n_heads + 2 * a.n_kv_heads;
+    const bool wide = a.head_dim > 128 || (a.head_dim > 64 && a.rope_dims % 16 == 0 && a.nt * heads >= (long long)sms * 8);
+    a.two_heads = a.head_dim <= (wide ? 128 : 64) ? 1 : 0;
     const int groups = ((a.n_heads + a.two_heads) >> a.two_heads) + 2 * ((a.n_kv_heads + a.two_heads) >> a.two_heads);
-    // Few rows: a group a warp, for latency.  More: up to kUnits groups a warp, which share the
-    // row's angles and its page.
+    // Few rows: a group a warp, for latency.  More: up to kUnits groups a warp (as many values for 8 a lane),
+    // which share the row's angles and its page.
+    const int most = wide ? kUnits / 2 : kUnits;
     const long long wave = (long long)sms * 32;  // warps
     long long units = ((long long)a.nt * groups + wave - 1) / wave;
-    units = units < 1 ? 1 : units > kUnits ? kUnits : units;
-    a.groups_per_cta = (int)units * kWarps;
-    const int ctas = (groups + a.groups_per_cta - 1) / a.groups_per_cta;
+    units = units < 1 ? 1 : units > most ? most : units;
+    const int ctas = (groups + (int)units * kWarps - 1) / ((int)units * kWarps);
+    a.groups_per_cta = ((groups + ctas - 1) / ctas + kWarps - 1) / kWarps * kWarps;  // alike, whole warps' groups
     const dim3 grid((unsigned)ctas, (unsigned)std::min(a.nt, kGridRows), (unsigned)((a.nt + kGridRows - 1) / kGridRows));
-    const auto kernel = a.head_dim <= 128 ? rope_append_kernel<4> : rope_append_kernel<8>;
+    const auto kernel = wide ? rope_append_kernel<8> : rope_append_kernel<4>;
     return launch_maybe_pdl(kernel, grid, dim3(kWarps * 32), 0, pdl, st, a);
 }
 

@@ -129,6 +129,25 @@ def test_row_counts_and_groups(mq, nt, hq, hkv):
     c.check(*c.run(mq))
 
 
+@pytest.mark.parametrize("kv", ["f16", "bf16", "q8"])
+@pytest.mark.parametrize("hq,hkv", [(7, 1), (9, 3), (40, 8)])
+@pytest.mark.parametrize("d,r,style", [(128, 128, "half"), (128, 16, "half"), (128, 24, "half"), (128, 80, "pairs"),
+                                       (96, 96, "half"), (96, 64, "pairs"), (96, 0, "half")])
+def test_many_rows_two_heads_a_warp(mq, kv, hq, hkv, d, r, style):
+    """Heads of 65 to 128 values go two a warp when rows are many: odd counts, heads of 96 in 12 of 16
+    lanes, and rotations whose pairs do not lie whole lanes apart (24), which stay one a warp."""
+    nt = 1250 // (hq + 2 * hkv) + 9
+    c = Case(nt, hq, hkv, d, r, style, kv, 16, hkv != 8, True, [(i * 37) % 500 for i in range(nt)], pad=3)
+    c.check(*c.run(mq))
+
+
+def test_rows_of_many_heads(mq):
+    """More heads than a CTA's share of a row, in CTAs of equal shares."""
+    for nt, d in ((3, 128), (300, 128), (600, 64), (300, 256)):
+        c = Case(nt, 90, 15, d, d, "half", "q8", 16, True, False, [7 + i for i in range(nt)])
+        c.check(*c.run(mq))
+
+
 def test_many_rows_of_small_heads(mq):
     c = Case(2000, 14, 2, 64, 64, "half", "bf16", 32, False, True, [5 * i for i in range(2000)], pad=1)
     c.check(*c.run(mq))
