@@ -993,23 +993,51 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
     }
 }
 
-// CTAs per row.  The fewest whose slice leaves room for two CTAs an SM; more of them while the rows'
-// CTAs stay within two thirds of the SMs (clusters do not pack further) and each has 2048 values or
-// more, or 8192 for the step to 16, whose barriers cost more.  Captured, us, top-k 40 + top-p / top-p
-// 0.9 of flat logits, C = 4, 8, 16: 152064 tokens, 1 row: -, 13.6 / 29.0, 13.0 / 23.0; 12 rows: -, 14.6 /
-// 29.6, 17.4 / 32.1; 50257 tokens, 1 row: 12.3 / 22.4, 11.2 / 18.4, 11.9 / 18.4; 64 rows: 16.8 / 32.5, 26.6 /
-// 50.6, 57 / 103 (the top-k of these by step 3).
+constexpr size_t kMaxSmem = 227 * 1024, kSmSmem = 228 * 1024;  // a CTA's most; an SM's (each CTA takes 1 KB more)
+
+// Values of a CTA: whole groups of four; a row may start up to 3 values behind a 16-byte border.
+int slice_of(int vocab, int c) { return ((vocab + 3 + c - 1) / c + 3) & ~3; }
+// Values of a thread. Odd: the threads' segments lie in different banks.
+int seg_of(int slice) { return (slice + kThreads - 1) / kThreads | 1; }
+size_t smem_of(int slice) { return sizeof(Shared) + (size_t)seg_of(slice) * kThreads * sizeof(float); }
+
+// CTAs per row: the ones that take the least, counted in values of a slice.  A wave of rows takes what its
+// barriers and latencies are worth, kWaveCost, and its values on an SM: one slice, or two where a slice leaves
+// room and the rows ask for it.  Clusters do not fill the GPU: `alone` of its SMs can hold one CTA each, `slots`
+// is what it holds at once.  Equal costs: the fewer CTAs.  Captured, us, top-k 40 / top-p 0.9 of flat logits /
+// min-p, C = 2, 4, 8, 16, the choice last:
+//   152064 tokens,  1 row:   -, 16.3 / 32.6 / 17.5, 12.5 / 23.7 / 11.7, 10.4 / 20.4 /  8.4   (16)
+//                  12 rows:  -, 16.8 / 32.9 / 17.3, 13.6 / 24.5 / 12.3, 14.8 / 28.4 / 12.4   (8)
+//                  32 rows:  -, 17.6 / 33.9 / 18.1, 19.0 / 37.2 / 18.9, 27.4 / 67.1 / 26.7   (4)
+//                  38 rows:  -, 28.6 / 63.5 / 32.6, 24.7 / 53.2 / 26.1, 30.5 / 77.3 / 31.1   (8)
+//                  64 rows:  -, 33.6 / 66.0 / 34.9, 31.8 / 71.9 / 35.3, 44.6 / 118 / 48.7    (4)
+//   50257 tokens,  16 rows: 13.9 / 25.6 / 13.3, 11.7 / 19.2 / 9.7, 13.7 / 22.0 / 10.5, 16.0 / 36.5 / 14.2   (4)
+//                  64 rows: 14.9 / 26.5 / 14.2, 16.5 / 27.4 / 14.4, 24.0 / 45.0 / 20.7, 36.4 / 96.2 / 37.1  (2)
+// CTAs of 1024 threads took longer in every one of these.
+constexpr int kWaveCost = 30000;
+constexpr int kLeast = 2048;  // values of a slice that are worth a CTA
+
 int cluster_for(int nt, int vocab, int sms)
 {
-    int c = 1;
-    while (c < 16 && (vocab + 3) / c > 20480) c <<= 1;
-    while (c < 16 && (long long)nt * 2 * c * 3 <= (long long)sms * 2 && vocab / (2 * c) >= (c < 8 ? 2048 : 8192)) c <<= 1;
-    return c;
+    int best = 16;
+    long long least = -1;
+    for (int c = 1; c <= 16 && (c == 1 || vocab / c >= kLeast); c <<= 1) {
+        const long long slice = (vocab + 3) / c + 1, cost = kWaveCost + (c == 16 ? kWaveCost / 15 : 0);
+        if (c < 16 && smem_of(slice_of(vocab, c)) > kMaxSmem) continue;
+        const bool two = 2 * (smem_of(slice_of(vocab, c)) + 1024) <= kSmSmem;
+        const int percent = c == 16 ? 74 : c == 8 ? 93 : 95;  // of the CTAs that its SMs could hold
+        const long long alone = (long long)sms * (c == 16 ? 74 : c == 8 ? 67 : 85) / 100 / c;  // rows
+        const long long slots = two ? (long long)sms * 2 * percent / 100 / c : alone;
+        if (slots < 1) continue;
+        const long long full = nt / slots, rest = nt % slots;
+        const long long t = full * (cost + slice * (two ? 2 : 1)) + (rest == 0 ? 0 : cost + slice * (rest > alone ? 2 : 1));
+        if (least < 0 || t < least) best = c, least = t;
+    }
+    return best;
 }
 
 constexpr int kMaxDevices = 64;
 std::atomic<bool> g_opted[kMaxDevices];
-constexpr size_t kMaxSmem = 227 * 1024;
 
 }  // namespace
 
@@ -1026,10 +1054,9 @@ cudaError_t launch_sample(SampleLaunch a, int sms, int pdl, cudaStream_t st)
         if (dev >= 0 && dev < kMaxDevices) g_opted[dev].store(true, std::memory_order_release);
     }
     const int c = cluster_for(a.nt, a.vocab, sms);
-    // a row may start up to 3 values behind a 16-byte border
-    a.slice = ((a.vocab + 3 + c - 1) / c + 3) & ~3;
-    a.seg = (a.slice + kThreads - 1) / kThreads | 1;  // odd: the threads' segments lie in different banks
-    const size_t smem = sizeof(Shared) + (size_t)a.seg * kThreads * sizeof(float);
+    a.slice = slice_of(a.vocab, c);
+    a.seg = seg_of(a.slice);
+    const size_t smem = smem_of(a.slice);
     if (smem > kMaxSmem) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.nt * c));
