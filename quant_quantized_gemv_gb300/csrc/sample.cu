@@ -54,6 +54,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 #include <utility>
 
 #include "f32x2.cuh"
@@ -800,46 +801,52 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
                 __syncthreads();
                 u64 total = 0, above = 0;
                 unsigned aside_bits = 0;  // of up to 32 values: those in the window
-                auto take = [&](float x, int i, unsigned wa, unsigned wm, int bin_x, int bit) {
-                    const bool in = passes(x, i);
-                    const int b = bin_x - from;
-                    wa = in ? wa : 0;
-                    total += (u64)wa * wm;
-                    above += (u64)(b < 0 ? wa : 0) * wm;
-                    aside_bits |= in && (unsigned)b < (unsigned)kWindow ? 1u << bit : 0u;
-                };
-                unsigned wa[2], wm[2];
-                int bins[2];
-                for (int chunk = first; chunk < first + a.seg; chunk += 32) {
-                    const int to = min(first + a.seg, chunk + 32);
-                    int i = chunk;
+                // -inf (weight 0) is in the last bin, which nothing that matters is in
+                const unsigned width = min(kWindow, kBins - 1 - from);
+                auto pass = [&](auto limited) {
+                    auto take = [&](float x, int i, unsigned wa, unsigned wm, int bin_x, int bit) {
+                        const int b = bin_x - from;
+                        bool in = true;
+                        if constexpr (limited.value) in = passes(x, i);
+                        if (in) total += (u64)wa * wm;
+                        if (in && b < 0) above += (u64)wa * wm;
+                        if (in && (unsigned)b < width) aside_bits |= 1u << bit;
+                    };
+                    unsigned wa[2], wm[2];
+                    int bins[2];
+                    for (int chunk = first; chunk < first + a.seg; chunk += 32) {
+                        const int to = min(first + a.seg, chunk + 32);
+                        int i = chunk;
 #pragma unroll 2
-                    for (; i + 1 < to; i += 2) {
-                        const float x0 = xs[i], x1 = xs[i + 1];
-                        weight.pair(x0, x1, wa, wm, bins);
-                        take(x0, i, wa[0], wm[0], bins[0], i - chunk);
-                        take(x1, i + 1, wa[1], wm[1], bins[1], i - chunk + 1);
-                    }
-                    if (i < to) {
-                        weight.pair(xs[i], xs[i], wa, wm, bins);
-                        take(xs[i], i, wa[0], wm[0], bins[0], i - chunk);
-                    }
-                    // room for the warp's at once
-                    if (__any_sync(0xffffffffu, aside_bits != 0)) {
-                        const unsigned n = __popc(aside_bits);
-                        unsigned sum = n;
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const unsigned t = __shfl_up_sync(0xffffffffu, sum, o);
-                            if (lane >= o) sum += t;
+                        for (; i + 1 < to; i += 2) {
+                            const float x0 = xs[i], x1 = xs[i + 1];
+                            weight.pair(x0, x1, wa, wm, bins);
+                            take(x0, i, wa[0], wm[0], bins[0], i - chunk);
+                            take(x1, i + 1, wa[1], wm[1], bins[1], i - chunk + 1);
                         }
-                        unsigned room = 0;
-                        if (lane == 31) room = atomicAdd(&sh.mine_n, sum);
-                        room = __shfl_sync(0xffffffffu, room, 31) + sum - n;
-                        for (; aside_bits; aside_bits &= aside_bits - 1, ++room)
-                            if (room < kMine) sh.mine[room] = place(chunk + __ffs(aside_bits) - 1);
+                        if (i < to) {
+                            weight.pair(xs[i], xs[i], wa, wm, bins);
+                            take(xs[i], i, wa[0], wm[0], bins[0], i - chunk);
+                        }
+                        // room for the warp's at once
+                        if (__any_sync(0xffffffffu, aside_bits != 0)) {
+                            const unsigned n = __popc(aside_bits);
+                            unsigned sum = n;
+#pragma unroll
+                            for (int o = 1; o < 32; o <<= 1) {
+                                const unsigned t = __shfl_up_sync(0xffffffffu, sum, o);
+                                if (lane >= o) sum += t;
+                            }
+                            unsigned room = 0;
+                            if (lane == 31) room = atomicAdd(&sh.mine_n, sum);
+                            room = __shfl_sync(0xffffffffu, room, 31) + sum - n;
+                            for (; aside_bits; aside_bits &= aside_bits - 1, ++room)
+                                if (room < kMine) sh.mine[room] = place(chunk + __ffs(aside_bits) - 1);
+                        }
                     }
-                }
+                };
+                if (cut) pass(std::true_type());
+                else pass(std::false_type());
                 mine = above;
                 for (int o = 16; o > 0; o >>= 1) {
                     total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -943,21 +950,28 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
     };
     if (!summed) {
         mine = 0;
-        auto take = [&](float x, int i, unsigned wa, unsigned wm) {
-            const u64 w = (u64)wa * wm;
-            if (passes(x, i) && w >= floor_w) mine += w;
-        };
-        unsigned wa[2], wm[2];
-        int bins[2];
-        weight.pair(xs[first], xs[first], wa, wm, bins);
-        take(xs[first], first, wa[0], wm[0]);
+        auto pass = [&](auto limited, auto floored) {
+            auto take = [&](float x, int i, unsigned wa, unsigned wm) {
+                bool in = true;
+                if constexpr (limited.value) in = passes(x, i);
+                if constexpr (floored.value) in = in && (u64)wa * wm >= floor_w;
+                if (in) mine += (u64)wa * wm;
+            };
+            unsigned wa[2], wm[2];
+            int bins[2];
+            weight.pair(xs[first], xs[first], wa, wm, bins);
+            take(xs[first], first, wa[0], wm[0]);
 #pragma unroll 2
-        for (int i = first + 1; i < first + a.seg; i += 2) {
-            const float x0 = xs[i], x1 = xs[i + 1];
-            weight.pair(x0, x1, wa, wm, bins);
-            take(x0, i, wa[0], wm[0]);
-            take(x1, i + 1, wa[1], wm[1]);
-        }
+            for (int i = first + 1; i < first + a.seg; i += 2) {
+                const float x0 = xs[i], x1 = xs[i + 1];
+                weight.pair(x0, x1, wa, wm, bins);
+                take(x0, i, wa[0], wm[0]);
+                take(x1, i + 1, wa[1], wm[1]);
+            }
+        };
+        if (last_x > -INFINITY) pass(std::true_type(), std::true_type());
+        else if (floor_w > 0) pass(std::false_type(), std::true_type());
+        else pass(std::false_type(), std::false_type());
     }
     u64 total;
     u64 before = block_scan(mine, sh.warp_sums, &total);
