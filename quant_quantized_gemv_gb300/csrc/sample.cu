@@ -33,9 +33,9 @@
 //      that were set aside); the sums before it and the random number say which
 //      CTA, which thread and which token is drawn.
 //
-// What bounds it: with many rows the instructions of step 4's pass (about 45 a
-// token; the row itself is read once); with few, the steps one after another
-// (a cluster barrier each).  Nothing uses 64-bit floating point (a division by
+// What bounds it: with many rows the load, the count and step 4's pass one after
+// another (64 rows of 152064, flat, top-p 0.9: 59 us, of which loads 6, some 90
+// instructions a token 30; each row is read once); with few, the steps' barriers.  Nothing uses 64-bit floating point (a division by
 // every thread took 2.9 us), and conversions between float and integer, at an
 // eighth of the rate of an addition, are kept to one a weight: the others add
 // 1.5 x 2^23 and take the low bits.
@@ -1019,7 +1019,7 @@ size_t smem_of(int slice) { return sizeof(Shared) + (size_t)seg_of(slice) * kThr
 // barriers and latencies are worth, kWaveCost, and its values on an SM: one slice, or two where a slice leaves
 // room and the rows ask for it.  Clusters do not fill the GPU: `alone` of its SMs can hold one CTA each, `slots`
 // is what it holds at once.  Equal costs: the fewer CTAs.  Captured, us, top-k 40 / top-p 0.9 of flat logits /
-// min-p, C = 2, 4, 8, 16, the choice last:
+// min-p, C = 2, 4, 8, 16, the choice last (before the passes without limits took a tenth less):
 //   152064 tokens,  1 row:   -, 16.3 / 32.6 / 17.5, 12.5 / 23.7 / 11.7, 10.4 / 20.4 /  8.4   (16)
 //                  12 rows:  -, 16.8 / 32.9 / 17.3, 13.6 / 24.5 / 12.3, 14.8 / 28.4 / 12.4   (8)
 //                  32 rows:  -, 17.6 / 33.9 / 18.1, 19.0 / 37.2 / 18.9, 27.4 / 67.1 / 26.7   (4)
