@@ -6,7 +6,7 @@
 // into shared memory, and everything after that happens there and in the
 // cluster's distributed shared memory: one launch, no workspace, no sort of
 // the vocabulary.
-//   0. a short top-k (up to 48 with 16 CTAs a row, 96 with 8, 192, then 256): every CTA
+//   0. a short top-k (up to 56 with 16 CTAs a row, 112 with 8, 224, then 256): every CTA
 //      sends the first top_k tokens of its slice, by bins as in 2, to rank 0, which
 //      narrows them to few more than top_k, applies every filter and draws: one
 //      exchange instead of four (one row of 152064, top-k 40: 12.6 -> 10.5 us). What does
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
     // A short top-k: every CTA sends its own first top_k tokens, and all of their bin, to rank 0, which
     // chooses and draws. The others leave after one barrier. (Infinities and long ties: below.)
     const int room = kSent / ranks;  // a power of two
-    if (!single && by_count && top_k <= min(room / 4 * 3, kMostSmall)) {
+    if (!single && by_count && top_k <= min(room - room / 8, kMostSmall)) {
         int sent = 0;
         if (own == INFINITY) sent = kSent + 1;
         else if (own != -INFINITY) {
