@@ -18,7 +18,9 @@
 //      groups over the cluster, then the bins of one group;
 //   3. top-k ends in the bin where the counts reach k.  With few tokens down
 //      to that bin (the usual chain of filters) they alone are gathered in
-//      rank 0, which applies every filter and draws.  Else the bin's tokens are
+//      rank 0, which applies every filter and draws; up to 2047 of them too, in the
+//      order of the vocabulary, where bins and bytes of the place find top-k's and
+//      top-p's last (one row of 152064, top-k 1000: 27 -> 17 us, 64 rows 93 -> 42).  Else the bin's tokens are
 //      gathered and ranked, which gives the last token kept, as a 64-bit place
 //      in the order (logit, then index): every CTA gets the list and ranks its
 //      own tokens.  A bin of more tokens than the list holds (ties) is first
@@ -73,6 +75,8 @@ constexpr float kBinsPerOctave = 64.0f;
 constexpr int kList = 512;       // tokens that rank 0 ranks at once
 constexpr int kMine = 1024;      // tokens that a CTA sets aside
 constexpr int kSent = 1024;      // tokens that rank 0 chooses from, in equal rooms for the CTAs
+constexpr int kLong = 2048;      // places for the tokens of a longer top-k, less one: sums in two halves fit 32 bits
+constexpr int kRest = 64;        // of these, what is ranked at once
 constexpr int kMostSmall = 256;  // the largest top-k that is chosen so
 constexpr int kFew = 128;        // tokens that rank 0 ranks without narrowing them first
 constexpr int kMaxCluster = 16;  // CTAs of a row (over 8: the non-portable size)
@@ -85,6 +89,7 @@ constexpr int kSums = 2 + 2 * kWindow + 1;
 struct alignas(16) Shared {
     union {
         unsigned cnt[kBins];                     // this CTA's bins
+        u64 longer[kLong];                       // rank 0: what a longer top-k may keep, in the order of the vocabulary
         struct {
             u64 mine[kMine];                     // afterwards: its tokens that may matter
             union {
@@ -250,6 +255,157 @@ __device__ __forceinline__ int reach(u64 v0, u64 v1, u64 target, u64 *before, u6
     return __shfl_sync(0xffffffffu, 2 * lane + (second ? 1 : 0), at);
 }
 
+// A share s < 1 of a sum: its floor, or that rounded up, by the 64 bits behind the point.
+__device__ __forceinline__ u64 share_of(float s, u64 all, bool up)
+{
+    const u64 f = __float2ull_rz(s * 18446744073709551616.0f);
+    return __umul64hi(f, all) + (up && f * all != 0 ? 1 : 0);
+}
+
+// w / all: the quotient and one correction.
+__device__ __forceinline__ float share_f32(u64 w, u64 all)
+{
+    const float wh = __ull2float_rn(w), ah = __ull2float_rn(all);
+    const float wl = __ll2float_rn((long long)(w - __float2ull_rn(wh)));
+    const float al = __ll2float_rn((long long)(all - __float2ull_rn(ah)));
+    const float q = wh / ah;
+    return q + ((fmaf(-q, ah, wh) + wl) - q * al) / ah;
+}
+
+// A row's filters and its random number.
+struct Filters {
+    float u, top_p;
+    int top_k;
+    u64 floor_w;     // min-p's least weight
+    bool by_weight;  // top-p is on
+
+    __device__ __forceinline__ u64 drawn_at(u64 all) const
+    {
+        return u > 0.0f ? (u < 1.0f ? share_of(u, all, false) : all - 1) : 0;
+    }
+    __device__ __forceinline__ u64 wanted(u64 all) const { return max(share_of(top_p, all, true), (u64)1); }  // top-p of a sum
+};
+
+// The draw from rank 0's longer list: n tokens in the order of the vocabulary, of which top-k keeps those
+// before bin `bin` and the first `left` of that bin's `population`.
+// A function of its own: its registers are not the kernel's.
+__device__ __noinline__ void draw_from_longer(Shared &sh, const Weight weight, const Filters f, const SampleLaunch &a,
+                                              int row, int n, int bin, unsigned left, unsigned population)
+{
+    const int tid = threadIdx.x, lane = tid & 31;
+    constexpr int kOwn = kLong / kThreads;
+    u64 p[kOwn], w[kOwn];
+    unsigned in = 0, in_bin = 0;  // a bit a token
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        const int i = tid * kOwn + j;
+        p[j] = i < n ? sh.longer[i] : 0;
+        const float x = logit_of((unsigned)(p[j] >> 32));
+        w[j] = p[j] ? weight(x) : 0;
+        if (p[j] && weight.bin(x) == bin) in_bin |= 1u << j;
+    }
+    // Of the tokens in play, the place of the one at which their number, or their weights, reach `left`: by
+    // coarse bins, bins, then bytes of the place (levels 0, 1, 2..9), until few are left, which are ranked.
+    unsigned *const lo = reinterpret_cast<unsigned *>(sh.digit_w), *const hi = lo + kDigits;
+    auto settle = [&](unsigned play, int level, u64 left, bool counts, unsigned population) {
+        auto digit_of = [&](int j) {
+            if (level >= 2) return kDigits - 1 - ((int)(p[j] >> (72 - 8 * level)) & (kDigits - 1));
+            const int b = weight.bin(logit_of((unsigned)(p[j] >> 32)));
+            return level == 0 ? b / (kBins / kDigits) : b % (kBins / kDigits);
+        };
+        for (; population > kRest && level < 10; ++level) {
+            __syncthreads();
+            if (tid < kDigits) sh.digit_n[tid] = lo[tid] = hi[tid] = 0;
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j)
+                if (play >> j & 1) {
+                    const int d = digit_of(j);
+                    atomicAdd(&sh.digit_n[d], 1u);
+                    if (!counts) atomicAdd(&lo[d], (unsigned)w[j] & 0x1fffffu), atomicAdd(&hi[d], (unsigned)(w[j] >> 21));
+                }
+            __syncthreads();
+            u64 v[8], sum = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int d = 8 * lane + j;
+                sum += v[j] = counts ? sh.digit_n[d] : ((u64)hi[d] << 21) + lo[d];
+            }
+            u64 to = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 t = __shfl_up_sync(0xffffffffu, to, o);
+                if (lane >= o) to += t;
+            }
+            const int at = __ffs(__ballot_sync(0xffffffffu, to >= left)) - 1;  // left <= the sum of all
+            u64 before = to - sum;
+            int digit = 8 * lane;
+            bool found = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (!found) {
+                    found = before + v[j] >= left;
+                    if (!found) before += v[j], ++digit;
+                }
+            digit = __shfl_sync(0xffffffffu, digit, at);
+            left -= __shfl_sync(0xffffffffu, before, at);
+            population = sh.digit_n[digit];
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j)
+                if ((play >> j & 1) && digit_of(j) != digit) play &= ~(1u << j);
+        }
+        u64 *const rest = sh.sent, *const rest_w = sh.sent + kRest;
+        if (tid == 0) sh.mine_n = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+            if (play >> j & 1) {
+                const unsigned at = atomicAdd(&sh.mine_n, 1u);
+                rest[at] = p[j], rest_w[at] = w[j];
+            }
+        __syncthreads();
+        const int m = (int)sh.mine_n, i = tid / (kThreads / kRest);
+        u64 before = 0;
+        if (i < m)
+            for (int j = tid % (kThreads / kRest); j < m; j += kThreads / kRest)
+                if (rest[j] > rest[i]) before += counts ? 1 : rest_w[j];
+#pragma unroll
+        for (int o = 1; o < kThreads / kRest; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+        if (i < m && tid % (kThreads / kRest) == 0 && before < left && left <= before + (counts ? 1 : rest_w[i]))
+            sh.boundary = rest[i];
+        __syncthreads();
+        return sh.boundary;
+    };
+    const u64 last = settle(in_bin, 2, left, true, population);
+    u64 sum = 0, all;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+        if (p[j] >= last) in |= 1u << j, sum += w[j];
+    if (f.by_weight) {
+        block_scan(sum, sh.warp_sums, &all);
+        const u64 end = settle(in, 0, f.wanted(all), false, (unsigned)f.top_k);
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+            if (p[j] < end) in &= ~(1u << j);
+    }
+    sum = 0;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        if (!(in >> j & 1) || w[j] < f.floor_w) w[j] = 0;
+        sum += w[j];
+    }
+    u64 before = block_scan(sum, sh.warp_sums, &all);
+    const u64 target = f.drawn_at(all);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        if (before <= target && target < before + w[j]) {
+            a.token[row] = (int)~(unsigned)p[j];
+            if (a.prob) a.prob[row] = share_f32(w[j], all);
+        }
+        before += w[j];
+    }
+}
+
 __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
@@ -319,23 +475,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
     if (!(fabsf(weight.c_lo) < weight.c_hi)) weight.c_lo = 0.0f;  // clamped, or an infinite temperature
     const u64 floor_w = min_p > 0.0f ? __float2ull_ru(min_p * (float)(1ull << kFixBits)) : 0;
     const bool by_count = top_k > 0 && top_k < a.vocab, by_weight = top_p < 1.0f;
+    const Filters filters = {u, top_p, top_k, floor_w, by_weight};
     const int first = tid * a.seg;  // this thread's values, in the order of the vocabulary
     auto index_of = [&](int i) { return base + i - shift; };
     auto place = [&](int i) { return place_of(xs[i], index_of(i)); };
-    // a share s < 1 of a sum: its floor, by the 64 bits behind the point
-    auto share_of = [](float s, u64 all, bool up) {
-        const u64 f = __float2ull_rz(s * 18446744073709551616.0f);
-        return __umul64hi(f, all) + (up && f * all != 0 ? 1 : 0);
-    };
-    auto drawn_at = [&](u64 all) { return u > 0.0f ? (u < 1.0f ? share_of(u, all, false) : all - 1) : 0; };
-    auto wanted = [&](u64 all) { return max(share_of(top_p, all, true), (u64)1); };  // top-p of a sum
-    auto share_f32 = [](u64 w, u64 all) {  // w / all: the quotient and one correction
-        const float wh = __ull2float_rn(w), ah = __ull2float_rn(all);
-        const float wl = __ll2float_rn((long long)(w - __float2ull_rn(wh)));
-        const float al = __ll2float_rn((long long)(all - __float2ull_rn(ah)));
-        const float q = wh / ah;
-        return q + ((fmaf(-q, ah, wh) + wl) - q * al) / ah;
-    };
+    auto drawn_at = [&](u64 all) { return filters.drawn_at(all); };
+    auto wanted = [&](u64 all) { return filters.wanted(all); };
 
     // Ranks the tokens [from, to) of a list of n.  body(i, tokens before i, weights before i) runs in
     // one thread for each of them; several threads share the comparisons of one token.
@@ -745,14 +890,46 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
             cut = n_all > (u64)top_k;
             if (cut) {
                 read_group(group);
-                auto read = cluster.barrier_arrive();
                 u64 in_group, bins_all;
                 const int at = reach(sh.bins_n[2 * lane], sh.bins_n[2 * lane + 1], (u64)top_k - before, &in_group, &bins_all);
                 cut_bin = group * 64 + at;
                 cut_left = (unsigned)((u64)top_k - before - in_group);
                 cut_n = sh.bins_n[at];
                 const unsigned cut_to = (unsigned)top_k - cut_left + cut_n;
-                cluster.barrier_wait(std::move(read));  // nobody reads this CTA's bins for this any more
+                const bool longer = cut_to > kList && cut_to < kLong;
+                if (longer) {  // how many of them are this CTA's
+                    u64 n = 0, own_n;
+#pragma unroll
+                    for (int j = 0; j < kBins / kThreads; ++j) {
+                        const int b = j * kThreads + tid;
+                        if (b <= cut_bin) n += sh.cnt[b];
+                    }
+                    block_scan(n, sh.warp_sums, &own_n);
+                    if (tid < ranks) cluster.map_shared_rank(&sh, tid)->sent_n[rank] = (int)own_n;
+                }
+                cluster.sync();  // nobody reads this CTA's bins for this any more
+                if (longer) {
+                    int to = 0;
+                    for (int r = 0; r < rank; ++r) to += sh.sent_n[r];
+                    auto hits_of = [&](int from) {  // of 64 of this thread's up to 128 values
+                        u64 hits = 0;
+                        for (int j = from; j < min(a.seg, from + 64); j += 2) {
+                            const float x0 = xs[first + j], x1 = j + 1 < a.seg ? xs[first + j + 1] : -INFINITY;
+                            int b0, b1;
+                            weight.bins(x0, x1, b0, b1);
+                            hits |= (u64)((b0 <= cut_bin && x0 != -INFINITY ? 1 : 0) |
+                                          (b1 <= cut_bin && x1 != -INFINITY ? 2 : 0)) << (j - from);
+                        }
+                        return hits;
+                    };
+                    u64 hits0 = hits_of(0), hits1 = hits_of(64), all;
+                    to += (int)block_scan((u64)(__popcll(hits0) + __popcll(hits1)), sh.warp_sums, &all);
+                    for (; hits0; hits0 &= hits0 - 1) root.longer[to++] = place(first + __ffsll(hits0) - 1);
+                    for (; hits1; hits1 &= hits1 - 1) root.longer[to++] = place(first + 63 + __ffsll(hits1));
+                    cluster.sync();
+                    if (rank == 0) draw_from_longer(sh, weight, filters, a, row, (int)cut_to, cut_bin, cut_left, cut_n);
+                    return;
+                }
                 if (cut_to <= kList) {
                     // everything that can be kept, in one list; rank 0 alone goes on
                     gather(0, cut_bin, 0, 0, false);
@@ -961,7 +1138,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
             int bins[2];
             weight.pair(xs[first], xs[first], wa, wm, bins);
             take(xs[first], first, wa[0], wm[0]);
-#pragma unroll 2
+#pragma unroll 3
             for (int i = first + 1; i < first + a.seg; i += 2) {
                 const float x0 = xs[i], x1 = xs[i + 1];
                 weight.pair(x0, x1, wa, wm, bins);
@@ -1069,9 +1246,9 @@ cudaError_t launch_sample(SampleLaunch a, int sms, int pdl, cudaStream_t st)
     }
     const int c = cluster_for(a.nt, a.vocab, sms);
     a.slice = slice_of(a.vocab, c);
-    a.seg = seg_of(a.slice);
+    a.seg = seg_of(a.slice);  // what fits shared memory is under 128
     const size_t smem = smem_of(a.slice);
-    if (smem > kMaxSmem) return cudaErrorInvalidValue;
+    if (smem > kMaxSmem || a.seg > 128) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.nt * c));
     cfg.blockDim = dim3(kThreads);

@@ -315,3 +315,28 @@ def test_short_top_k(mq, v, kind):
             s = slice(a, a + 6)
             check(x[s], u[s], run(mq, x[s], u[s], k=ks[s], **more), k=ks[s], **more)
     check(x[:1], u[:1], run(mq, x[:1], u[:1], k=40, p=0.95), k=40, p=0.95)
+
+
+@pytest.mark.parametrize("kind", ["spread", "flat", "ties", "ties at the end", "near", "one place", "half infinite"])
+@pytest.mark.parametrize("v", [2100, 9001, 50257, 152064])
+def test_longer_top_k(mq, v, kind):
+    """Top-k whose tokens one CTA takes from all of them, up to and past what it has room for; top-p among
+    them ends anywhere; ties by the hundred, within and across parts."""
+    ks = [300, 511, 513, 1000, 1500, 1990, 2040, 2046, 2047, 2048, 2060, 4000]
+    x, u = rows("longer " + kind, len(ks), v, 0.5 if kind == "flat" else 2.5, 40 if kind == "one place" else 0)
+    g = synth.rng("longer", kind, v)
+    if kind == "ties":                       # 700 equal ones above the rest
+        x[:, g.choice(v, 700, replace=False)] = 20.0
+    elif kind == "ties at the end":          # top-k ends among 1900 equal ones
+        x[:, g.choice(v, 1900, replace=False)] = 20.0
+        x[:, g.choice(v, 100, replace=False)] = 20.5
+    elif kind == "near":                     # one bin, the order in the last bits
+        x[:, g.choice(v, 1800, replace=False)] = 20.0 + g.integers(0, 5, 1800) * np.float32(2.0 ** -19)
+    elif kind == "one place":                # nearly all of them in one part
+        x[:, v // 3:v // 3 + 1700] += 15.0
+    elif kind == "half infinite":
+        x[:, g.choice(v, v // 2, replace=False)] = -np.inf
+    for more in (dict(), dict(p=0.9), dict(p=0.3, t=0.5), dict(m=0.2, t=2.0), dict(p=0.97, m=0.01, t=1.3)):
+        for a in range(0, len(ks), 6):
+            s = slice(a, a + 6)
+            check(x[s], u[s], run(mq, x[s], u[s], k=ks[s], **more), k=ks[s], **more)
