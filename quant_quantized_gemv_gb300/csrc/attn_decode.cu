@@ -221,7 +221,7 @@ struct Smem {
     float total[kAttnHeads];
     int sums[S::warps];
     int last;
-    int rounds[kAttnMaxRows + 1], lens[kAttnMaxRows];      // rounds of the rows before each row; their tokens
+    int rounds[kAttnMaxRows + 1], lens[kAttnMaxRows], seqs[kAttnMaxRows];  // rounds of the rows before each row; their tokens, sequences
 };
 
 // A place in the line of rounds: a unit, or the part of it that falls to this CTA.
@@ -268,13 +268,14 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
 
     const int units = a.n_kv_heads * a.subgroups;  // of a row
     const bool shared_out = a.nt <= kAttnMaxRows;  // else a CTA per unit
-    int end, share = 0, single_n = 0;
+    int end, share = 0, single_n = 0, single_seq = 0;
     Segment load_at;
     if (shared_out) {
         // rounds of the rows before each row: up to 32 rows by every warp for itself
         int before = 0;
         if (a.nt <= 32) {
             const int n = lane < a.nt ? __ldcg(a.lens + lane) : -1;
+            const int seq = a.seq && lane < a.nt ? __ldcg(a.seq + lane) : lane;
             const int mine = line_of(n);
             int s = mine;
 #pragma unroll
@@ -284,11 +285,12 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
             }
             before = __shfl_sync(kFull, s, 31);
             sh.rounds[lane] = s - mine;  // every warp writes the same
-            if (lane < a.nt) sh.lens[lane] = n;
+            if (lane < a.nt) sh.lens[lane] = n, sh.seqs[lane] = seq;
             __syncwarp();
         } else for (int r0 = 0; r0 < a.nt; r0 += kThreads) {
             const int r = r0 + tid;
             const int n = r < a.nt ? __ldcg(a.lens + r) : -1;
+            const int seq = a.seq && r < a.nt ? __ldcg(a.seq + r) : r;
             const int mine = line_of(n);
             int s = mine;
 #pragma unroll
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                 if (w == warp) s += all;
                 all += sh.sums[w];
             }
-            if (r < a.nt) sh.rounds[r] = before + s - mine, sh.lens[r] = n;
+            if (r < a.nt) sh.rounds[r] = before + s - mine, sh.lens[r] = n, sh.seqs[r] = seq;
             before += all;
             if (r0 + kThreads < a.nt) __syncthreads();
         }
@@ -336,10 +338,12 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
         load_at.unit = blockIdx.x - load_at.row * units;
         load_at.pos = load_at.round = 0;
         single_n = __ldcg(a.lens + load_at.row);
+        single_seq = a.seq ? __ldcg(a.seq + load_at.row) : load_at.row;
         end = line_of(single_n);
     }
     auto kv_head = [&](int unit) { return a.subgroups == 1 ? unit : unit / a.subgroups; };
     auto n_of = [&](int row) { return shared_out ? sh.lens[row] : single_n; };
+    auto seq_of = [&](int row) { return shared_out ? sh.seqs[row] : single_seq; };
     // completes a segment that begins where its fields say (its round counted with the unit's cost; from
     // then on without); false: none is left
     auto enter = [&](Segment &s) {
@@ -387,11 +391,12 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
     int load_round = 0, load_count = 0;              // round of the segment; segments begun
     int l_first = 0, l_n = 0, l_from = 0, l_to = 0;
     int l_pages = -1, l_slots = 0;                   // pages and places in them: a lane a round, 32 at a time
+    int asked_row = -1, asked_from = 0, asked_to = 0;  // of these tokens: the next unit of the row may need the same
     const int *l_table = nullptr;
     size_t l_head = 0;
     auto open_load = [&]() {
         l_n = n_of(load_at.row);
-        const int seq = a.seq ? __ldcg(a.seq + load_at.row) : load_at.row;
+        const int seq = seq_of(load_at.row);
         const bool bad = (unsigned)seq >= (unsigned)a.n_seqs || too_long(l_n);
         l_first = first_of(l_n);
         l_from = start_of(l_n) + load_at.round * kRound + warp * kAttnTile;
@@ -400,6 +405,8 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
         l_head = (size_t)kv_head(load_at.unit) * a.head_bytes;
     };
     auto ask_pages = [&]() {
+        if (asked_row == load_at.row && asked_from == l_from && asked_to == l_to) return;
+        asked_row = load_at.row, asked_from = l_from, asked_to = l_to;
         const int tok = l_from + lane * kRound;
         if (tok < l_to) {
             const int i = tok / a.page_size;
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
         const int head0 = kvh * a.group + sg * kAttnHeads, heads = min(kAttnHeads, a.group - sg * kAttnHeads);
         const int n = n_of(at.row), first = first_of(n);
         const int from = start_of(n) + at.round * kRound + warp * kAttnTile;
-        const int seq = a.seq ? __ldcg(a.seq + at.row) : at.row;
+        const int seq = seq_of(at.row);
         bool bad = (unsigned)seq >= (unsigned)a.n_seqs || too_long(n);
         const int to = bad ? 0 : min(n, start_of(n) + (at.round + at.take) * kRound);
         const bool whole = at.take == at.rounds;
