@@ -20,11 +20,11 @@
 //      to that bin (the usual chain of filters) they alone are gathered in
 //      rank 0, which applies every filter and draws; up to 2047 of them too, in the
 //      order of the vocabulary, where bins and bytes of the place find top-k's and
-//      top-p's last (one row of 152064, top-k 1000: 27 -> 17 us, 64 rows 93 -> 42).  Else the bin's tokens are
-//      gathered and ranked, which gives the last token kept, as a 64-bit place
-//      in the order (logit, then index): every CTA gets the list and ranks its
-//      own tokens.  A bin of more tokens than the list holds (ties) is first
-//      narrowed by 8 bits of that place at a time;
+//      top-p's last (one row of 152064, top-k 1000: 27 -> 17 us, 64 rows 93 -> 42).
+//      Else the bin's tokens are gathered and ranked, which gives the last token
+//      kept, as a 64-bit place in the order (logit, then index): every CTA gets the
+//      list and ranks its own tokens.  A bin of more tokens than the list holds
+//      (ties) is first narrowed by 8 bits of that place at a time;
 //   4. top-p: the counts times the bins' weights name a bin.  One pass then sums
 //      the weights of all tokens, of those above a window of bins around it and
 //      of the window's bins one by one, exactly, and sets the window's tokens
@@ -37,10 +37,10 @@
 //
 // What bounds it: with many rows the load, the count and step 4's pass one after
 // another (64 rows of 152064, flat, top-p 0.9: 59 us, of which loads 6, some 90
-// instructions a token 30; each row is read once); with few, the steps' barriers.  Nothing uses 64-bit floating point (a division by
-// every thread took 2.9 us), and conversions between float and integer, at an
-// eighth of the rate of an addition, are kept to one a weight: the others add
-// 1.5 x 2^23 and take the low bits.
+// instructions a token 30; each row is read once); with few, the steps' barriers.
+// Nothing uses 64-bit floating point (a division by every thread took 2.9 us), and
+// conversions between float and integer, at an eighth of the rate of an addition,
+// are kept to one a weight: the others add 1.5 x 2^23 and take the low bits.
 //
 // Weights.  w = 2^-t, t = (max - logit) log2(e) / temperature, as an integer in
 // units of 2^-42: integer sums do not depend on their order, so neither
