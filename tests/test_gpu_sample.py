@@ -340,3 +340,42 @@ def test_longer_top_k(mq, v, kind):
         for a in range(0, len(ks), 6):
             s = slice(a, a + 6)
             check(x[s], u[s], run(mq, x[s], u[s], k=ks[s], **more), k=ks[s], **more)
+
+
+@pytest.mark.parametrize("v", [900, 9001, 50257, 152064])
+@pytest.mark.parametrize("kind", ["peaks", "few", "ties", "room", "infinite"])
+def test_small_nucleus(mq, v, kind):
+    """Top-p alone, of one token to some thousands: peaks, ties by the hundred, a plateau, infinities."""
+    x, u = rows("nucleus " + kind, 12, v, 1.0, 30 if kind == "peaks" else 0)
+    g = synth.rng("nucleus", kind, v)
+    for i in range(len(x)):
+        if kind == "few":
+            x[i, g.choice(v, 5, replace=False)] = 25.0 + i
+        elif kind == "ties":
+            x[i, g.choice(v, min(v // 2, 100 + 170 * i), replace=False)] = 20.0
+        elif kind == "room":                 # 1500 to 2600 tokens within an octave, above all others
+            n = min(v - 10, 1500 + 100 * i)
+            x[i, g.choice(v, n, replace=False)] = 30.0 - g.uniform(0, 0.7, n)
+        elif kind == "infinite":
+            x[i, g.choice(v, 1 + i % 3, replace=False)] = np.inf
+    for more in (dict(p=0.5), dict(p=0.9), dict(p=0.999, t=0.6), dict(p=0.95, m=0.1, t=1.4), dict(p=1e-6), dict(p=0.9999999)):
+        for a in (0, 6):
+            s = slice(a, a + 6)
+            check(x[s], u[s], run(mq, x[s], u[s], **more), **more)
+
+
+@pytest.mark.parametrize("n", [1, 2, 40])
+def test_an_estimate_that_stops_short(mq, n):
+    """The sum by bins of 1/64 octave takes the first token for the whole nucleus; by the weights, the next ones,
+    five octaves below, are needed too: equal, at the heavy end of their bin, n of the 64 by their index."""
+    v, w = 5000, 2.0 ** -(5 - 0.45 / 64)
+    x = np.full((1, v), -60.0, np.float32)
+    x[0, 7] = 0.0
+    tail = np.sort(synth.rng("short", n).choice(np.arange(10, v), 64, replace=False))
+    x[0, tail] = np.float32(-(5 - 0.45 / 64) * np.log(2))
+    p = (1 + (n - 0.5) * w) / (1 + 64 * w) if n > 1 else (1 + 0.02 * w) / (1 + 64 * w)
+    for u in (0.0, 0.5, 0.9, 0.99, 0.9999):
+        got = run(mq, x, np.array([u], np.float32), p=p)
+        tok, pr, kept, _ = ref.sample(x[0], float(np.float32(u)), p=float(np.float32(p)))
+        assert kept.sum() == n + 1
+        check(x, np.array([u], np.float32), got, p=p)
