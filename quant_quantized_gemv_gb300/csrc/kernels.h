@@ -212,7 +212,7 @@ struct RopeAppendLaunch {
     int type, n_pages, page_size, n_kv_heads, head_dim;  // the cache (type: MQ_KV_*)
     int nt, n_heads, rope_dims, style, n_seqs, pages_stride;
     float eps;
-    int two_heads, groups_per_cta, page_shift;  // set by the launch
+    int heads_log, groups_per_cta, page_shift;  // set by the launch
 };
 cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_t st);
 

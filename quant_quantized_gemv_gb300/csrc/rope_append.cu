@@ -13,13 +13,13 @@
 // f32 product would be off by 2^-24 of the whole angle: 0.06 radian at
 // position 10^6.
 //
-// Layout: a lane holds EPL consecutive values of a head, so 16 or 32 lanes hold
-// a head, loads and f32 stores are float4, and the partner of a value under
-// MQ_ROPE_HALF is rope_dims / 2 values away in another lane at the same place
-// (rope_dims a multiple of 2 EPL): one shuffle per value.  EPL is 4 (two heads a
-// warp up to 64 values, else one), or 8 (one head above 128 values; and two heads
-// of 65 to 128 where rows are many: less to do per value, but fewer warps).  A q8
-// block is 32 / EPL lanes: max and codes as in the q8 producers.
+// Layout: a lane holds EPL values of a head, 4 or 8, so 8, 16 or 32 lanes hold a
+// head and a warp 1 to 4 heads; loads and f32 stores are float4.  Where
+// MQ_ROPE_HALF turns whole heads the 8 are four and their four partners, half a
+// head away: nothing is exchanged.  Else they are consecutive, and the partner of
+// a value under MQ_ROPE_HALF is in another lane at the same place (rope_dims a
+// multiple of 2 EPL): one shuffle per value.  A q8 block is the 8 lanes' fours, or
+// 32 / EPL lanes: max and codes as in the q8 producers.
 //
 // Work: a row's heads, queries | keys | values, in groups of what a warp's lanes
 // hold, are shared by the CTAs of the row.  A CTA first writes down where each
@@ -27,11 +27,11 @@
 // way while one thread per pair computes an angle and the row's page is found,
 // which only the cache entries wait for.
 //
-// What bounds it: few rows, the launch and three dependent loads (2.7 us a call
-// in a captured chain).  Many rows, the latency of a CTA's loads, one batch after
-// another, before HBM.  4096 rows of 40 + 8 + 8 heads of 128, 218 MB, which take 33
-// us: f16 38 us (5.7 TB/s), with biases 43, q8 with norms 45.  EPL 4: 40, 47 and
-// 55.  28 groups of EPL 4 a CTA: 45 instead of 40; biases fetched with the values
+// What bounds it: few rows, the launch and three dependent loads (2.6 us a call
+// in a captured chain).  Many rows, HBM and the latency of a CTA's loads, one batch
+// after another.  4096 rows of 40 + 8 + 8 heads of 128, 218 MB, which take 33 us:
+// f16 37 us (5.9 TB/s), with biases 39, q8 with norms 42.  Four values a lane: 40, 47
+// and 55; 28 groups of those a CTA: 45 instead of 40; biases fetched with the values
 // cost registers, so warps: 44 instead of 43; one group a warp: 66.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -61,32 +61,32 @@ struct Vals {
 
 // Biases and gains are weights, which no preceding kernel writes.
 template <int EPL>
-__device__ __forceinline__ Vals<EPL> load_weight(const float *p)
+__device__ __forceinline__ Vals<EPL> load_weight(const float *p, int gap)
 {
     Vals<EPL> r;
 #pragma unroll
     for (int i = 0; i < EPL; i += 4) {
-        const float4 f = __ldg(reinterpret_cast<const float4 *>(p + i));
+        const float4 f = __ldg(reinterpret_cast<const float4 *>(p + (i ? gap : 0)));
         r.v[i] = f.x, r.v[i + 1] = f.y, r.v[i + 2] = f.z, r.v[i + 3] = f.w;
     }
     return r;
 }
 
 template <int EPL>
-__device__ __forceinline__ Vals<EPL> load_cg(const float *p)
+__device__ __forceinline__ Vals<EPL> load_cg(const float *p, int gap)
 {
     Vals<EPL> r;
 #pragma unroll
     for (int i = 0; i < EPL; i += 4) {
-        const float4 f = __ldcg(reinterpret_cast<const float4 *>(p + i));
+        const float4 f = __ldcg(reinterpret_cast<const float4 *>(p + (i ? gap : 0)));
         r.v[i] = f.x, r.v[i + 1] = f.y, r.v[i + 2] = f.z, r.v[i + 3] = f.w;
     }
     return r;
 }
 
 // One cache entry's EPL values: rounded once to 16 bits, to nearest even.
-template <int EPL, class T>
-__device__ __forceinline__ void store16(uint8_t *dst, const Vals<EPL> &x)
+template <int EPL, bool SPLIT, class T>
+__device__ __forceinline__ void store16(uint8_t *dst, const Vals<EPL> &x, int gap)
 {
     alignas(16) T t[EPL];
 #pragma unroll
@@ -94,18 +94,20 @@ __device__ __forceinline__ void store16(uint8_t *dst, const Vals<EPL> &x)
         if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) t[i] = __float2half_rn(x.v[i]);
         else t[i] = __float2bfloat16_rn(x.v[i]);
     }
-    if constexpr (EPL == 4) *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<uint2 *>(t);
+    if constexpr (EPL == 4 || SPLIT) *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<uint2 *>(t);
     else *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<uint4 *>(t);
+    if constexpr (SPLIT) *reinterpret_cast<uint2 *>(dst + 2 * gap) = *reinterpret_cast<uint2 *>(t + 4);
 }
 
 // A group of heads: where it is read, its biases, and its first head.
 struct alignas(16) Group {
     const float *src, *bias;
     float *dst;             // queries: their place in q_out
-    int kind, head, heads;  // 0 queries, 1 keys, 2 values; heads that exist (1 or 2)
+    int kind, head, heads;  // 0 queries, 1 keys, 2 values; heads that exist (1 to 4)
 };
 
-template <int EPL>
+// SPLIT: a lane's 8 values are 4 and their 4 partners, half a head away (MQ_ROPE_HALF of whole heads).
+template <int EPL, bool SPLIT>
 __global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(const RopeAppendLaunch a)
 {
     constexpr int kBatch = kLoads * 4 / EPL;  // groups a warp loads at a time
@@ -113,28 +115,29 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(con
     __shared__ float cosine[128], sine[128];
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, D = a.head_dim;
-    const int two = a.two_heads, lph = 32 >> two;  // lanes of a head: 16 (two heads a group) or 32
+    const int lg = a.heads_log, lph = 32 >> lg;  // a group is 1 << lg heads, of lph lanes each
     const int half = a.rope_dims >> 1;
-    const int sub = lane >= lph ? 1 : 0, e = (lane & (lph - 1)) * EPL;  // this lane's head of a group, first value
-    const bool in_head = e < D, rotated = e < a.rope_dims;
+    const int sub = lane / lph, e = (lane & (lph - 1)) * (SPLIT ? 4 : EPL);  // this lane's head of a group, first value
+    const int gap = SPLIT ? half : 4;                   // from its first four values to the others
+    const bool in_head = e < (SPLIT ? half : D), rotated = e < a.rope_dims;
     const bool upper = e >= half;  // MQ_ROPE_HALF: the b of its pairs
     const int from = (lane + (rotated ? (upper ? -half : half) / EPL : 0)) & 31;
 
     // this CTA's row and groups
     const int t = blockIdx.y + blockIdx.z * kGridRows, c = blockIdx.x;
     if (t >= a.nt) return;
-    const int gq = (a.n_heads + two) >> two, gk = (a.n_kv_heads + two) >> two;
+    const int more = (1 << lg) - 1, gq = (a.n_heads + more) >> lg, gk = (a.n_kv_heads + more) >> lg;
     const int first = c * a.groups_per_cta, n = min(a.groups_per_cta, gq + 2 * gk - first);
     for (int i = tid; i < n; i += kWarps * 32) {
         const int gr = first + i, kind = gr < gq ? 0 : gr < gq + gk ? 1 : 2;
-        const int h = (kind == 0 ? gr : kind == 1 ? gr - gq : gr - gq - gk) << two;
+        const int h = (kind == 0 ? gr : kind == 1 ? gr - gq : gr - gq - gk) << lg;
         const float *bias = kind == 0 ? a.q_bias : kind == 1 ? a.k_bias : a.v_bias;
         Group &g = groups[i];
         g.src = (kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride) + h * D;
         g.bias = bias ? bias + h * D : nullptr;
         g.dst = a.q_out + t * a.q_out_stride + h * D;
         g.kind = kind, g.head = h;
-        g.heads = min(1 + two, (kind == 0 ? a.n_heads : a.n_kv_heads) - h);
+        g.heads = min(1 + more, (kind == 0 ? a.n_heads : a.n_kv_heads) - h);
     }
     const unsigned long long step = tid < half ? __ldg(a.rope_table + tid) : 0;  // no preceding kernel writes it
     __syncthreads();
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(con
             const int i = i0 + k * kWarps;
 #pragma unroll
             for (int j = 0; j < EPL; ++j) x[k].v[j] = 0.0f;
-            if (i < n && in_head && sub < groups[i].heads) x[k] = load_cg<EPL>(groups[i].src + sub * D + e);
+            if (i < n && in_head && sub < groups[i].heads) x[k] = load_cg<EPL>(groups[i].src + sub * D + e, gap);
         }
     };
     load(warp);  // on their way while the page and the angles are found
@@ -167,10 +170,15 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(con
     const bool ok = (unsigned)page < (unsigned)a.n_pages;
     const size_t page_at = (size_t)(ok ? page : 0) * a.page_stride, slot_at = (size_t)slot * D + e;
     __syncthreads();
-    float cs[EPL], sn[EPL];
+    constexpr int kAngles = SPLIT ? 4 : EPL;
+    float cs[kAngles], sn[kAngles];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
+    for (int i = 0; i < kAngles; ++i) {
         cs[i] = 1.0f, sn[i] = 0.0f;
+        if (SPLIT) {
+            if (in_head) cs[i] = cosine[e + i], sn[i] = sine[e + i];
+            continue;
+        }
         if (!rotated) continue;
         const int at = a.style == 0 ? e + i - (upper ? half : 0) : (e + i) >> 1;
         cs[i] = cosine[at];
@@ -187,7 +195,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(con
             const int kind = g.kind;
             const bool valid = in_head && sub < g.heads;
             if (g.bias && valid) {
-                const Vals<EPL> b = load_weight<EPL>(g.bias + sub * D + e);
+                const Vals<EPL> b = load_weight<EPL>(g.bias + sub * D + e, gap);
 #pragma unroll
                 for (int j = 0; j < EPL; ++j) x[k].v[j] += b.v[j];
             }
@@ -200,12 +208,19 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(con
                     for (int o = lph >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
                     if (valid) {
                         const float scale = 1.0f / sqrtf(ss / (float)D + a.eps);
-                        const Vals<EPL> w = load_weight<EPL>(gain + e);
+                        const Vals<EPL> w = load_weight<EPL>(gain + e, gap);
 #pragma unroll
                         for (int j = 0; j < EPL; ++j) x[k].v[j] = (x[k].v[j] * scale) * w.v[j];
                     }
                 }
-                if (half > 0) {
+                if constexpr (SPLIT) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float lo = x[k].v[j], hi = x[k].v[EPL - 4 + j];
+                        x[k].v[j] = fmaf(lo, cs[j], hi * -sn[j]);
+                        x[k].v[EPL - 4 + j] = fmaf(hi, cs[j], lo * sn[j]);
+                    }
+                } else if (half > 0) {
                     Vals<EPL> p;
                     if (a.style == 0) {
 #pragma unroll
@@ -224,7 +239,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(con
                         float *dst = g.dst + sub * D + e;
 #pragma unroll
                         for (int j = 0; j < EPL; j += 4)
-                            *reinterpret_cast<float4 *>(dst + j) =
+                            *reinterpret_cast<float4 *>(dst + (j ? gap : 0)) =
                                 make_float4(x[k].v[j], x[k].v[j + 1], x[k].v[j + 2], x[k].v[j + 3]);
                     }
                     continue;
@@ -233,28 +248,34 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(con
             uint8_t *base = (kind == 1 ? a.k_pages : a.v_pages) + page_at + (size_t)(g.head + sub) * a.head_bytes;
             const bool cached = valid && ok;  // the first use of the page: the queries do not wait for it
             if (a.type == 1) {
-                if (cached) store16<EPL, __half>(base + slot_at * 2, x[k]);
+                if (cached) store16<EPL, SPLIT, __half>(base + slot_at * 2, x[k], gap);
             } else if (a.type == 2) {
-                if (cached) store16<EPL, __nv_bfloat16>(base + slot_at * 2, x[k]);
+                if (cached) store16<EPL, SPLIT, __nv_bfloat16>(base + slot_at * 2, x[k], gap);
             } else {
-                float am = 0.0f;
+                // blocks of 32 values: 32 / EPL lanes, or 8 lanes' fours
+                constexpr int kPer = SPLIT ? 4 : EPL;
 #pragma unroll
-                for (int j = 0; j < EPL; ++j) am = fmaxf(am, fabsf(x[k].v[j]));
+                for (int i = 0; i < EPL; i += kPer) {
+                    float am = 0.0f;
 #pragma unroll
-                for (int o = 1; o < 32 / EPL; o <<= 1) am = fmaxf(am, __shfl_xor_sync(kFull, am, o));
-                const float d = am / 127.0f;
-                const float di = (d != 0.0f) ? 1.0f / d : 0.0f;
-                uint32_t w[EPL / 4];
+                    for (int j = 0; j < kPer; ++j) am = fmaxf(am, fabsf(x[k].v[i + j]));
 #pragma unroll
-                for (int j = 0; j < EPL; ++j) {
-                    const int q = max(-128, min(127, __float2int_rn(x[k].v[j] * di)));
-                    w[j / 4] = (j & 3) ? w[j / 4] | ((uint32_t)(q & 0xff) << (8 * (j & 3))) : (uint32_t)(q & 0xff);
-                }
-                if (cached) {
+                    for (int o = 1; o < 32 / kPer; o <<= 1) am = fmaxf(am, __shfl_xor_sync(kFull, am, o));
+                    const float d = am / 127.0f;
+                    const float di = (d != 0.0f) ? 1.0f / d : 0.0f;
+                    uint32_t w[kPer / 4];
 #pragma unroll
-                    for (int j = 0; j < EPL / 4; ++j) reinterpret_cast<uint32_t *>(base + slot_at)[j] = w[j];
-                    if ((e & 31) == 0)
-                        reinterpret_cast<__half *>(base + (size_t)a.page_size * D)[slot_at >> 5] = __float2half_rn(d);
+                    for (int j = 0; j < kPer; ++j) {
+                        const int q = max(-128, min(127, __float2int_rn(x[k].v[i + j] * di)));
+                        w[j / 4] = (j & 3) ? w[j / 4] | ((uint32_t)(q & 0xff) << (8 * (j & 3))) : (uint32_t)(q & 0xff);
+                    }
+                    if (cached) {
+                        const size_t at = slot_at + (i ? gap : 0);
+#pragma unroll
+                        for (int j = 0; j < kPer / 4; ++j) reinterpret_cast<uint32_t *>(base + at)[j] = w[j];
+                        if ((e & 31) == 0)
+                            reinterpret_cast<__half *>(base + (size_t)a.page_size * D)[at >> 5] = __float2half_rn(d);
+                    }
                 }
             }
         }
@@ -266,7 +287,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(con
             const float nan = __int_as_float(0x7fc00000);
 #pragma unroll
             for (int j = 0; j < EPL; j += 4)
-                *reinterpret_cast<float4 *>(g.dst + sub * D + e + j) = make_float4(nan, nan, nan, nan);
+                *reinterpret_cast<float4 *>(g.dst + sub * D + e + (j ? gap : 0)) = make_float4(nan, nan, nan, nan);
         }
         if (a.status && c == 0 && tid == 0) atomicOr(a.status, 1);
     }
@@ -277,13 +298,18 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(con
 cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_t st)
 {
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
-    // 8 values a lane where the warps are enough all the same (40 + 8 + 8 heads of 128, EPL 4 and 8: 1 row 2.7
-    // and 3.0 us, 16 rows 3.3 and 3.3, 64 rows 4.6 and 3.9, 256 rows 5.2 and 6.0, 1024 rows 16.9 and 16.5,
-    // 4096 rows 47 and 43)
-    const long long heads = a.n_heads + 2 * a.n_kv_heads;
-    const bool wide = a.head_dim > 128 || (a.head_dim > 64 && a.rope_dims % 16 == 0 && a.nt * heads >= (long long)sms * 8);
-    a.two_heads = a.head_dim <= (wide ? 128 : 64) ? 1 : 0;
-    const int groups = ((a.n_heads + a.two_heads) >> a.two_heads) + 2 * ((a.n_kv_heads + a.two_heads) >> a.two_heads);
+    // 8 values a lane, partners in one lane, where pairs lie half a head apart and halves are whole blocks of q8.
+    // Else 8 where rows are many. (Captured, us, 4 values / 8, 8 with partners: 40 + 8 + 8 heads of 128, biases: 1 row
+    // 2.7 / 2.9, 2.6; 24 rows 3.3 / 3.5, 3.1; 64 rows 4.7 / 3.9, 3.4; 256 rows 5.1 / 5.9, 4.7; 1024 rows 17.9 / 16.9, 14.4;
+    // 4096 rows 47 / 43, 39. q8, 28 + 4 + 4 heads: 1 row 3.1 / -, 3.3; 64 rows 4.1 / -, 3.9; 1024 rows 15.4 / -, 12.5.
+    // Heads of 64: 64 rows 3.5 / 3.6, 3.1; 1024 rows 7.8 / 7.4, 6.)
+    const long long heads = (long long)a.nt * (a.n_heads + 2 * a.n_kv_heads);
+    const bool many = heads >= sms * (a.head_dim > 64 ? 8LL : 128LL);
+    const bool q8 = a.type == 3, partners = a.style == 0 && a.rope_dims == a.head_dim && (!q8 || a.head_dim % 64 == 0);
+    const bool wide = a.head_dim > 128 || (partners ? !q8 || heads >= sms * 8LL : many && a.rope_dims % 16 == 0);
+    a.heads_log = wide ? (a.head_dim <= 64 ? 2 : a.head_dim <= 128 ? 1 : 0) : a.head_dim <= 64 ? 1 : 0;
+    const int more = (1 << a.heads_log) - 1;
+    const int groups = ((a.n_heads + more) >> a.heads_log) + 2 * ((a.n_kv_heads + more) >> a.heads_log);
     // Few rows: a group a warp, for latency.  More: up to kUnits groups a warp (as many values for 8 a lane),
     // which share the row's angles and its page.
     const int most = wide ? kUnits / 2 : kUnits;
@@ -293,7 +319,9 @@ cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_
     const int ctas = (groups + (int)units * kWarps - 1) / ((int)units * kWarps);
     a.groups_per_cta = ((groups + ctas - 1) / ctas + kWarps - 1) / kWarps * kWarps;  // alike, whole warps' groups
     const dim3 grid((unsigned)ctas, (unsigned)std::min(a.nt, kGridRows), (unsigned)((a.nt + kGridRows - 1) / kGridRows));
-    const auto kernel = wide ? rope_append_kernel<8> : rope_append_kernel<4>;
+    const auto kernel = wide && partners ? rope_append_kernel<8, true>
+                        : wide           ? rope_append_kernel<8, false>
+                                         : rope_append_kernel<4, false>;
     return launch_maybe_pdl(kernel, grid, dim3(kWarps * 32), 0, pdl, st, a);
 }
 

@@ -132,11 +132,12 @@ def test_row_counts_and_groups(mq, nt, hq, hkv):
 @pytest.mark.parametrize("kv", ["f16", "bf16", "q8"])
 @pytest.mark.parametrize("hq,hkv", [(7, 1), (9, 3), (40, 8)])
 @pytest.mark.parametrize("d,r,style", [(128, 128, "half"), (128, 16, "half"), (128, 24, "half"), (128, 80, "pairs"),
-                                       (96, 96, "half"), (96, 64, "pairs"), (96, 0, "half")])
-def test_many_rows_two_heads_a_warp(mq, kv, hq, hkv, d, r, style):
-    """Heads of 65 to 128 values go two a warp when rows are many: odd counts, heads of 96 in 12 of 16
-    lanes, and rotations whose pairs do not lie whole lanes apart (24), which stay one a warp."""
-    nt = 1250 // (hq + 2 * hkv) + 9
+                                       (96, 96, "half"), (96, 64, "pairs"), (96, 0, "half"), (64, 64, "half"),
+                                       (64, 32, "half"), (64, 64, "pairs")])
+def test_many_rows_several_heads_a_warp(mq, kv, hq, hkv, d, r, style):
+    """Heads go two (65 to 128 values) or four a warp when rows are many: odd counts, heads of 96 in 12 of 16
+    lanes, and rotations whose pairs do not lie whole lanes apart (24), which stay as they are for few rows."""
+    nt = (1250 if d > 64 or (r == 64 and style == "half") else 19600) // (hq + 2 * hkv) + 9
     c = Case(nt, hq, hkv, d, r, style, kv, 16, hkv != 8, True, [(i * 37) % 500 for i in range(nt)], pad=3)
     c.check(*c.run(mq))
 
