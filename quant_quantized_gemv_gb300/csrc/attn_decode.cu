@@ -783,6 +783,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
             constexpr int kMeet = S::meet * D / 4;  // float4s of these heads
 #pragma unroll 1
             for (int i0 = 0; i0 < kMeet; i0 += kThreads) {
+                if (kMeet > kThreads && h0 + i0 / (D / 4) >= heads) break;  // heads that do not exist: a turn less
                 const int i = i0 + tid, hh = i / (D / 4), d = (i - hh * (D / 4)) * 4, h = h0 + hh;
                 const bool in_range = i < kMeet;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -857,6 +858,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                 __syncthreads();
 #pragma unroll 1
                 for (int i0 = 0; i0 < kSlots; i0 += kThreads) {
+                    if (kSlots > kThreads && i0 / (D / 4) >= heads) break;
                     const int idx = i0 + tid, h = min(idx / (D / 4), kAttnHeads - 1);
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                     for (int p0 = 0; p0 < pieces; p0 += kAhead) {
