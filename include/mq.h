@@ -427,6 +427,7 @@ int mq_check_coverage(int nchunks, int splits, int chunks_per_split);
  * on only when the kernel that directly precedes a GEMV in the stream does
  * not write that GEMV's weight matrix, nor the kernel before an rms
  * producer its gain (both are weights in a decode step).
+ * mq_rope_append, mq_attn_decode and mq_sample read nothing before they wait.
  * ------------------------------------------------------------------------ */
 int mq_set_pdl(int enable);
 

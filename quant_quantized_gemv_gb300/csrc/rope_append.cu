@@ -59,14 +59,14 @@ struct Vals {
     float v[EPL];
 };
 
-// Biases and gains are weights, which no preceding kernel writes.
+// Biases and gains: shared by many rows, so through L1, but coherent: a preceding kernel may have written them.
 template <int EPL>
 __device__ __forceinline__ Vals<EPL> load_weight(const float *p, int gap)
 {
     Vals<EPL> r;
 #pragma unroll
     for (int i = 0; i < EPL; i += 4) {
-        const float4 f = __ldg(reinterpret_cast<const float4 *>(p + (i ? gap : 0)));
+        const float4 f = __ldca(reinterpret_cast<const float4 *>(p + (i ? gap : 0)));
         r.v[i] = f.x, r.v[i + 1] = f.y, r.v[i + 2] = f.z, r.v[i + 3] = f.w;
     }
     return r;
@@ -139,10 +139,10 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) rope_append_kernel(con
         g.kind = kind, g.head = h;
         g.heads = min(1 + more, (kind == 0 ? a.n_heads : a.n_kv_heads) - h);
     }
-    const unsigned long long step = tid < half ? __ldg(a.rope_table + tid) : 0;  // no preceding kernel writes it
     __syncthreads();
-    griddep_wait();  // q, k, v (and the positions) may come from the preceding kernels
+    griddep_wait();  // nothing is read before: any of the inputs may come from the preceding kernels
 
+    const unsigned long long step = tid < half ? __ldca(a.rope_table + tid) : 0;
     const int pos = __ldcg(a.positions + t);
     Vals<EPL> x[kBatch];
     auto load = [&](int i0) {

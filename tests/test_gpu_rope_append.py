@@ -338,3 +338,44 @@ def test_queries_made_for_another_stream_are_of_its_memory(mq):
     out = mq.mq_rope_append(kv, q, k, v, pos, table, stream=st)
     st.synchronize()
     assert out.data_ptr() != given_back and torch.equal(out, q)
+
+
+@pytest.mark.parametrize("d,style,norm", [(128, "half", True), (64, "pairs", False)])
+def test_inputs_written_just_before_under_pdl(mq, d, style, norm):
+    """The kernel right before writes the rotation's table, a bias, a gain, the positions or the page table
+    of a captured step with programmatic dependent launch: nothing is read before it has finished."""
+    import torch
+    c = Case(24, 8, 2, d, d, style, "f16", 16, True, norm, [3 + 17 * i for i in range(24)], key="pdl")
+    want_q, want = c.run(mq)
+    torch.cuda.synchronize()
+    args = dict(rope=mq.mq_rope_table(c.freqs), q_bias=dev(c.qb), k_bias=dev(c.kb), v_bias=dev(c.vb),
+                q_gain=dev(c.qg), k_gain=dev(c.kg))
+    fixed = dict(positions=dev(c.pos), pages=dev(c.table))
+    big = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    sink = torch.empty_like(big)
+    for name, new in [*args.items(), *fixed.items()]:
+        if new is None:
+            continue
+        live = torch.zeros_like(new)
+        call = {**args, **fixed, name: live}
+        positions, pages = call.pop("positions"), call.pop("pages")
+        kv = mq.MQKVCache(c.kv, c.n_pages, c.ps, c.hkv, c.d)
+        q, k, v, q_out = dev(c.q), dev(c.k), dev(c.v), torch.full((c.rows, c.hq * d), 5.0, device="cuda")
+        whole = new.numel() * new.element_size() // 16 * 16       # what mq_copy takes; the rest is there already
+        live.view(torch.uint8).view(-1)[whole:] = new.view(torch.uint8).view(-1)[whole:]
+        old = live.clone()
+        mq.mq_set_pdl(True)
+        try:
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr, stream=torch.cuda.Stream()):
+                mq.mq_copy(sink, big)                              # what the copy behind it waits for
+                mq.mq_copy(live, new, whole)
+                mq.mq_rope_append(kv, q, k, v, positions, pages, q_out=q_out, style=style, eps=1e-6, **call)
+        finally:
+            mq.mq_set_pdl(False)
+        for _ in range(3):
+            live.copy_(old), kv.k.fill_(9.0), kv.v.fill_(9.0), q_out.fill_(5.0)
+            gr.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(q_out, want_q), name
+            assert torch.equal(kv.k, want.k) and torch.equal(kv.v, want.v), name
