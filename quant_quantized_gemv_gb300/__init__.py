@@ -21,7 +21,6 @@ import numpy as np
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _SO = os.path.join(_PKG, "_build", "libmq.so")
-_BINDING = os.path.join(_PKG, "_build", "mq_binding.so")
 _lib = None
 
 (MQ_OK, MQ_ERR_SHAPE, MQ_ERR_ALIGN, MQ_ERR_NULL, MQ_ERR_COVERAGE, MQ_ERR_WORKSPACE, MQ_ERR_CUDA,
@@ -795,10 +794,11 @@ def _bind():
     import torch  # noqa: F401  (its libraries must be loaded first)
     from importlib.machinery import ExtensionFileLoader
     from importlib.util import module_from_spec, spec_from_file_location
-    L = lib()
-    if not os.path.exists(_BINDING):
-        raise FileNotFoundError(f"{_BINDING} is missing: run build()")
-    spec = spec_from_file_location("mq_binding", _BINDING, loader=ExtensionFileLoader("mq_binding", _BINDING))
+    from .build import binding
+    L, path = lib(), binding()
+    if not os.path.exists(path):
+        raise FileNotFoundError(f"{path} is missing: run build()")
+    spec = spec_from_file_location("mq_binding", path, loader=ExtensionFileLoader("mq_binding", path))
     m = module_from_spec(spec)
     spec.loader.exec_module(m)
     m.setup(*(ctypes.cast(f, ctypes.c_void_p).value

@@ -4,12 +4,14 @@ nvcc compiles every translation unit of csrc/ in parallel (one -gencode,
 sm_103a only, no fast-math so that the producers' IEEE division, reciprocal
 and rounding match the definition), then links a shared library against the
 shared CUDA runtime.  Output: quant_quantized_gemv_gb300/_build/libmq.so.
-Beside it _build/mq_binding.so, a Python module over torch's headers, with the
-calls of the operators that name many tensors (csrc/binding.cpp).
+That needs nvcc alone.  Beside it, where torch is installed, a Python module over
+its headers with the calls of the operators that name many tensors
+(csrc/binding.cpp), in a file named after the Python and the torch it is for.
 """
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -22,7 +24,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 SO = os.path.join(BUILD, "libmq.so")
-BINDING = os.path.join(BUILD, "mq_binding.so")
 SOURCES = ["gemv.cu", "gemv_batch.cu", "gemv_gateup.cu", "gemv_f32.cu", "producers.cu", "noalloc.cu",
            "readfloor.cu", "copy.cu", "repack_device.cu", "rope_append.cu", "attn_decode.cu", "sample.cu",
            "api.cpp", "repack.cpp", "decode.cpp"]
@@ -34,14 +35,27 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else (shutil.which("nvcc") or "nvcc")
 
 
-def _torch() -> str:
-    return find_spec("torch").submodule_search_locations[0]
+def _torch() -> tuple[str, str] | None:
+    """Where torch lies and its version, without an import; None where there is none."""
+    spec = find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    path = spec.submodule_search_locations[0]
+    with open(os.path.join(path, "version.py")) as f:
+        return path, re.search(r"^__version__\s*=\s*['\"]([^'\"]+)", f.read(), re.M)[1]
+
+
+def binding() -> str | None:
+    """The module of the Python calls for this Python and torch; None without torch."""
+    torch = _torch()
+    return torch and os.path.join(BUILD, f"mq_binding.{sysconfig.get_config_var('SOABI')}.torch-{torch[1]}.so")
 
 
 def _stale() -> bool:
-    if not os.path.exists(SO) or not os.path.exists(BINDING):
+    made = [f for f in (SO, binding()) if f]
+    if not all(os.path.exists(f) for f in made):
         return True
-    t = min(os.path.getmtime(SO), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(f) for f in made)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "mq.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -51,9 +65,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return SO
     os.makedirs(BUILD, exist_ok=True)
     common = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
-    torch = _torch()
-    headers = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, src + ".o")
@@ -61,6 +72,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if src.endswith(".cu"):
             cmd[1:1] = [*ARCH, "-lineinfo", "-Xptxas", "-v" if verbose else "-O3"]
         if src == "binding.cpp":
+            headers = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+                       sysconfig.get_paths()["include"],
+                       os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
             cmd[1:1] = [x for h in headers for x in ("-I", h)]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -77,12 +91,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, so)
 
+    so, torch = binding(), (_torch() or [None])[0]
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        *objs, binding = ex.map(compile_one, SOURCES + ["binding.cpp"])
-    link(SO, objs, [])
-    lib = os.path.join(torch, "lib")
-    link(BINDING, [binding], ["-L", lib, "-Xlinker", "-rpath", "-Xlinker", lib, "-ltorch_python", "-ltorch_cpu",
-                              "-lc10_cuda", "-lc10"])
+        calls = ex.submit(compile_one, "binding.cpp") if so else None
+        link(SO, list(ex.map(compile_one, SOURCES)), [])
+    if calls:
+        lib = os.path.join(torch, "lib")
+        link(so, [calls.result()], ["-L", lib, "-Xlinker", "-rpath", "-Xlinker", lib, "-ltorch_python", "-ltorch_cpu",
+                                    "-lc10_cuda", "-lc10"])
     return SO
 
 

@@ -288,3 +288,76 @@ def test_reference_rotation_by_hand():
     assert np.allclose(half, [[[0.0, 0.0, 1.0, -2.0]]])
     pairs, _ = ref.rotate(x, np.abs(x), [1], f, "pairs")                # pairs (0, 1), (2, 3)
     assert np.allclose(pairs, [[[0.0, 1.0, 0.0, -2.0]]])
+
+
+# ------------------------------------------------------------------ the build
+class Compiler:
+    """Stands for nvcc: writes what a command names as its output; refuses a source."""
+
+    def __init__(self, refuse=None):
+        self.commands, self.refuse = [], refuse
+
+    def __call__(self, cmd, **_):
+        import types
+        self.commands.append(cmd)
+        if self.refuse and any(str(x).endswith(self.refuse) for x in cmd):
+            return types.SimpleNamespace(returncode=1, stdout="", stderr="no")
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+
+@pytest.fixture
+def elsewhere(monkeypatch, tmp_path):
+    from quant_quantized_gemv_gb300 import build as b
+    monkeypatch.setattr(b, "BUILD", str(tmp_path))
+    monkeypatch.setattr(b, "SO", str(tmp_path / "libmq.so"))
+    return b
+
+
+def torch_at(path, version):
+    import types
+    path.mkdir(exist_ok=True)
+    (path / "version.py").write_text(f"__version__ = '{version}'\n")
+    return lambda name: types.SimpleNamespace(submodule_search_locations=[str(path)])
+
+
+def test_the_library_builds_without_torch(elsewhere, monkeypatch, tmp_path):
+    """The C ABI needs nvcc alone; the Python calls over torch's headers are left out."""
+    cc = Compiler()
+    monkeypatch.setattr(elsewhere, "find_spec", lambda name: None)
+    monkeypatch.setattr(elsewhere.subprocess, "run", cc)
+    assert elsewhere.build(force=True) == str(tmp_path / "libmq.so") and (tmp_path / "libmq.so").exists()
+    assert not any("binding" in str(x) for c in cc.commands for x in c)
+    assert not elsewhere._stale()
+
+
+def test_the_library_is_linked_before_the_calls_over_torch(elsewhere, monkeypatch, tmp_path):
+    cc = Compiler(refuse="binding.cpp")
+    monkeypatch.setattr(elsewhere, "find_spec", torch_at(tmp_path / "torch", "1.0"))
+    monkeypatch.setattr(elsewhere.subprocess, "run", cc)
+    with pytest.raises(RuntimeError, match="binding.cpp"):
+        elsewhere.build(force=True)
+    assert (tmp_path / "libmq.so").exists()
+    cc.refuse = None
+    monkeypatch.setattr(elsewhere, "find_spec", lambda name: None)
+    assert not elsewhere._stale()
+
+
+def test_another_torch_has_calls_of_its_own(elsewhere, monkeypatch, tmp_path):
+    """What was compiled over one torch's headers is not taken for another's."""
+    monkeypatch.setattr(elsewhere.subprocess, "run", Compiler())
+    monkeypatch.setattr(elsewhere, "find_spec", torch_at(tmp_path / "torch", "1.0"))
+    elsewhere.build()
+    assert not elsewhere._stale()
+    monkeypatch.setattr(elsewhere, "find_spec", torch_at(tmp_path / "torch", "1.1+x"))
+    assert elsewhere._stale()
+    elsewhere.build()
+    assert not elsewhere._stale()
+    monkeypatch.setattr(elsewhere.sysconfig, "get_config_var", lambda name: "cpython-399-there")
+    assert elsewhere._stale()
+
+
+def test_the_calls_are_those_of_the_torch_that_runs(mq):
+    import torch
+    from quant_quantized_gemv_gb300 import build as b
+    assert torch.__version__ in b.binding() and mq._bind().__file__ == b.binding()
