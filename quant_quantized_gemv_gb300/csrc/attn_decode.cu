@@ -516,8 +516,9 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
             }
             am = fmaxf(am, __shfl_xor_sync(kFull, am, 1));
             am = fmaxf(am, __shfl_xor_sync(kFull, am, 2));
-            // 2^(13 - exponent), within f32's normal range both ways
-            const int e = min(max((int)(__float_as_uint(am) >> 23) - 127, -100), 100);
+            // 2^(13 - exponent), a normal number as its inverse is: of every finite magnitude down to 2^-113, and what
+            // is smaller still keeps its 22 bits
+            const int e = min(max((int)(__float_as_uint(am) >> 23) - 127, -113), 127);
             up = __uint_as_float((unsigned)(127 + 13 - e) << 23);
             q_factor = __uint_as_float((unsigned)(127 - 13 + e) << 23);
         }

@@ -405,3 +405,14 @@ def test_refusals(mq):
         with pytest.raises(mq.MQError) as e:
             call(**bad)
         assert e.value.status == status, bad
+
+
+@pytest.mark.parametrize("kv,q_std", [("f16", 5e30), ("f16", 1e33), ("f16", 5e37), ("q8", 1e33), ("q8", 5e37),
+                                      ("bf16", 1e33)])
+def test_the_largest_queries(mq, kv, q_std):
+    """Queries of every finite magnitude, under a scale that brings their scores back: the factor of a head's
+    parts follows its largest value to the end of f32.  (bf16 sums q k itself, so less room.)"""
+    c = Case(mq, kv, 128, 8, 2, 16, [1, 50, 600], q_std=q_std)
+    assert np.isfinite(c.q).all()
+    c.scale = 2 / (math.sqrt(128) * q_std)
+    c.check(c.run())
