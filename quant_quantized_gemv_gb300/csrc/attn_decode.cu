@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
 
     // ---- the working side
     const bool capped = a.softcap > 0.0f;
-    const float inv_cap = capped ? 1.0f / a.softcap : 0.0f;
+    const float inv_cap = capped ? fminf(1.0f / a.softcap, 3.4e38f) : 0.0f;  // finite: a score of 0 stays 0
     int stage = 0;
     for (int count = 0;; ++count) {
         const int kvh = kv_head(at.unit), sg = at.unit - kvh * a.subgroups;

@@ -416,3 +416,12 @@ def test_the_largest_queries(mq, kv, q_std):
     assert np.isfinite(c.q).all()
     c.scale = 2 / (math.sqrt(128) * q_std)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16", "q8"])
+@pytest.mark.parametrize("cap", [1e-30, 1e-39, 1e-44])
+def test_caps_whose_inverse_overflows(mq, kv, cap):
+    """A cap that leaves nothing of any score, over scores of 0 and others: the mean of the values."""
+    c = Case(mq, kv, 64, 4, 2, 16, [90, 1, 300])
+    c.q.reshape(3, 4, 64)[:, ::2] = 0.0
+    c.check(c.run(softcap=cap), softcap=cap)
