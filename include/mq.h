@@ -699,8 +699,10 @@ int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *args, void *stream
  * u times their sum; prob is its share of that sum.
  *   temperature <= 0 (or NaN): the largest logit, the lowest index where equal;
  *     prob is 1.  top_k <= 0: no such filter; top_p <= 0 keeps one token.
+ *     A temperature under 2.9e-37 counts as that.
  *   A NaN logit counts as -inf; -inf is never drawn.  A row of nothing else
  *     gives token -1 and prob 0.  Infinite logits share the draw evenly.
+ *     A logit that lies further below the largest than FLT_MAX weighs nothing.
  *   u: in [0, 1); outside it counts as the nearest end.
  * Weights are summed as 64-bit integers (2^-42 of the largest; the border of
  * top_p 2^-32), so the result depends on nothing but the inputs.

@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleLaunch a)
 
     // log2(e) / temperature in two parts: the quotient, and what its product leaves
     Weight weight;
-    weight.c_hi = fminf(1.44269502f / temperature, 1e30f);
+    weight.c_hi = fminf(1.44269502f / temperature, 5e36f);  // its product with the bins of an octave is finite
     weight.c_lo = (fmaf(-weight.c_hi, temperature, 1.44269502f) + 1.92596299e-8f) / temperature;
     if (!(fabsf(weight.c_lo) < weight.c_hi)) weight.c_lo = 0.0f;  // clamped, or an infinite temperature
     const u64 floor_w = min_p > 0.0f ? __float2ull_ru(min_p * (float)(1ull << kFixBits)) : 0;

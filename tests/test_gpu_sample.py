@@ -379,3 +379,12 @@ def test_an_estimate_that_stops_short(mq, n):
         tok, pr, kept, _ = ref.sample(x[0], float(np.float32(u)), p=float(np.float32(p)))
         assert kept.sum() == n + 1
         check(x, np.array([u], np.float32), got, p=p)
+
+
+@pytest.mark.parametrize("t", [1e-28, 1e-31, 1e-33, 1e-36])
+def test_logits_as_small_as_their_temperature(mq, t):
+    """What counts is the quotient: logits and temperature of vanishing size draw as their multiples do."""
+    x, u = rows("vanishing", 6, 3001, 2.0, 8)
+    x = (x.astype(np.float64) * t).astype(np.float32)
+    for f in (dict(), dict(k=40), dict(p=0.9), dict(k=1500, p=0.95), dict(m=0.05)):
+        check(x, u, run(mq, x, u, t=t, **f), t=t, **f)
