@@ -555,7 +555,8 @@ int mq_device_sms(void);
  * [i * page_size, (i + 1) * page_size) of sequence s, 0 <= s < n_seqs,
  * 0 <= i < pages_stride.  Row t of a call belongs to sequence seq[t], or to
  * sequence t where seq is NULL.  Entries behind a sequence's last page are
- * never read.  Tables, positions and lengths are device memory, 4-byte
+ * never used, whatever they hold (a table of up to 256 KB may be fetched into
+ * L2 as a whole).  Tables, positions and lengths are device memory, 4-byte
  * aligned, read by the kernel: a captured graph replays with their new values.
  *
  * Values on the device cannot be checked before the launch.  A row whose

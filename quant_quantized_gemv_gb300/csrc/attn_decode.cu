@@ -247,11 +247,14 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     griddep_wait();  // queries, lengths, tables and the cache may come from the preceding kernels
 
-    // The page tables and queries to L2 while the lengths are fetched: they lie on the way to the first
-    // tile, one behind the other, and a long context's stream leaves nothing of them there.
+    // A small page table and the queries to L2 while the lengths are fetched: they lie on the way to the first
+    // tile, one behind the other, and a long context's stream leaves nothing of them there. (One row of 32768: 28.6 us
+    // without the table, 28.4 with it; by the rows' lengths, once they are there, it takes 28.5 and costs short rows
+    // 0.2 us. A large table is mostly of places that no row of the call uses.)
     {
         const unsigned i = blockIdx.x * kThreads + tid;  // 128 bytes a thread
-        if ((size_t)i * 32 < (size_t)a.n_seqs * a.pages_stride)
+        const size_t entries = (size_t)a.n_seqs * a.pages_stride;
+        if (entries <= kAttnTableAhead && (size_t)i * 32 < entries)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(a.pages + (size_t)i * 32));
         const unsigned lines = a.n_heads * (D / 32), r = i / lines;
         if (r < (unsigned)a.nt)

@@ -230,6 +230,8 @@ constexpr int kAttnWhole = 2;
 // Rounds that the beginning and end of a unit are worth (63 rows of 1 to 8191 tokens, 28 and 4 heads:
 // f16 42.8 us at 0, 29.5 at 1, 28.7 at 2, 28.8 at 3; q8 42.0, 30.4, 30.6, 33.6).
 constexpr int kAttnUnitCost = 2;
+// Entries of a page table that is fetched into L2 as a whole, used or not (256 KB: 1/500 of L2, 40 ns of HBM).
+constexpr unsigned kAttnTableAhead = 65536;
 // Warps of a CTA (one CTA an SM) and stages of a warp, by cache type (MQ_KV_*) and head size: what
 // fits 227 KB, a stage being 16 tokens' K and V.  f16 heads of 128, 16 rows of 16384 tokens: 8 warps
 // 161 us, 10 warps 168.  q8, which its instructions bound: 8 warps 134 us, 12 warps 116, 16 warps (128
