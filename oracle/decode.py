@@ -138,3 +138,90 @@ def sample(logits, u, t=1.0, k=0, p=1.0, m=0.0):
     at = min(at, int(np.flatnonzero(kept)[-1]))
     lo = c[at] - weight[at]
     return at, weight[at] / c[-1], kept, min(u * c[-1] - lo, c[at] - u * c[-1]) / c[-1]
+
+
+# ------------------------------------------------------------------ sharp checks of an attention
+U = 2.0 ** -24  # half a step of f32
+
+
+def parts_of(x, kind, n):
+    """x as the sum of n successive roundings to fp16 or bf16 (float64)."""
+    rest, out = np.asarray(x, np.float64), 0.0
+    for _ in range(n):
+        if kind == "bf16":
+            b = rest.astype(np.float32).view(np.uint32).astype(np.uint64)
+            p = ((b + 0x7fff + ((b >> 16) & 1)) >> 16 << 16).astype(np.uint32).view(np.float32).astype(np.float64)
+        else:
+            p = rest.astype(np.float16).astype(np.float64)
+        out, rest = out + p, rest - p
+    return out
+
+
+def attention_in_parts(q, k, v, scale, kind, n_q, n_p):
+    """`attention` with q in n_q parts and the weights of the values in n_p parts,
+    and nothing else rounded: what an evaluation through 16-bit products loses.
+    fp16 parts are of q under a power of two that brings a head's largest value
+    to [2^13, 2^14), and of 2^14 p."""
+    hq, d = q.shape
+    hkv = len(k)
+    q = q.astype(np.float64)
+    f, g = np.ones((hq, 1)), 1.0
+    if kind == "fp16":
+        f, g = 2.0 ** (13 - np.floor(np.log2(np.abs(q).max(-1, keepdims=True)))), 2.0 ** 14
+    qg = (parts_of(q * f, kind, n_q) / f).reshape(hkv, hq // hkv, d)
+    s = np.matmul(qg, k.transpose(0, 2, 1)) * scale
+    e = np.exp(s - s.max(-1, keepdims=True))
+    return (np.matmul(parts_of(e * g, kind, n_p) / g, v) / e.sum(-1, keepdims=True)).reshape(hq, d)
+
+
+class TwoTokens:
+    """A row in which two tokens alone matter, and every rounding on the way to
+    the result can be counted: key A is one value of 1, key B another, and all
+    other keys are -1 at a third place, where the queries are large.  Value B is
+    +1 or -1, all others are 0, so a result is +-w or 0 with w = 1 / (1 + e^(s_A - s_B)).
+
+    of="queries": s_A and s_B are 8 to 16, of 24 bits, so what a query's parts
+    lose shows.  of="weights": s_A = 0 and s_B = -0.7 to 0, so that the weight of
+    B is 0.5 to 1, of 24 bits, beside the largest in the same tile of 16."""
+
+    def __init__(self, rng, hq, hkv, d, n, of):
+        self.of, grp = of, hq // hkv
+        self.q = rng.uniform(-15, 15, (hkv, grp, d)).astype(np.float32)
+        self.k, self.v = np.zeros((hkv, n, d)), np.zeros((hkv, n, d))
+        for h in range(hkv):
+            a, b, c = rng.choice(d, 3, replace=False)
+            tile = 16 * rng.integers(0, n // 16) if of == "weights" else 0
+            ta, tb = tile + rng.choice(min(16, n) if of == "weights" else n, 2, replace=False)
+            self.k[h, :, c] = -1.0
+            self.k[h, [ta, tb]] = 0.0
+            self.k[h, ta, a] = self.k[h, tb, b] = 1.0
+            self.v[h, tb] = rng.choice([-1.0, 1.0], d)
+            if of == "queries":
+                self.q[h, :, a] = rng.uniform(8, 16, grp)
+                self.q[h, :, b] = self.q[h, :, a] + rng.uniform(-2, 2, grp)
+                self.q[h, :, c] = 15.9
+            else:
+                self.q[h, :, a], self.q[h, :, b], self.q[h, :, c] = 0.0, -rng.uniform(0, 0.69, grp), 25.0
+        self.q = self.q.reshape(hq, d)
+
+    def bound(self, want, fp16):
+        """How far an f32 evaluation with every part may be off, value by value.
+        s: fp16 parts end 2^-23 below a head's largest query, bf16's three hold
+        all of it; their sum rounds 2, the factor 1 (its own 3 roundings are
+        common, so relative to s_A - s_B), the difference to the maximum 1;
+        exp2: 2 ulp = 4.
+        w: the parts of p 1; the sums 4 of the value's side and 6 of the
+        divisor's, two rescalings and the warps' exchange 2 each side, the
+        division and its product 2: 17, of |w|."""
+        w = np.abs(want)
+        top = np.abs(self.q).max(-1, keepdims=True)
+        s = 16.0 + 2 if self.of == "queries" else 0.69
+        gap = 2.0 if self.of == "queries" else 0.69
+        raw = (2 * 2.0 ** np.floor(np.log2(top)) if fp16 else 0.0) + 2 * s
+        return U * (w * (1 - w) * (2 * raw + 2 * s + 4 * gap + 4) + 17 * w + 1)
+
+
+def exact_mean_bound(want):
+    """The mean of whole numbers under equal scores: weights of 1 and sums under
+    2^24 are exact in f32, so the division and its product round once each."""
+    return 2.0 ** -23 * (1 + 2.0 ** -20) * np.abs(want)
