@@ -592,7 +592,8 @@ size_t mq_kv_page_bytes(int type, int n_kv_heads, int page_size, int head_dim);
  *   MQ_ROPE_PAIRS: x[2 i], x[2 i + 1].
  * The angle is kept modulo one turn in 64-bit fixed point, so far positions
  * lose nothing.  rope_table (device, 8-byte aligned) holds the rope_dims / 2
- * steps that mq_rope_table (host) makes of freqs (radians per position).
+ * steps that mq_rope_table (host) makes of freqs (radians per position); like
+ * every other input it may be written by the kernel right before.
  * rope_dims: 0 (no rotation, rope_table may be NULL) to head_dim, a multiple
  * of 8, of 16 where head_dim is 256.
  * Rows with a negative position are padding: nothing of them is written.  Two
@@ -705,8 +706,9 @@ int mq_attn_decode(const mq_kv_cache *kv, const mq_attn_args *args, void *stream
  *     gives token -1 and prob 0.  Infinite logits share the draw evenly.
  *     A logit that lies further below the largest than FLT_MAX weighs nothing.
  *   u: in [0, 1); outside it counts as the nearest end.
- * Weights are summed as 64-bit integers (2^-42 of the largest; the border of
- * top_p 2^-32), so the result depends on nothing but the inputs.
+ * Weights are summed as 64-bit integers, in units of 2^-42 of the largest, and
+ * top_p's share of a sum is exact, rounded up to such a unit, so the result
+ * depends on nothing but the inputs.
  *   logits: nt rows of vocab f32 (4-byte aligned, any stride >= vocab).
  *   temperature, top_k, top_p, min_p: one value a row (device), or NULL: 1, and
  *     no filter.  u, token: one a row.  prob: one a row, or NULL.

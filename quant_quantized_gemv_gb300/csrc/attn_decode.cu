@@ -5,10 +5,14 @@
 //   maximum m and sum l:  m' = max(m, s),  l = l e^(m - m') + e^(s - m'), and
 //   the same for the sum of p v.
 //
-// Every cached byte is used by the 1..8 query heads of its kv head, a handful
-// of operations a byte: the pass is bound by HBM when contexts are long and
-// by latency when they are short, never by the tensor cores.  tcgen05 products
-// would fill 8 of their 128 rows and hand every tile over twice.
+// A unit of work reads its cached bytes for 1 to 8 query heads of a kv head, a
+// handful of operations a byte: the pass is bound by HBM when contexts are long
+// and by latency when they are short, never by the tensor cores.  tcgen05
+// products would fill 8 of their 128 rows and hand every tile over twice.  Where
+// a kv head has more query heads, or several rows name one sequence, each unit
+// reads the cache for itself, partly from L2: 16 rows of 16384 tokens over one kv
+// head, 8 query heads 28 us, 16 41 us (q8 25 and 37); one row of 32768, 40 and 8
+// heads, 28 us, 4 such rows of one sequence 64 us.
 //
 // Each warp streams its tokens, 16 at a time (a tile), through stages of its
 // own in shared memory, filled by 16-byte asynchronous copies: no warp waits for
@@ -49,8 +53,8 @@
 // kAttnWhole rounds or less are not cut: the join costs more than they do.
 //
 // Measured (GB300, captured): 16 rows of 16384 tokens, 40 and 8 heads of 128:
-// f16 and bf16 159 us, 6.68 TB/s of the cache, the rate of a plain copy; q8 116
-// us, 4.9 TB/s, bound by 650 instructions a tile (f16: 350), a quarter of them
+// f16 and bf16 159 us, 6.68 TB/s of the cache, the rate of a plain copy; q8 117
+// us, 4.9 TB/s, bound by 650 instructions a tile (f16: 360), a quarter of them
 // to turn codes into fp16.  One row of 32768 tokens: 28.5 us, where the bytes
 // take 20; of the rest 3 us pass before the first copy (length, page, launch)
 // and 3 in the join.  One row of 117 tokens: 5.1 us, all of it latency.

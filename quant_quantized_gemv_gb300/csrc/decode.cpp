@@ -129,7 +129,7 @@ int mq_rope_append(const mq_kv_cache *kv, const mq_rope_append_args *a, void *st
     if (a->rope_dims > 0 && !a->rope_table) return MQ_ERR_NULL;
     if (a->q_stride < nq || a->q_out_stride < nq || a->k_stride < nk || a->v_stride < nk)
         return MQ_ERR_SHAPE;
-    // one CTA per row at the least: the grid's x dimension holds 2^31 - 1
+    // rows lie along the grid's y (32768 of them) and z (65535 at most), a row's CTAs along x: well inside
     if ((long long)a->nt * (a->n_heads + 2 * kv->n_kv_heads) >= (1LL << 31)) return MQ_ERR_SHAPE;
     const void *p16[] = {a->q, a->k, a->v, a->q_out, a->q_bias, a->k_bias, a->v_bias, a->q_gain, a->k_gain};
     for (const void *p : p16)

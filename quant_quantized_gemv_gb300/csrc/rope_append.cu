@@ -30,9 +30,8 @@
 // What bounds it: few rows, the launch and three dependent loads (2.6 us a call
 // in a captured chain).  Many rows, HBM and the latency of a CTA's loads, one batch
 // after another.  4096 rows of 40 + 8 + 8 heads of 128, 218 MB, which take 33 us:
-// f16 37 us (5.9 TB/s), with biases 39, q8 with norms 42.  Four values a lane: 40, 47
-// and 55; 28 groups of those a CTA: 45 instead of 40; biases fetched with the values
-// cost registers, so warps: 44 instead of 43; one group a warp: 66.
+// f16 37 us (5.9 TB/s), with biases 39.5, q8 with norms 42.  With four values a lane
+// in the place of eight: 40, 47 and 56.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -300,8 +299,8 @@ cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     // 8 values a lane, partners in one lane, where pairs lie half a head apart and halves are whole blocks of q8.
     // Else 8 where rows are many. (Captured, us, 4 values / 8, 8 with partners: 40 + 8 + 8 heads of 128, biases: 1 row
-    // 2.7 / 2.9, 2.6; 24 rows 3.3 / 3.5, 3.1; 64 rows 4.7 / 3.9, 3.4; 256 rows 5.1 / 5.9, 4.7; 1024 rows 17.9 / 16.9, 14.4;
-    // 4096 rows 47 / 43, 39. q8, 28 + 4 + 4 heads: 1 row 3.1 / -, 3.3; 64 rows 4.1 / -, 3.9; 1024 rows 15.4 / -, 12.5.
+    // 2.8 / 2.9, 2.7; 24 rows 3.3 / 3.5, 3.1; 64 rows 4.4 / 3.9, 3.2; 256 rows 5.1 / 5.9, 4.6; 1024 rows 18.3 / 16.9, 14.6;
+    // 4096 rows 47 / 43, 39.5. q8, 28 + 4 + 4 heads: 1 row 3.1 / -, 3.3; 64 rows 4.1 / -, 3.9; 1024 rows 15.4 / -, 12.5.
     // Heads of 64: 64 rows 3.5 / 3.6, 3.1; 1024 rows 7.8 / 7.4, 6.)
     const long long heads = (long long)a.nt * (a.n_heads + 2 * a.n_kv_heads);
     const bool many = heads >= sms * (a.head_dim > 64 ? 8LL : 128LL);
