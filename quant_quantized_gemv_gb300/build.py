@@ -38,10 +38,11 @@ def nvcc() -> str:
 def _torch() -> tuple[str, str] | None:
     """Where torch lies and its version, without an import; None where there is none."""
     spec = find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
+    path = spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else ""
+    version = os.path.join(path, "version.py")
+    if not path or not os.path.exists(version):  # none, or a folder of that name
         return None
-    path = spec.submodule_search_locations[0]
-    with open(os.path.join(path, "version.py")) as f:
+    with open(version) as f:
         return path, re.search(r"^__version__\s*=\s*['\"]([^'\"]+)", f.read(), re.M)[1]
 
 

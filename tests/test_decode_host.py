@@ -361,3 +361,12 @@ def test_the_calls_are_those_of_the_torch_that_runs(mq):
     import torch
     from quant_quantized_gemv_gb300 import build as b
     assert torch.__version__ in b.binding() and mq._bind().__file__ == b.binding()
+
+
+def test_a_folder_named_torch_is_no_torch(elsewhere, monkeypatch, tmp_path):
+    import types
+    monkeypatch.setattr(elsewhere.subprocess, "run", Compiler())
+    for spec in (None, types.SimpleNamespace(submodule_search_locations=None),
+                 types.SimpleNamespace(submodule_search_locations=[str(tmp_path / "torch")])):
+        monkeypatch.setattr(elsewhere, "find_spec", lambda name: spec)
+        assert elsewhere.binding() is None and elsewhere.build(force=True)
