@@ -82,5 +82,34 @@ __device__ __forceinline__ u64 left_of(const VerifyLaunch &a, const Sequence &of
     return w > taken ? w - taken : 0;
 }
 
+// What is left of p, max(0, w / all - q): f32 of the exact difference. w is in two parts and 1 / all in two, and what the
+// first product rounds off is added behind the subtraction: off by 2^-24 of itself and 2^-45 of p, however near q is.
+// The sums are of these in units of 2^-42 (fixed_of), token by token, so that they are the same in whatever order and by
+// whatever threads they are formed: a token found by a sum is found again.
+struct Rest {
+    float ih, il;
+
+    __device__ __forceinline__ explicit Rest(u64 all)
+    {
+        const float ah = __ull2float_rn(all), al = __ll2float_rn((long long)(all - __float2ull_rn(ah)));
+        ih = 1.0f / ah * 0x1p42f, il = ih * (fmaf(-ah, ih * 0x1p-42f, 1.0f) - al / ah);
+    }
+    __device__ __forceinline__ void operator()(const Weight &weight, float x0, float x1, float q0, float q1, float &r0, float &r1) const
+    {
+        Two hi, lo;
+        weight.parts(x0, x1, hi, lo);
+        const Two h = two(ih, ih), minus = two(-1.0f, -1.0f), p = mul2(hi, h);
+        const Two low = fma2(hi, two(il, il), fma2(lo, h, fma2(hi, h, mul2(p, minus))));
+        split(add2(add2(p, two(-q0, -q1)), low), r0, r1);
+        r0 = __saturatef(r0), r1 = __saturatef(r1);
+    }
+    // The same from weights of f32, to 2^-23 of p beside what the weights are off by.
+    __device__ __forceinline__ void quick(Two w, float q0, float q1, float &r0, float &r1) const
+    {
+        split(fma2(w, two(ih, ih), fma2(w, two(il, il), two(-q0, -q1))), r0, r1);
+        r0 = __saturatef(r0), r1 = __saturatef(r1);
+    }
+};
+
 }  // namespace
 }  // namespace mq

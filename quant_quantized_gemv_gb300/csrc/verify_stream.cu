@@ -17,9 +17,12 @@
 // behind the other (the sequence's first row, the row, the logits; the last CTA the sums, then the chunk again); 3 in the
 // clusters that look for rows with filters. A CTA a chunk with an atomic for each took 26 and 24 us.
 //
-// Sums: a thread's 32 weights, 2^x to 2 ulp, in f32; everything above in integers of 2^-42 of the chunk's largest, times
-// that one's weight in the row. In the second pass the tokens that have more than 2^-10 of the row, whose errors would
-// not vanish among the others', are the draw's integers.
+// Sums: a thread's 32 weights in f32, a weight of 2^-t of the largest being off by (t 2^-23.5 + 2^-22) of itself at the
+// most (the difference of two logits, its factor, ex2.approx); everything above in integers of 2^-42 of the chunk's largest, times
+// that one's weight in the row. In the second pass what is left of a token is rounded to units of 2^-42 of the row by itself,
+// so that the pass that finds the chunk and the one that finds the token in it add up the same integers; of tokens that have
+// more than 2^-10 of the row, whose errors would not vanish among the others', it is the draw's weight (32 x 5 rows of
+// 152064: 41.4 us; for every token 45.4).
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <stdint.h>
@@ -292,28 +295,6 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_sums_kernel(const 
     }
 }
 
-// max(0, w / all - q) of two logits, by a reciprocal in two parts; w / all itself where q is 0.
-struct Rest {
-    float ih, il;
-
-    __device__ __forceinline__ explicit Rest(u64 all)
-    {
-        const float ah = __ull2float_rn(all), al = __ll2float_rn((long long)(all - __float2ull_rn(ah)));
-        ih = 1.0f / ah * 0x1p42f, il = ih * (fmaf(-ah, ih * 0x1p-42f, 1.0f) - al / ah);
-    }
-    // A sum of weights as a share of all, in units of 2^-42.
-    __device__ __forceinline__ u64 share(u64 t) const
-    {
-        const float th = __ull2float_rn(t), tl = __ll2float_rn((long long)(t - __float2ull_rn(th))), hi = th * ih;
-        return __float2ull_rn(hi) + (u64)__float2ll_rn(fmaf(th, ih, -hi) + (tl * ih + th * il));
-    }
-    __device__ __forceinline__ void operator()(Two w, float q0, float q1, float &r0, float &r1) const
-    {
-        split(fma2(w, two(ih, ih), fma2(w, two(il, il), two(-q0, -q1))), r0, r1);
-        r0 = __saturatef(r0), r1 = __saturatef(r1);
-    }
-};
-
 // CTAs of the rest, two on an SM: a thread's 16 logits and 16 probabilities fit its 64 registers at a time.
 constexpr int kRestThreads = 512, kRestWarps = kRestThreads / 32, kRestPer = kVerifyChunk / kRestThreads;
 
@@ -321,7 +302,8 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
 {
     __shared__ u64 sums[kRestWarps], target_at;
     __shared__ int chunk_at;
-    __shared__ bool last, from_p;
+    __shared__ bool last;
+    __shared__ u64 chunk_sums[kVerifyChunks];
     __shared__ float found[kRestPer];  // of the thread that has the token
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int at = blockIdx.x / a.chunks, chunk = blockIdx.x - at * a.chunks;
@@ -347,30 +329,19 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
     const Row r(a.logits + row * a.stride, a.vocab);
     const float *q = a.draft_probs && !final ? a.draft_probs + row * a.q_stride - r.shift : nullptr;
     const bool fours = q && ((uintptr_t)q & 15) == 0;
-    // What is left of the value at place p, in integers.
-    auto left_at = [&](int p, bool none) -> u64 {
-        float x = __ldcg(r.src + p);
-        if (infinite) x = x == INFINITY ? 0.0f : -INFINITY;
-        const u64 share = rest.share(weight(x));
-        u64 taken = 0;
-        if (!none && q) taken = __float2ull_rn(__saturatef(__ldcg(q + p)) * (float)(1ull << kFixBits));
-        else if (!none && !final && p - r.shift == draft) taken = 1ull << kFixBits;
-        return share > taken ? share - taken : 0;
-    };
     float v[kRestPer];
-    unsigned heavy;  // those of them that have more than 2^-10 of the row: left to left_at (there are 1024 at the most)
     const Fast fast(weight, weight.top);
     const float least = 0x1p-10f / rest.ih;
-    // v: what is left of this thread's values of a chunk, fours kRestThreads apart or consecutive. Everything is on its way
-    // before the first value is used.
+    // v: what is left of this thread's values of a chunk (none: nothing is taken off), fours kRestThreads apart or
+    // consecutive. Everything is on its way before the first value is used.
     auto place_in = [&](auto consecutive, int c, int k) {
         return c * kVerifyChunk + (decltype(consecutive)::value ? tid * kRestPer + k : (k & ~3) * kRestThreads + tid * 4 + (k & 3));
     };
     auto left = [&](auto consecutive, int c, bool none) {
         float t[kRestPer];  // what the draft takes off
         auto place = [&](int k) { return place_in(consecutive, c, k); };
-        heavy = 0;
         const bool whole = r.whole(c);
+        unsigned heavy = 0;
 #pragma unroll
         for (int k = 0; k < kRestPer; k += 4) {
             const float4 f = whole ? __ldcg(reinterpret_cast<const float4 *>(r.src + place(k))) : r.four(place(k), -INFINITY);
@@ -396,31 +367,65 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
             if (infinite) x0 = x0 == INFINITY ? 0.0f : -INFINITY, x1 = x1 == INFINITY ? 0.0f : -INFINITY;
             // (a q that is NaN counts as 0)
             const Two w = fast(x0, x1);
-            rest(w, __saturatef(t[k]), __saturatef(t[k + 1]), v[k], v[k + 1]);
+            rest.quick(w, __saturatef(t[k]), __saturatef(t[k + 1]), v[k], v[k + 1]);
             split(w, x0, x1);
-            if (x0 >= least) v[k] = 0.0f, heavy |= 1u << k;
-            if (x1 >= least) v[k + 1] = 0.0f, heavy |= 2u << k;
+            if (x0 >= least) heavy |= 1u << k;
+            if (x1 >= least) heavy |= 2u << k;
+        }
+        for (; heavy; heavy &= heavy - 1) {
+            const int k = __ffs(heavy) - 1, p = place(k & ~3) + (k & 3);
+            float x = __ldcg(r.src + p), none_left, exact;
+            if (infinite) x = x == INFINITY ? 0.0f : -INFINITY;
+            const float taken = none ? 0.0f : q ? __saturatef(__ldcg(q + p)) : !final && p - r.shift == draft ? 1.0f : 0.0f;
+            rest(weight, x, x, taken, taken, exact, none_left);
+#pragma unroll
+            for (int i = 0; i < kRestPer; ++i)
+                if (i == k) v[i] = exact;
         }
     };
-    left(std::false_type(), chunk, false);
-    float sum = 0.0f;
+    auto own_sum = [&]() {  // this thread's, in units of 2^-42
+        unsigned sum_hi = 0;
+        int sum_lo = 0;
 #pragma unroll
-    for (int k = 0; k < kRestPer; ++k) sum += v[k];
-    u64 mine = __float2ull_rn(sum * (float)(1ull << kFixBits));
-    for (; heavy; heavy &= heavy - 1) mine += left_at(place_in(std::false_type(), chunk, __ffs(heavy) - 1), false);
-    mine = warp_sum(mine);
-    if (lane == 0) sums[warp] = mine;
-    __syncthreads();
-    if (tid == 0) {
+        for (int k = 0; k < kRestPer; ++k) {
+            unsigned h;
+            int l;
+            fixed_of(v[k], h, l);
+            sum_hi += h, sum_lo += l;
+        }
+        return ((u64)sum_hi << 22) + (u64)(long long)sum_lo;
+    };
+    // The CTA's sum of `mine`, in thread 0.
+    auto cta_sum = [&](u64 mine) {
+        mine = warp_sum(mine);
+        if (lane == 0) sums[warp] = mine;
+        __syncthreads();
         u64 s = 0;
+        if (tid == 0)
 #pragma unroll
-        for (int w = 0; w < kRestWarps; ++w) s += sums[w];
-        ws.rest[chunk] = s;
+            for (int w = 0; w < kRestWarps; ++w) s += sums[w];
+        return s;
+    };
+    left(std::false_type(), chunk, false);
+    const u64 chunk_sum = cta_sum(own_sum());
+    if (tid == 0) {
+        ws.rest[chunk] = chunk_sum;
         last = arrive(&ws.rest_met, 1) + 1 == (unsigned)a.chunks;
         if (last) ws.rest_met = 0;
     }
     __syncthreads();
     if (!last) return;
+
+    // ---- nothing is left (probabilities that are none): from p itself, whose sums this CTA forms chunk by chunk
+    for (int c = tid; c < a.chunks; c += kRestThreads) chunk_sums[c] = __ldcg(&ws.rest[c]);
+    const bool none = !__syncthreads_or(tid < a.chunks && chunk_sums[tid] != 0);
+    if (none)
+        for (int c = 0; c < a.chunks; ++c) {
+            left(std::false_type(), c, true);
+            const u64 s = cta_sum(own_sum());
+            if (tid == 0) chunk_sums[c] = s;
+            __syncthreads();
+        }
 
     // ---- the token: its chunk, by one warp
     if (warp == 0) {
@@ -428,21 +433,10 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
 #pragma unroll
         for (int j = 0; j < kVerifyLane; ++j) {
             const int c = lane + 32 * j;
-            s[j] = c < a.chunks ? __ldcg(&ws.rest[c]) : 0;
+            s[j] = c < a.chunks ? chunk_sums[c] : 0;
             total += s[j];
         }
-        total = warp_sum(total);
-        const bool none = total == 0;  // nothing is left (probabilities that are none): from p itself
-        if (none) {
-#pragma unroll
-            for (int j = 0; j < kVerifyLane; ++j) {
-                const int c = lane + 32 * j;
-                const float t = c < a.chunks ? __ldcg(&ws.chunk[c].top) : -INFINITY;
-                s[j] = t == -INFINITY ? 0 : joined(__ldcg(&ws.chunk[c].sum), t, top, weight);
-                total += s[j];
-            }
-            total = warp_sum(total);
-        }
+        total = warp_sum(total);  // (not 0: of p the largest alone has 2^-20)
         const u64 target = u_draw > 0.0f ? (u_draw < 1.0f ? share_of(u_draw, total, false) : total - 1) : 0;
         u64 before = 0;
 #pragma unroll
@@ -454,17 +448,14 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
                 if (lane >= o) to += u;
             }
             if (before + to - s[j] <= target && target < before + to)
-                chunk_at = lane + 32 * j, target_at = none ? rest.share(target - (before + to - s[j])) : target - (before + to - s[j]), from_p = none;
+                chunk_at = lane + 32 * j, target_at = target - (before + to - s[j]);
             before += __shfl_sync(kAll, to, 31);
         }
     }
     __syncthreads();
     // and in it, in the order of the vocabulary
-    left(std::true_type(), chunk_at, from_p);
-    u64 own = 0;
-#pragma unroll
-    for (int k = 0; k < kRestPer; ++k) own += fixed_of(v[k]);
-    for (unsigned h = heavy; h; h &= h - 1) own += left_at(place_in(std::true_type(), chunk_at, __ffs(h) - 1), from_p);
+    left(std::true_type(), chunk_at, none);
+    const u64 own = own_sum();
     u64 to = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -473,23 +464,20 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
     }
     if (lane == 31) sums[warp] = to;
     __syncthreads();
-    u64 before = to - own, total = 0;
+    u64 before = to - own;
 #pragma unroll
-    for (int w = 0; w < kRestWarps; ++w) {
+    for (int w = 0; w < kRestWarps; ++w)
         if (w < warp) before += sums[w];
-        total += sums[w];
-    }
-    // (the chunk's own sum was f32's: the last token at the most)
-    const u64 target = min(target_at, total - 1);
-    if (before <= target && target < before + own) {  // (a chunk that was found has a sum)
+    // (the chunk's sum is of the same integers: it ends behind the target)
+    const u64 target = target_at;
+    if (before <= target && target < before + own) {
         int token = -1;
 #pragma unroll
         for (int k = 0; k < kRestPer; ++k) found[k] = v[k];
 #pragma unroll 1
         for (int k = 0; k < kRestPer; ++k) {
-            const int p = place_in(std::true_type(), chunk_at, k);
-            const u64 w = heavy >> k & 1 ? left_at(p, from_p) : fixed_of(found[k]);
-            if (before <= target && target < before + w) token = p - r.shift;
+            const u64 w = fixed_of(found[k]);
+            if (before <= target && target < before + w) token = place_in(std::true_type(), chunk_at, k) - r.shift;
             before += w;
         }
         a.tokens[row] = token;

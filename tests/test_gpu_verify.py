@@ -497,3 +497,100 @@ def test_many_rows_on_two_streams_at_once(mq):
 def test_the_largest_vocabulary(mq, f):
     c = Case(mq.MQ_SAMPLE_MAX_VOCAB, [2, 0, 1], key=("largest", str(f)), lead=1).filters(**f)
     c.check(*c.run(mq))
+
+
+# ------------------------------------------------------------------ faint ends, addresses
+def borders(c, tokens, counts, i, near=2.0 ** -21):
+    """Sequence i's tokens where a random number may lie on a border: what stands is the reference's, and the drawn token is
+    one of a finite logit whose interval reaches to within `near` of the draw."""
+    names = dict(temperature="t", top_k="k", top_p="p", min_p="m")
+    a, b = int(c.starts[i]), int(c.starts[i + 1])
+    want, n, _ = c.want(i)
+    got = tokens[a:b]
+    assert counts[i] == n and np.array_equal(got[:n - 1], want[:n - 1]) and np.all(got[n:] == -1)
+    r, at = a + n - 1, int(got[n - 1])
+    assert 0 <= at < c.v and np.isfinite(c.logits[r, at])
+    w = p = ref.distribution(c.logits[r], **{names[k]: x[i].item() for k, x in c.f.items()})
+    if r + 1 < b:
+        q = np.zeros(c.v)
+        if c.q is not None:
+            q = np.clip(np.nan_to_num(c.q[r].astype(np.float64), nan=0.0), 0, 1)
+        else:
+            q[c.drafts[r]] = 1.0
+        w = np.maximum(p - q, 0)
+        w = w if w.sum() > 0 else p
+    sums = np.cumsum(w) / w.sum()
+    u = float(c.u_draw[i])
+    assert sums[at] - w[at] / w.sum() - near <= u <= sums[at] + near, (i, at)
+
+
+def faint(v, probs, temperature, key, other=1.0):
+    """Rows of one or a few likely tokens amid ones that have 2^-43 of the row or less: as many as chunks hold, the first and
+    the last among them.  Drafts that stand, drafts that do not, none."""
+    drafts = [0, 1, 2] * 8
+    c = Case(v, drafts, probs, key=key).filters(temperature=np.float32(temperature))
+    g = np.random.default_rng(v)
+    c.logits = (g.standard_normal(c.logits.shape).astype(np.float32) * np.float32(0.1) - np.float32(30.5)) * np.float32(temperature)
+    c.u[:] = np.float32(0.25)
+    for r in range(c.rows):
+        likely = v // 2 + 3 * np.arange(1 + r % 3)
+        c.logits[r, likely] = np.float32([0.0, -1.0, -2.0])[:len(likely)] * np.float32(temperature)
+        c.drafts[r] = likely[0] if r % 2 else 5             # one that stands, one that does not
+        if probs:
+            c.q[r] = 0.0
+            c.q[r, c.drafts[r]] = np.float32(other)
+    ends = np.float32([0.0, 1e-30, 2.0 ** -24, 0.5, 1 - 2.0 ** -24, 1.0, 2.0, -1.0])
+    c.u_draw = ends[np.arange(c.n) // 3 % 8]
+    return c
+
+
+@pytest.mark.parametrize("v", [152064, 50257])
+@pytest.mark.parametrize("probs", [True, False])
+@pytest.mark.parametrize("temperature", [1.0, 0.2])
+def test_many_rows_the_ends_of_the_draw(mq, v, probs, temperature):
+    c = faint(v, probs, temperature, "ends")
+    assert c.rows * v >= 2 << 20
+    t, n = (x.cpu().numpy() for x in c.run(mq))
+    c.u_draw = np.clip(c.u_draw, 0, 1 - 2.0 ** -24).astype(np.float32)
+    for i in range(c.n):
+        borders(c, t, n, i)
+
+
+@pytest.mark.parametrize("v", [152064, 50257])
+def test_many_rows_the_ends_of_a_draw_from_p_itself(mq, v):
+    """Probabilities of 1 everywhere: nothing is left of p."""
+    c = faint(v, True, 1.0, "ends of p")
+    c.q[:] = 1.0
+    c.u[:] = np.float32(1 - 2.0 ** -24)
+    c.drafts[:] = 5
+    t, n = (x.cpu().numpy() for x in c.run(mq))
+    c.u_draw = np.clip(c.u_draw, 0, 1 - 2.0 ** -24).astype(np.float32)
+    for i in range(c.n):
+        borders(c, t, n, i)
+
+
+def test_many_rows_a_padded_vocabulary(mq):
+    """Nothing in the last two chunks: a draw of 1 ends in front of them."""
+    c = faint(50257, False, 0.5, "padded")
+    c.logits[:, 40000:] = -np.inf
+    t, n = (x.cpu().numpy() for x in c.run(mq))
+    c.u_draw = np.clip(c.u_draw, 0, 1 - 2.0 ** -24).astype(np.float32)
+    for i in range(c.n):
+        borders(c, t, n, i)
+
+
+def test_many_rows_the_borders_of_the_random_numbers(mq):
+    """Rows as any, by chunks; u at its ends as well."""
+    c = many(30011, "borders many")
+    c.u[::3] = np.resize(np.float32([0, -1, 2, 1 - 2.0 ** -24]), len(c.u[::3]))
+    c.u_draw = np.resize(np.float32([0, 1 - 2.0 ** -24, 1, 2, -1, 0.5, 1e-30, -0.0]), c.n)
+    t, n = (x.cpu().numpy() for x in c.run(mq))
+    c.u = np.clip(c.u, 0, 1 - 2.0 ** -24).astype(np.float32)
+    c.u_draw = np.clip(c.u_draw, 0, 1 - 2.0 ** -24).astype(np.float32)
+    for i in range(c.n):
+        near = False                                        # (u = 1 - 2^-24 over equal probabilities decides by 2^-24 of them)
+        for r in range(c.starts[i], c.starts[i + 1] - 1):
+            least, x = float(c.u[r]) * float(c.q[r, c.drafts[r]]), ref.distribution(c.logits[r])[c.drafts[r]]
+            near = near or abs(least - x) <= NEAR * max(least, x)
+        if not near:
+            borders(c, t, n, i)
