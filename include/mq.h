@@ -774,9 +774,12 @@ int mq_sample(const mq_sample_args *args, void *stream);
  *     smaller calls too), device, 16-byte aligned, zero-filled before its first use;
  *     every completed call leaves its counts zero.  Calls that share a workspace,
  *     replayed graphs among them, must be ordered on one stream.
- * tokens may be drafts.  Sums are the integers of mq_sample (what is left of p in
- * f32; of many logits the weights too, in one order), so the result depends on
- * nothing but the inputs.
+ * tokens may be drafts.  Sums are integers, as mq_sample's, of what is left of p as well;
+ * without a filter and with 2^20 logits or more (2^21 where an array of filters is
+ * given) 32 weights at a time in f32, in an order that goes by the tokens' numbers.  A
+ * sequence's result depends on its own inputs alone, wherever they lie, but where a
+ * random number falls within some 2^-22 of a border: there the way that the call takes,
+ * by its rows, vocabulary and filters, may decide.
  * Shapes: 1 <= vocab <= MQ_SAMPLE_MAX_VOCAB; nt, n_seqs >= 1, at most 65536.
  * Errors: MQ_ERR_NULL, MQ_ERR_SHAPE, MQ_ERR_ALIGN, MQ_ERR_WORKSPACE, MQ_ERR_CUDA.
  * ------------------------------------------------------------------------ */

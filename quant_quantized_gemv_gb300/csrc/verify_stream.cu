@@ -17,9 +17,9 @@
 // behind the other (the sequence's first row, the row, the logits; the last CTA the sums, then the chunk again); 3 in the
 // clusters that look for rows with filters. A CTA a chunk with an atomic for each took 26 and 24 us.
 //
-// Sums: a thread's 32 weights in f32, a weight of 2^-t of the largest being off by (t 2^-23.5 + 2^-22) of itself at the
-// most (the difference of two logits, its factor, ex2.approx); everything above in integers of 2^-42 of the chunk's largest, times
-// that one's weight in the row. In the second pass what is left of a token is rounded to units of 2^-42 of the row by itself,
+// Sums: a lane's 32 weights (of tokens 32 apart, wherever among 16 bytes the row begins) in f32, a weight of 2^-t of the
+// largest being off by (t 2^-23.5 + 2^-22) of itself at the most (the difference of two logits, its factor, ex2.approx);
+// everything above in integers of 2^-42 of the chunk's largest, times that one's weight in the row. In the second pass what is left of a token is rounded to units of 2^-42 of the row by itself,
 // so that the pass that finds the chunk and the one that finds the token in it add up the same integers; of tokens that have
 // more than 2^-10 of the row, whose errors would not vanish among the others', it is the draw's weight (32 x 5 rows of
 // 152064: 41.4 us; for every token 45.4).
@@ -185,11 +185,15 @@ __device__ __forceinline__ void decide(Sequence &of, const VerifyLaunch &a, int 
 }
 
 constexpr int kResident = 3;  // CTAs of the sums on an SM, each with two chunks in shared memory
+// Tokens of a chunk that a warp sums, and fours that hold them wherever among 16 bytes the row begins: which weights
+// a lane adds up goes by the tokens' numbers, not by their addresses.
+constexpr int kSegment = kVerifyChunk / kWarps, kFours = kSegment / 4 + 1;
+static_assert(kSegment == 32 * kPer, "a lane's tokens");
 
 __global__ void __launch_bounds__(kThreads, kResident) verify_sums_kernel(const VerifyLaunch a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
-    float4(*ring)[kPer / 4][kThreads] = reinterpret_cast<float4(*)[kPer / 4][kThreads]>(raw);
+    float4(*const ring)[kFours] = reinterpret_cast<float4(*)[kFours]>(raw) + (threadIdx.x >> 5) * 2;  // the warp's
     __shared__ Sequence of;
     __shared__ float tops[kVerifyChunks][kWarps];  // of the row's chunks that are this CTA's, warp by warp
     __shared__ u64 sums[kVerifyChunks][kWarps];
@@ -200,21 +204,20 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_sums_kernel(const 
     griddep_launch_dependents();
     griddep_wait();  // any of the inputs may come from the preceding kernels
 
-    // a thread reads the values that it copied itself: fours kThreads apart
-    auto issue = [&](int i) {
-        const int row = i / a.chunks, chunk = i - row * a.chunks;
+    auto issue = [&](int i) {  // (-inf where the row has no value)
+        const int row = i / a.chunks, chunk = i - row * a.chunks, from = chunk * kVerifyChunk + warp * kSegment;
         const Row r(a.logits + row * a.stride, a.vocab);
-        const float *src = r.src + chunk * kVerifyChunk + tid * 4;
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(&ring[i & 1][0][tid]);
-        const bool whole = r.whole(chunk);
-#pragma unroll
-        for (int k = 0; k < kPer / 4; ++k) {
-            const int p = chunk * kVerifyChunk + (k * kThreads + tid) * 4;
-            if (whole || (p >= r.lo && p + 4 <= r.hi))
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * kThreads * 16), "l"(src + k * kThreads * 4) : "memory");
+        const bool whole = from >= r.lo && from + kSegment <= r.hi;
+        auto copy = [&](int f, bool inside) {
+            const int p = from + 4 * f;
+            if (inside || (p >= r.lo && p + 4 <= r.hi))
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(&ring[i & 1][f])), "l"(r.src + p) : "memory");
             else
-                ring[i & 1][k][tid] = r.four(p, -INFINITY);
-        }
+                ring[i & 1][f] = r.four(p, -INFINITY);
+        };
+#pragma unroll
+        for (int k = 0; k < kSegment / 128; ++k) copy(32 * k + lane, whole);
+        if (lane == 0 && r.shift > 0) copy(kSegment / 4, false);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     issue(begin);
@@ -235,13 +238,15 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_sums_kernel(const 
             if (i + 1 < end) issue(i + 1);
             else asm volatile("cp.async.commit_group;" ::: "memory");
             asm volatile("cp.async.wait_group 1;" ::: "memory");
-            if (!to_do) continue;
-            float v[kPer];
+            __syncwarp();
+            float v[kPer];  // of tokens 32 apart
+            const float *const values = reinterpret_cast<const float *>(ring[i & 1]) + shift + lane;
+            if (to_do) {
 #pragma unroll
-            for (int k = 0; k < kPer / 4; ++k) {
-                const float4 f = ring[i & 1][k][tid];
-                v[4 * k] = f.x, v[4 * k + 1] = f.y, v[4 * k + 2] = f.z, v[4 * k + 3] = f.w;
+                for (int k = 0; k < kPer; ++k) v[k] = values[32 * k];
             }
+            __syncwarp();  // the warp's next copies go where these lie
+            if (!to_do) continue;
             float top = -INFINITY;
 #pragma unroll
             for (float x : v) top = fmaxf(top, x);  // (no NaN)
@@ -251,9 +256,9 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_sums_kernel(const 
                 int at = INT_MAX;
 #pragma unroll
                 for (int k = kPer - 1; k >= 0; --k)
-                    if (v[k] == top) at = (first + c) * kVerifyChunk + (k / 4 * kThreads + tid) * 4 + k % 4;
+                    if (v[k] == top) at = (first + c) * kVerifyChunk + warp * kSegment + 32 * k + lane;
                 at = __reduce_min_sync(kAll, at);
-                if (lane == 0) tops[c][warp] = top, sums[c][warp] = (unsigned)(at - shift);
+                if (lane == 0) tops[c][warp] = top, sums[c][warp] = (unsigned)at;
                 continue;
             }
             const bool infinite = top == INFINITY;  // those logits share the draw: as equal ones
@@ -490,7 +495,7 @@ cudaError_t launch_verify_stream(const VerifyLaunch &a, int sms, int pdl, cudaSt
 {
     static_assert(kVerifyLane * 32 >= kVerifyChunks, "a warp's lanes hold a row's chunks");
     static_assert((long long)kVerifyMaxRows * kVerifyChunks < 1 << 30, "chunks, and rows with a bit, in an int");
-    constexpr int room = 2 * kVerifyChunk * 4;
+    constexpr int room = 2 * kWarps * kFours * 16;
     static std::atomic<bool> opted[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -594,3 +594,24 @@ def test_many_rows_the_borders_of_the_random_numbers(mq):
             near = near or abs(least - x) <= NEAR * max(least, x)
         if not near:
             borders(c, t, n, i)
+
+
+def test_many_rows_wherever_they_begin(mq):
+    """A row among 16 bytes: its sums, and so its token, do not change.  Draws of many numbers over many tokens of nearly
+    equal weight, so that some fall near a border."""
+    import torch
+    v, n = 152063, 64                                       # an odd stride: four rows begin in four ways
+    g = torch.Generator(device="cuda").manual_seed(5)
+    ws = mq.mq_verify_workspace(n, n)
+    starts = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    zeros, u = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(n, device="cuda")
+    tokens, counts = torch.zeros_like(zeros), torch.zeros_like(zeros)
+    other = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(4):
+        logits = (torch.randn(n // 4, 1, v, device="cuda", generator=g) * 0.5).expand(-1, 4, -1).contiguous().view(n, v)
+        for _ in range(3000):
+            draws = torch.rand(n // 4, 1, device="cuda", generator=g).expand(-1, 4).reshape(n)
+            mq.mq_verify(logits, zeros, starts, u, draws, tokens=tokens, counts=counts, ws=ws)
+            t = tokens.view(-1, 4)
+            other += (t != t[:, :1]).sum()
+    assert int(other) == 0
