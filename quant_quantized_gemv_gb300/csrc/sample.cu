@@ -1227,9 +1227,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const std::conditional
                 if (rank == 0 && tid == 0) finish_row(a, sh.of, row, draft, true);
                 return;  // alike in every CTA of the row; nobody reads another's memory after the barrier
             }
-            // the rest, max(0, p - q), in place of the logits, as f32: p = w / all by a reciprocal in two parts
-            const float ah = __ull2float_rn(all), al = __ll2float_rn((long long)(all - __float2ull_rn(ah)));
-            const float ih = 1.0f / ah * 0x1p42f, il = ih * (fmaf(-ah, ih * 0x1p-42f, 1.0f) - al / ah);
+            // the rest, max(0, p - q), in place of the logits
+            const Rest rest_of(all);
             const float *q = a.draft_probs ? a.draft_probs + row * a.q_stride - shift + base : nullptr;
             const bool limited = last_x > -INFINITY;
             constexpr int kAtOnce = 4;  // pairs of values: of each the loads of q are under way together
@@ -1249,13 +1248,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const std::conditional
                     float r0 = 0.0f, r1 = 0.0f;
                     const bool in0 = !limited || passes(x0, i), in1 = !limited || passes(x1, k);
                     if (in0 || in1) {  // (of a limited row few are)
-                        const Two w = weight.pair_f32(x0, x1);
-                        split(fma2(w, two(ih, ih), fma2(w, two(il, il), two(-qs[j], -qs[j + 1]))), r0, r1);
+                        rest_of(weight, x0, x1, qs[j], qs[j + 1], r0, r1);
                         if (!in0 || (floor_w > 0 && there0 && kept(i) == 0)) r0 = 0.0f;
                         if (!in1 || (floor_w > 0 && there1 && kept(k) == 0)) r1 = 0.0f;
                     }
-                    if (there0) xs[i] = fminf(fmaxf(r0, 0.0f), 1.0f);
-                    if (there1) xs[k] = fminf(fmaxf(r1, 0.0f), 1.0f);
+                    if (there0) xs[i] = r0;
+                    if (there1) xs[k] = r1;
                 }
             }
             __syncthreads();

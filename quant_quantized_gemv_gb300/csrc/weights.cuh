@@ -82,6 +82,19 @@ struct Weight {
         }
     }
 
+    // The weights of two logits as f32 (rounded once more, 2^-24), in units of the largest: for sums that take
+    // something off them.
+    __device__ __forceinline__ Two pair_f32(float x0, float x1) const
+    {
+        float w[2];
+        unsigned a[2], m[2];
+        int none[2];
+        pair(x0, x1, a, m, none);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i] = __uint2float_rn(a[i]) * (__uint2float_rn(m[i]) * 0x1p-42f);
+        return two(w[0], w[1]);
+    }
+
     // The same in units of the largest, each as two f32 whose sum it is (22 bits and the other 8).
     __device__ __forceinline__ void parts(float x0, float x1, Two &hi, Two &lo) const
     {
@@ -95,19 +108,6 @@ struct Weight {
             h[i] = __uint2float_rn(a[i] & ~0xffu) * unit, l[i] = __uint2float_rn(a[i] & 0xffu) * unit;
         }
         hi = two(h[0], h[1]), lo = two(l[0], l[1]);
-    }
-
-    // The weights of two logits as f32 (rounded once more, 2^-24), in units of the largest: for sums that take
-    // something off them.
-    __device__ __forceinline__ Two pair_f32(float x0, float x1) const
-    {
-        float w[2];
-        unsigned a[2], m[2];
-        int none[2];
-        pair(x0, x1, a, m, none);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) w[i] = __uint2float_rn(a[i]) * (__uint2float_rn(m[i]) * 0x1p-42f);
-        return two(w[0], w[1]);
     }
 
     __device__ __forceinline__ u64 operator()(float x) const

@@ -615,3 +615,22 @@ def test_many_rows_wherever_they_begin(mq):
             t = tokens.view(-1, 4)
             other += (t != t[:, :1]).sum()
     assert int(other) == 0
+
+
+@pytest.mark.parametrize("v", [20000, 152064])
+@pytest.mark.parametrize("f", [dict(), dict(top_k=700), dict(top_p=0.95)])
+def test_what_is_left_of_nearly_equal_probabilities(mq, v, f):
+    """q within a thousandth of p: the differences are exact, so what is left is off by what the weights are (5 x 2^-26 of p) as a
+    share of all that is left."""
+    c = Case(v, [1] * (8 if v < 50000 else 40), noise=0.0, key=("nearly", str(f))).filters(**f)
+    g = np.random.default_rng(v)
+    names = dict(top_k="k", top_p="p")
+    for i in range(c.n):
+        r = c.starts[i]
+        p = ref.distribution(c.logits[r], **{names[k]: x[i].item() for k, x in c.f.items()})
+        c.q[r] = np.clip(p * (1 + 1e-3 * g.uniform(-1, 1, v)), 0, 1)
+        c.q[r, c.drafts[r]] = 1.0                             # refused
+    c.u[:] = np.float32(0.9999)
+    t, n = (x.cpu().numpy() for x in c.run(mq))
+    for i in range(c.n):
+        borders(c, t, n, i, 2.0 ** -23 / 2.0 ** -13)          # what is left adds up to 1 / 4 x 10^-3 > 2^-13
