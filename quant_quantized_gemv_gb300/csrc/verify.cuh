@@ -44,13 +44,17 @@ __device__ __forceinline__ bool find_sequence(Sequence &of, const VerifyLaunch &
         const int from = __ldcg(a.starts + i), to = __ldcg(a.starts + i + 1);
         bad = bad || from < 0 || to < from || to > a.nt;
         if (from <= row && row < to) {
-            of.seq = i, of.from = from, of.to = to;
-            of.final = row + 1 == to;
-            of.temperature = a.temperature ? __ldcg(a.temperature + i) : 1.0f;
-            of.top_p = a.top_p ? __ldcg(a.top_p + i) : 1.0f;
-            of.min_p = a.min_p ? __ldcg(a.min_p + i) : 0.0f;
-            of.top_k = a.top_k ? __ldcg(a.top_k + i) : 0;
-            if (NUMBERS) read_row(of, a, row);
+            // formed in registers: where starts do not ascend several threads may find one, and none of them may take
+            // another's numbers for an address
+            Sequence mine = {};
+            mine.seq = i, mine.from = from, mine.to = to;
+            mine.final = row + 1 == to;
+            mine.temperature = a.temperature ? __ldcg(a.temperature + i) : 1.0f;
+            mine.top_p = a.top_p ? __ldcg(a.top_p + i) : 1.0f;
+            mine.min_p = a.min_p ? __ldcg(a.min_p + i) : 0.0f;
+            mine.top_k = a.top_k ? __ldcg(a.top_k + i) : 0;
+            if (NUMBERS) read_row(mine, a, row);
+            of = mine;
         }
     }
     return bad;

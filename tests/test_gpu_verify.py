@@ -634,3 +634,18 @@ def test_what_is_left_of_nearly_equal_probabilities(mq, v, f):
     t, n = (x.cpu().numpy() for x in c.run(mq))
     for i in range(c.n):
         borders(c, t, n, i, 2.0 ** -23 / 2.0 ** -13)          # what is left adds up to 1 / 4 x 10^-3 > 2^-13
+
+
+@pytest.mark.parametrize("v", [1000, 152064])
+@pytest.mark.parametrize("starts", [[0, 3, 1, 9], [0, 9, 0, 9], [0, 4, 3, 9]])
+def test_starts_that_overlap(mq, v, starts):
+    """A row of two sequences, of one of them the last, whose draft is no token: refused as a whole, nothing read for it."""
+    import torch
+    c = Case(v, [2, 2, 2], key="overlap")
+    c.drafts[:] = [-1, -2 ** 31, v, 2 ** 31 - 1, -1, 5, -1, v, -1]
+    for f in (dict(), dict(top_p=0.9)):
+        c.filters(**f)
+        for _ in range(20):
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            t, n = c.run(mq, starts=dev(np.int32(starts)), status=status)
+            assert int(status) == 1 and (t == -9).all() and (n == -9).all()
