@@ -290,12 +290,16 @@ constexpr int kQ4Group = D / 32 < 4 ? D / 32 : 4;
 
 // One tile of TILE tokens of a 4-bit cache, from its stage; lane = 4 g + t has tokens 2t, 2t+1 of each eight.
 // Scores: a block's products end with the token's scale. Output: p's two parts take V's scales, block by block.
-// p is in units of 2^-unit: 2^-13, so that its products with scales under 2 stay in fp16's range and hold the bits of
-// f32, or what brings the largest product that the group of blocks has met below 2^14. The whole tile goes through the tensor core
-// before a sum is rescaled and added to.
+// The products of p and a scale are fp16 parts, which hold the bits of f32 where the largest are well above fp16's
+// subnormals. p is in units of 2^-unit: 2^-13, or, for scales of 2 and more, what brings the largest product that the group of
+// blocks has met below 2^14. While no scale of 2^-6 or more has been met (a V of small values; a warp's first tile), the
+// scales are taken times 2^more, which is exact, for a largest of 1 to 2 (of 2^-9, if all are fp16's least), and the sums are
+// in units of 2^-(unit + more). Without that, V of 10^-5 over 16384 tokens is off by 7 x 10^-5 of itself; it takes 1 to 3% of
+// the time (16 x 16384 tokens: 99.8 -> 101.4 us). The whole tile goes through the tensor core before a sum is rescaled and
+// added to.
 // lo, hi: the tokens that are seen; full: all.
 template <int D, int KC, int TILE>
-__device__ __forceinline__ void q4_tile(Two (&o)[D / 8], float &m, float &l, int (&unit)[KC / kQ4Group<D>], const uint8_t *stage,
+__device__ __forceinline__ void q4_tile(Two (&o)[D / 8], float &m, float &l, int (&unit)[KC / kQ4Group<D>], int (&more)[KC / kQ4Group<D>], const uint8_t *stage,
                                         const uint4 (*q_frag)[32], float s_factor, float softcap,
                                         float inv_cap, bool full, int lo, int hi, int lane)
 {
@@ -402,14 +406,14 @@ __device__ __forceinline__ void q4_tile(Two (&o)[D / 8], float &m, float &l, int
                 for (int b = 0; b < H; ++b) vs[i][b] = 0;
             }
         }
-        // Scales under 2, as bits: no change. Else the largest, which is 2^e at the most.
+        // Scales under 2, as bits, and one of 2^-6 has been met: no change. Else the largest, which is under 2^e.
         unsigned any = 0;
 #pragma unroll
         for (int i = 0; i < 2 * J; ++i)
 #pragma unroll
             for (int b = 0; b < H; ++b) any |= vs[i][b];
         float down = alpha;
-        if (__any_sync(kFull, any & 0x40004000)) {
+        if (__any_sync(kFull, (any & 0x40004000) != 0 || more[group] > 0)) {
             float big = 0.0f;
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i)
@@ -417,9 +421,15 @@ __device__ __forceinline__ void q4_tile(Two (&o)[D / 8], float &m, float &l, int
                 for (int b = 0; b < G; ++b) big = fmaxf(big, fabsf(scale_of(vs[i], b)));
             big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
             big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
-            const int e = min((int)(__float_as_uint(big) >> 23) - 126, 17), now = min(unit[group], 14 - e);
-            down *= __uint_as_float((unsigned)(127 + now - unit[group]) << 23);
-            unit[group] = now;
+            const int e = min((int)(__float_as_uint(big) >> 23) - 126, 17);
+            const int now = min(unit[group], 14 - max(e, 1)), k = e < -5 ? min(more[group], 1 - e) : 0;
+            down *= __uint_as_float((unsigned)(127 + now + k - unit[group] - more[group]) << 23);
+            unit[group] = now, more[group] = k;
+            const __half2 by = half2_of((unsigned)(k + 15) * 0x04000400u);  // 2^k
+#pragma unroll
+            for (int i = 0; i < 2 * J; ++i)
+#pragma unroll
+                for (int b = 0; b < H; ++b) vs[i][b] = bits(__hmul2(half2_of(vs[i][b]), by));
         }
         const Two down2 = two(down, down);
         const float up = __uint_as_float((unsigned)(127 + unit[group]) << 23);
@@ -830,6 +840,9 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
         int q4_unit[TYPE == kQ4 ? KC / kQ4Group<D> : 1];  // q4: the sums of a group of blocks are in units of 2^-unit
 #pragma unroll
         for (int &u : q4_unit) u = 13;
+        int q4_more[sizeof(q4_unit) / sizeof(int)];  // and of 2^-more of that: the first scales settle it
+#pragma unroll
+        for (int &u : q4_more) u = 15;
         int unit_exp = -30;             // q8: the sums of p v are in units of 2^unit_exp
 
         for (int r = 0; r < at.take; ++r) {
@@ -839,7 +852,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
             if constexpr (TYPE == kQ4) {
                 if (tok < to) {
                     bad = bad || (missing >> stage & 1);
-                    q4_tile<D, KC, S::tile>(o, m, l, q4_unit, sh.ring[warp][stage], sh.q_frag, s_factor, a.softcap, inv_cap,
+                    q4_tile<D, KC, S::tile>(o, m, l, q4_unit, q4_more, sh.ring[warp][stage], sh.q_frag, s_factor, a.softcap, inv_cap,
                                    tok >= first && tok + S::tile <= n, first - tok, n - tok, lane);
                 }
             } else if (tok < to) {
@@ -1065,7 +1078,7 @@ __global__ void __launch_bounds__(Shape<TYPE, D>::threads, 1) attn_decode_kernel
                     // four accumulators are four values side by side: whole 16-byte stores, which meet every bank once
 #pragma unroll
                     for (int j = 0; j < NJ; j += 4) {
-                        const float one = __uint_as_float((unsigned)(127 - q4_unit[j / (4 * kQ4Group<D>)]) << 23);
+                        const float one = __uint_as_float((unsigned)(127 - q4_unit[j / (4 * kQ4Group<D>)] - q4_more[j / (4 * kQ4Group<D>)]) << 23);
                         float x[4][2];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) split(mul2(o[j + i], two(one, one)), x[i][0], x[i][1]);

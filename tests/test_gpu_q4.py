@@ -483,3 +483,60 @@ def test_caps_whose_inverse_overflows(mq, cap):
     c = Q4(mq, 64, 4, 2, 16, [90, 1, 300])
     c.q.reshape(3, 4, 64)[:, ::2] = 0.0
     c.check(c.run(softcap=cap), softcap=cap)
+
+
+# ------------------------------------------------------------------ small values
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("v_scale", [1e-2, 1e-4, 1e-5, 2e-6])
+def test_small_values(mq, d, v_scale):
+    """Scales down to fp16's least: the bound is a share of the values."""
+    c = Q4(mq, d, 8, 2, 16, [1, 50, 600, 5000], v_scale=v_scale, key="small")
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("order", ["up", "down", "zeros first", "by block"])
+def test_scales_that_change_along_a_sequence(mq, d, order):
+    """From 2^-20 to 2^11 and back: the sums' units follow the largest that has been met."""
+    c = Q4(mq, d, 8, 2, 16, [700, 4100, 33], key=order)
+    u, s = c.codes[1], c.scales[1]
+    factor = np.ones(s.shape)
+    for i, n in enumerate(c.lens):
+        e = np.linspace(-18, 12, int(n))
+        e = {"up": e, "down": e[::-1], "zeros first": np.where(np.arange(n) < n // 2, -np.inf, -16), "by block": e * 0 - 10}[order]
+        for t in range(int(n)):
+            at = c.table[i, t // 16], slice(None), t % 16
+            factor[at] = 2.0 ** e[t] * (2.0 ** (4 * np.arange(d // 32)) if order == "by block" else 1.0)
+    with np.errstate(invalid="ignore"):
+        c.scales[1] = np.clip(s.astype(np.float64) * factor, -60000, 60000).astype(np.float16)
+    c.store()
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("shift", [0, -9, -20])
+def test_every_bit_of_a_weight_shows_at_every_scale(mq, d, shift):
+    """Two tokens alone matter (oracle.decode.TwoTokens) and nothing is allowed for but what its bound counts, under value
+    scales of 1, 2^-9 and 2^-20."""
+    g, hq, hkv, nt = synth.rng("q4 bits", d, shift), 10, 2, 24
+    lens = g.integers(17, 200, nt)
+    c = Q4(mq, d, hq, hkv, 16, lens)
+    rng = np.random.default_rng(int(g.integers(1 << 30)))
+    cases = [ref.TwoTokens(rng, hq, hkv, d, int(n), "weights") for n in lens]
+    for x, name in ((0, "k"), (1, "v")):
+        vals = np.zeros(c.codes[x].shape)
+        for i, t in enumerate(cases):
+            y = getattr(t, name)
+            for j in range(-(-int(lens[i]) // 16)):
+                m = min(16, int(lens[i]) - j * 16)
+                vals[c.table[i, j], :, :m] = y[:, j * 16:j * 16 + m]
+        c.codes[x] = (vals + 8).astype(np.uint8)
+        c.scales[x] = np.where(np.isnan(c.scales[x]), np.nan, 2.0 ** shift if x else 1.0).astype(np.float16)
+    c.store()
+    c.q = np.stack([t.q.reshape(-1) for t in cases])
+    c.scale = 1.0
+    got = c.run().cpu().numpy().reshape(nt, hq, d).astype(np.float64) * 2.0 ** -shift
+    for i, t in enumerate(cases):
+        want = ref.attention(t.q, t.k, t.v, 1.0)
+        ratio = np.abs(got[i] - want) / t.bound(want, True)
+        assert ratio.max() <= 1, (i, ratio.max())
