@@ -52,6 +52,30 @@ __device__ __forceinline__ float4 times(float4 v, float s, float4 g)
     return make_float4((v.x * s) * g.x, (v.y * s) * g.y, (v.z * s) * g.z, (v.w * s) * g.w);
 }
 
+// A sum of squares of a long row: 16 groups of four at a time in f32, and what adding such a sum rounds off (which two f32
+// additions find exactly) kept beside the others, so that the error does not grow with the row. (Rows of 2^26 equal values,
+// 2^16 squares a thread, added one after the other were off by up to 8 x 10^-4.)
+struct LongSum {
+    float sum = 0.0f, rest = 0.0f, some = 0.0f;
+
+    __device__ __forceinline__ void add(float4 v, int i)
+    {
+        some = dot(v, some);
+        if ((i / kMaxThreads & 15) == 15) settle();
+    }
+    __device__ __forceinline__ void settle()
+    {
+        const float t = __fadd_rn(sum, some), b = __fsub_rn(t, sum);
+        rest += __fadd_rn(__fsub_rn(sum, __fsub_rn(t, b)), __fsub_rn(some, b));
+        sum = t, some = 0.0f;
+    }
+    __device__ __forceinline__ float total()
+    {
+        settle();
+        return sum < INFINITY ? sum + rest : sum;  // (an infinite sum has no rest)
+    }
+};
+
 // K groups of four a lane; K = 0: rows longer than a CTA holds, whose x' is read again from where it was written.
 // GATE: a gate, which is loaded ahead of the first sum with x and y (4096 rows of 5120: 75.5 -> 72.8 us; its registers
 // in a kernel without one cost a CTA an SM, 55.6 -> 59.7).
@@ -122,17 +146,17 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const Residual
     } else {
         float ys = 1.0f;
         if (post4) {
-            float s = 0.0f;
-            for (int i = tid; i < n4; i += T) s = dot(__ldcg(y4 + i), s);
-            ys = factor(s, 0);
+            LongSum s;
+            for (int i = tid; i < n4; i += T) s.add(__ldcg(y4 + i), i);
+            ys = factor(s.total(), 0);
         }
-        float s = 0.0f;
+        LongSum s;
         for (int i = tid; i < n4; i += T) {
             const float4 v = added(__ldcg(x4 + i), __ldcg(y4 + i), GATE ? __ldcg(gate4 + i) : one, ys, i);
             out4[i] = v;
-            s = dot(v, s);
+            s.add(v, i);
         }
-        const float xs = factor(s, 1);
+        const float xs = factor(s.total(), 1);
         for (int i0 = 0; i0 < n4; i0 += T) finish(i0 + tid < n4 ? out4[i0 + tid] : zero, xs, i0 + tid);
     }
 }

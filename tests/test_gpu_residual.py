@@ -188,3 +188,31 @@ def test_refusals(mq):
         mq.mq_add_rmsnorm_quant_q8(x, x, x[0], 1e-6, x_out=x, z=x, q8=a["q8"])
     torch.cuda.synchronize()
     assert (a["x_out"] == 7.0).all()
+
+
+@pytest.mark.parametrize("n", [1 << 15 | 32, 1 << 21, (1 << 26) - 32])
+@pytest.mark.parametrize("post", [False, True])
+def test_long_rows_of_equal_magnitudes(mq, n, post):
+    """Squares that all round to one side, in a bound that does not grow with the row: 16 groups of four of a thread, a
+    butterfly and 32 warps are 101 roundings; what is kept beside the sums 2 more."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x, y = ((torch.randint(0, 2, (1, n), device="cuda", generator=g) * 2 - 1) * v for v in (1.1, 0.77))
+    x, y = x.float(), y.float()
+    gain, more = torch.full((n,), 1.25, device="cuda"), torch.full((n,), 0.75, device="cuda") if post else None
+    out, z, _ = mq.mq_add_rmsnorm_quant_q8(x, y, gain, 1e-6, post_gain=more, scale=0.5)
+    host = [None if t is None else t.cpu().numpy() for t in (x, y, gain, more)]
+    want_x, want_z, tol_x, tol_z = ref.add_rmsnorm(host[0], host[1], host[2].astype(np.float64), float(np.float32(1e-6)),
+                                                   host[3], None, 0.5, 103)
+    assert np.all(np.abs(out.cpu().numpy() - want_x) <= tol_x)
+    assert np.all(np.abs(z.cpu().numpy() - want_z) <= tol_z)
+
+
+def test_a_long_row_whose_squares_overflow(mq):
+    """The mean is infinite, its root's inverse 0, as in shorter rows."""
+    import torch
+    for n in (1024, 40000):
+        x, gain = torch.full((1, n), 1e19, device="cuda"), torch.ones(n, device="cuda")
+        x[0, 5] = 3e19
+        out, z, _ = mq.mq_add_rmsnorm_quant_q8(x, x, gain, 1e-6)
+        assert torch.equal(out, x + x) and not z.any()
