@@ -111,14 +111,13 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const Residual
         if (q8) quantize4(z, valid, i, q8, a.q8_d_off, a.q8_sum_off);
     };
     if constexpr (K > 0) {
-        constexpr bool kAhead = GATE && K <= 4;
-        float4 x[K], y[K], gate[kAhead ? K : 1];
+        float4 x[K], y[K], gate[GATE ? K : 1];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int i = tid + k * T;
             y[k] = i < n4 ? __ldcg(y4 + i) : zero;
             x[k] = i < n4 ? __ldcg(x4 + i) : zero;
-            if constexpr (kAhead) gate[k] = i < n4 ? __ldcg(gate4 + i) : one;
+            if constexpr (GATE) gate[k] = i < n4 ? __ldcg(gate4 + i) : one;
         }
         float ys = 1.0f;
         if (post4) {
@@ -133,8 +132,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const Residual
             const int i = tid + k * T;
             if (i < n4) {
                 float4 g = one;
-                if constexpr (kAhead) g = gate[k];
-                else if constexpr (GATE) g = __ldcg(gate4 + i);
+                if constexpr (GATE) g = gate[k];
                 x[k] = added(x[k], y[k], g, ys, i);
                 out4[i] = x[k];
             }
@@ -175,14 +173,14 @@ cudaError_t launch_add_rmsnorm(const ResidualLaunch &a, int pdl, cudaStream_t st
     const int n4 = a.n / 4;
     int k = 1;
     // as many threads as a CTA has: the fewest groups a lane (one row of 5120 in 640 threads 3.5 us, in 320 4.5; 4096 rows
-    // 72.8 and 73.0)
-    while (k < 8 && (n4 + k - 1) / k > kMaxThreads) k *= 2;
+    // 72.8 and 73.0). Four at the most: eight spill (1000 rows of 20480: 82 us where reading x' again takes 69, with a norm
+    // behind the block and a gate 129 and 102; of 32768 123 and 107, 177 and 158).
+    while (k < 4 && (n4 + k - 1) / k > kMaxThreads) k *= 2;
     const int threads = ((n4 + k - 1) / k + 31) / 32 * 32;
     if (threads > kMaxThreads) return launch_k<0>(a, kMaxThreads, pdl, st);
     return k == 1   ? launch_k<1>(a, threads, pdl, st)
            : k == 2 ? launch_k<2>(a, threads, pdl, st)
-           : k == 4 ? launch_k<4>(a, threads, pdl, st)
-                    : launch_k<8>(a, threads, pdl, st);
+                    : launch_k<4>(a, threads, pdl, st);
 }
 
 }  // namespace mq
