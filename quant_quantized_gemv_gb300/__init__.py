@@ -964,11 +964,14 @@ def mq_add_rmsnorm_quant_q8(x, y, gain, eps: float, post_gain=None, gate=None, s
     given), z = rms_norm(x_out) * gain and z's q8 planes.  Returns (x_out, z, q8).
 
     x, y: [nt, n] or [n] f32; gain, post_gain: [n]; gate: [n], or [nt, n] with
-    any row stride.  x_out may be x (in place), z may be y."""
+    any row stride.  x_out may be x (in place), z may be y.  z or q8 False: it
+    is not wanted, neither made nor written (None in what is returned)."""
     import torch
     x_out = _made(x, x.shape, x.dtype, stream) if x_out is None else x_out
-    z = _made(x, x.shape, x.dtype, stream) if z is None else z
-    if q8 is None:
+    z = _made(x, x.shape, x.dtype, stream) if z is None else None if z is False else z
+    if q8 is False:
+        q8 = None
+    elif q8 is None:
         n = x.shape[-1]
         q8 = _made(x, (x.numel() // max(n, 1) * mq_q8_bytes(n),), torch.uint8, stream)
     (_calls or _bind()).add_rmsnorm(x, y, gain, eps, post_gain, gate, scale, x_out, z, q8,

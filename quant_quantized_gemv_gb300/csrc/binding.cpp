@@ -327,7 +327,7 @@ PyObject *add_rmsnorm(PyObject *const *a, Py_ssize_t n)
     r.nt = (int)nt, r.n = (int)cols;
     if (!launch_stream(a[10], dev, &stream) || !dense(a[0], "x", nt, cols, dev, &r.x) ||
         !dense(a[1], "y", nt, cols, dev, &r.y) || !dense(a[7], "x_out", nt, cols, dev, &r.x_out) ||
-        !dense(a[8], "z", nt, cols, dev, &r.z) || !vec(a[2], "gain", kF32, cols, dev, &r.gain) ||
+        (a[8] != Py_None && !dense(a[8], "z", nt, cols, dev, &r.z)) || !vec(a[2], "gain", kF32, cols, dev, &r.gain) ||
         !vec(a[4], "post_gain", kF32, cols, dev, &r.post_gain) || !vec(a[9], "q8", kU8, -1, dev, &q8, &q8_n) ||
         !number(a[3], &r.eps) || !number(a[6], &r.scale))
         return nullptr;
@@ -340,7 +340,7 @@ PyObject *add_rmsnorm(PyObject *const *a, Py_ssize_t n)
             return nullptr;
         }
     }
-    if (cols > 0 && q8_n < nt * (long long)g.q8_bytes((int)cols)) {
+    if (a[9] != Py_None && cols > 0 && q8_n < nt * (long long)g.q8_bytes((int)cols)) {
         PyErr_Format(PyExc_ValueError, "q8: smaller than %lld planes of %lld values", nt, cols);
         return nullptr;
     }

@@ -200,7 +200,7 @@ def test_long_rows_of_equal_magnitudes(mq, n, post):
     x, y = ((torch.randint(0, 2, (1, n), device="cuda", generator=g) * 2 - 1) * v for v in (1.1, 0.77))
     x, y = x.float(), y.float()
     gain, more = torch.full((n,), 1.25, device="cuda"), torch.full((n,), 0.75, device="cuda") if post else None
-    out, z, _ = mq.mq_add_rmsnorm_quant_q8(x, y, gain, 1e-6, post_gain=more, scale=0.5)
+    out, z, _ = mq.mq_add_rmsnorm_quant_q8(x, y, gain, 1e-6, post_gain=more, scale=0.5, q8=False)
     host = [None if t is None else t.cpu().numpy() for t in (x, y, gain, more)]
     want_x, want_z, tol_x, tol_z = ref.add_rmsnorm(host[0], host[1], host[2].astype(np.float64), float(np.float32(1e-6)),
                                                    host[3], None, 0.5, 103)
@@ -216,3 +216,19 @@ def test_a_long_row_whose_squares_overflow(mq):
         x[0, 5] = 3e19
         out, z, _ = mq.mq_add_rmsnorm_quant_q8(x, x, gain, 1e-6)
         assert torch.equal(out, x + x) and not z.any()
+
+
+@pytest.mark.parametrize("n", [1024, 33024])
+def test_outputs_that_are_not_wanted(mq, n):
+    import torch
+    c = Case(3, n, True, "row", 0.5)
+    a = c.args(mq)
+    want = mq.mq_add_rmsnorm_quant_q8(**a)
+    out, z, q8 = mq.mq_add_rmsnorm_quant_q8(**{**c.args(mq), "z": False})
+    assert z is None and torch.equal(out, want[0]) and torch.equal(q8, want[2])
+    out, z, q8 = mq.mq_add_rmsnorm_quant_q8(**{**c.args(mq), "q8": False})
+    assert q8 is None and torch.equal(out, want[0]) and torch.equal(z, want[1])
+    with pytest.raises(mq.MQError):
+        mq.mq_add_rmsnorm_quant_q8(**{**c.args(mq), "z": False, "q8": False})
+    with pytest.raises(ValueError):
+        mq.mq_add_rmsnorm_quant_q8(**{**c.args(mq), "q8": want[2][:0]})
