@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
 {
     __shared__ u64 sums[kRestWarps], target_at;
     __shared__ int chunk_at;
-    __shared__ bool last;
-    __shared__ u64 chunk_sums[kVerifyChunks];
+    __shared__ bool last, from_p;
+    __shared__ double part_at;         // of a chunk's sum that lies before the draw
     __shared__ float found[kRestPer];  // of the thread that has the token
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int at = blockIdx.x / a.chunks, chunk = blockIdx.x - at * a.chunks;
@@ -330,34 +330,40 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
     Weight weight(__ldcg(&ws.temperature));
     const bool final = draw & 1, infinite = top == INFINITY;
     weight.top = infinite ? 0.0f : top;
-    const Rest rest(all);
+    Rest rest(all);
     const Row r(a.logits + row * a.stride, a.vocab);
     const float *q = a.draft_probs && !final ? a.draft_probs + row * a.q_stride - r.shift : nullptr;
     const bool fours = q && ((uintptr_t)q & 15) == 0;
     float v[kRestPer];
-    const Fast fast(weight, weight.top);
-    const float least = 0x1p-10f / rest.ih;
-    // v: what is left of this thread's values of a chunk (none: nothing is taken off), fours kRestThreads apart or
-    // consecutive. Everything is on its way before the first value is used.
+    Fast fast(weight, weight.top);
+    float least = 0x1p-10f / rest.ih;
+    // v: what is left of this thread's values of a chunk of places, fours kRestThreads apart or consecutive; or (of_p)
+    // their weights alone, of a chunk of tokens, as the first pass has them. Everything is on its way before the first value is
+    // used.
     auto place_in = [&](auto consecutive, int c, int k) {
         return c * kVerifyChunk + (decltype(consecutive)::value ? tid * kRestPer + k : (k & ~3) * kRestThreads + tid * 4 + (k & 3));
     };
-    auto left = [&](auto consecutive, int c, bool none) {
+    auto left = [&](auto consecutive, int c, bool of_p) {
         float t[kRestPer];  // what the draft takes off
-        auto place = [&](int k) { return place_in(consecutive, c, k); };
+        auto place = [&](int k) { return place_in(consecutive, c, k) + (of_p ? r.shift : 0); };
         const bool whole = r.whole(c);
         unsigned heavy = 0;
+        if (of_p) {
 #pragma unroll
-        for (int k = 0; k < kRestPer; k += 4) {
-            const float4 f = whole ? __ldcg(reinterpret_cast<const float4 *>(r.src + place(k))) : r.four(place(k), -INFINITY);
-            v[k] = f.x, v[k + 1] = f.y, v[k + 2] = f.z, v[k + 3] = f.w;
+            for (int k = 0; k < kRestPer; ++k) v[k] = place(k) < r.hi ? __ldcg(r.src + place(k)) : -INFINITY;
+        } else {
+#pragma unroll
+            for (int k = 0; k < kRestPer; k += 4) {
+                const float4 f = whole ? __ldcg(reinterpret_cast<const float4 *>(r.src + place(k))) : r.four(place(k), -INFINITY);
+                v[k] = f.x, v[k + 1] = f.y, v[k + 2] = f.z, v[k + 3] = f.w;
+            }
         }
 #pragma unroll
         for (int k = 0; k < kRestPer; k += 4) {
             const int p = place(k);
-            if (none || !q) {
+            if (of_p || !q) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) t[k + i] = !none && !final && p + i - r.shift == draft ? 1.0f : 0.0f;
+                for (int i = 0; i < 4; ++i) t[k + i] = !of_p && !final && p + i - r.shift == draft ? 1.0f : 0.0f;
             } else if (fours && (whole || (p >= r.lo && p + 4 <= r.hi))) {
                 const float4 f = __ldcg(reinterpret_cast<const float4 *>(q + p));
                 t[k] = f.x, t[k + 1] = f.y, t[k + 2] = f.z, t[k + 3] = f.w;
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
             const int k = __ffs(heavy) - 1, p = place(k & ~3) + (k & 3);
             float x = __ldcg(r.src + p), none_left, exact;
             if (infinite) x = x == INFINITY ? 0.0f : -INFINITY;
-            const float taken = none ? 0.0f : q ? __saturatef(__ldcg(q + p)) : !final && p - r.shift == draft ? 1.0f : 0.0f;
+            const float taken = of_p ? 0.0f : q ? __saturatef(__ldcg(q + p)) : !final && p - r.shift == draft ? 1.0f : 0.0f;
             rest(weight, x, x, taken, taken, exact, none_left);
 #pragma unroll
             for (int i = 0; i < kRestPer; ++i)
@@ -400,37 +406,20 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
         }
         return ((u64)sum_hi << 22) + (u64)(long long)sum_lo;
     };
-    // The CTA's sum of `mine`, in thread 0.
-    auto cta_sum = [&](u64 mine) {
-        mine = warp_sum(mine);
-        if (lane == 0) sums[warp] = mine;
-        __syncthreads();
-        u64 s = 0;
-        if (tid == 0)
-#pragma unroll
-            for (int w = 0; w < kRestWarps; ++w) s += sums[w];
-        return s;
-    };
     left(std::false_type(), chunk, false);
-    const u64 chunk_sum = cta_sum(own_sum());
+    const u64 mine = warp_sum(own_sum());
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
     if (tid == 0) {
-        ws.rest[chunk] = chunk_sum;
+        u64 s = 0;
+#pragma unroll
+        for (int w = 0; w < kRestWarps; ++w) s += sums[w];
+        ws.rest[chunk] = s;
         last = arrive(&ws.rest_met, 1) + 1 == (unsigned)a.chunks;
         if (last) ws.rest_met = 0;
     }
     __syncthreads();
     if (!last) return;
-
-    // ---- nothing is left (probabilities that are none): from p itself, whose sums this CTA forms chunk by chunk
-    for (int c = tid; c < a.chunks; c += kRestThreads) chunk_sums[c] = __ldcg(&ws.rest[c]);
-    const bool none = !__syncthreads_or(tid < a.chunks && chunk_sums[tid] != 0);
-    if (none)
-        for (int c = 0; c < a.chunks; ++c) {
-            left(std::false_type(), c, true);
-            const u64 s = cta_sum(own_sum());
-            if (tid == 0) chunk_sums[c] = s;
-            __syncthreads();
-        }
 
     // ---- the token: its chunk, by one warp
     if (warp == 0) {
@@ -438,10 +427,21 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
 #pragma unroll
         for (int j = 0; j < kVerifyLane; ++j) {
             const int c = lane + 32 * j;
-            s[j] = c < a.chunks ? chunk_sums[c] : 0;
+            s[j] = c < a.chunks ? __ldcg(&ws.rest[c]) : 0;
             total += s[j];
         }
-        total = warp_sum(total);  // (not 0: of p the largest alone has 2^-20)
+        total = warp_sum(total);
+        const bool none = total == 0;  // nothing is left (probabilities that are none): from p itself, by the first pass' sums
+        if (none) {
+#pragma unroll
+            for (int j = 0; j < kVerifyLane; ++j) {
+                const int c = lane + 32 * j;
+                const float t = c < a.chunks ? __ldcg(&ws.chunk[c].top) : -INFINITY;
+                s[j] = t == -INFINITY ? 0 : joined(__ldcg(&ws.chunk[c].sum), t, top, weight);
+                total += s[j];
+            }
+            total = warp_sum(total);
+        }
         const u64 target = u_draw > 0.0f ? (u_draw < 1.0f ? share_of(u_draw, total, false) : total - 1) : 0;
         u64 before = 0;
 #pragma unroll
@@ -453,13 +453,17 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
                 if (lane >= o) to += u;
             }
             if (before + to - s[j] <= target && target < before + to)
-                chunk_at = lane + 32 * j, target_at = target - (before + to - s[j]);
+                chunk_at = lane + 32 * j, target_at = target - (before + to - s[j]), part_at = (double)target_at / (double)s[j], from_p = none;
             before += __shfl_sync(kAll, to, 31);
         }
     }
     __syncthreads();
     // and in it, in the order of the vocabulary
-    left(std::true_type(), chunk_at, none);
+    if (from_p) {  // weights in units of the chunk's largest, which has one then: the chunk has a sum
+        if (!infinite) weight.top = __ldcg(&ws.chunk[chunk_at].top);
+        fast = Fast(weight, weight.top), rest.ih = 1.0f, rest.il = 0.0f, least = 0x1p-10f;
+    }
+    left(std::true_type(), chunk_at, from_p);
     const u64 own = own_sum();
     u64 to = own;
 #pragma unroll
@@ -469,12 +473,15 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
     }
     if (lane == 31) sums[warp] = to;
     __syncthreads();
-    u64 before = to - own;
+    u64 before = to - own, total = 0;
 #pragma unroll
-    for (int w = 0; w < kRestWarps; ++w)
+    for (int w = 0; w < kRestWarps; ++w) {
         if (w < warp) before += sums[w];
-    // (the chunk's sum is of the same integers: it ends behind the target)
-    const u64 target = target_at;
+        total += sums[w];
+    }
+    // (what is left has the same integers in both passes: their sum ends behind the target; p's are the first pass' to some
+    // 2^-22, and go by the part of the sum)
+    const u64 target = from_p ? min((u64)(part_at * (double)total), total - 1) : target_at;
     if (before <= target && target < before + own) {
         int token = -1;
 #pragma unroll
@@ -482,7 +489,7 @@ __global__ void __launch_bounds__(kRestThreads, 2) verify_rest_kernel(const Veri
 #pragma unroll 1
         for (int k = 0; k < kRestPer; ++k) {
             const u64 w = fixed_of(found[k]);
-            if (before <= target && target < before + w) token = place_in(std::true_type(), chunk_at, k) - r.shift;
+            if (before <= target && target < before + w) token = place_in(std::true_type(), chunk_at, k) - (from_p ? 0 : r.shift);
             before += w;
         }
         a.tokens[row] = token;

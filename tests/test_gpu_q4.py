@@ -513,16 +513,16 @@ def test_scales_that_change_along_a_sequence(mq, d, order):
     c.check(c.run())
 
 
-@pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("shift", [0, -9, -20])
-def test_every_bit_of_a_weight_shows_at_every_scale(mq, d, shift):
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("of,shift", [("queries", 0), ("weights", 0), ("weights", -9), ("weights", -20)])
+def test_every_bit_shows_at_every_scale(mq, d, of, shift):
     """Two tokens alone matter (oracle.decode.TwoTokens) and nothing is allowed for but what its bound counts, under value
     scales of 1, 2^-9 and 2^-20."""
-    g, hq, hkv, nt = synth.rng("q4 bits", d, shift), 10, 2, 24
+    g, hq, hkv, nt = synth.rng("q4 bits", d, of, shift), 10, 2, 24
     lens = g.integers(17, 200, nt)
     c = Q4(mq, d, hq, hkv, 16, lens)
     rng = np.random.default_rng(int(g.integers(1 << 30)))
-    cases = [ref.TwoTokens(rng, hq, hkv, d, int(n), "weights") for n in lens]
+    cases = [ref.TwoTokens(rng, hq, hkv, d, int(n), of) for n in lens]
     for x, name in ((0, "k"), (1, "v")):
         vals = np.zeros(c.codes[x].shape)
         for i, t in enumerate(cases):

@@ -649,3 +649,25 @@ def test_starts_that_overlap(mq, v, starts):
             status = torch.zeros(1, dtype=torch.int32, device="cuda")
             t, n = c.run(mq, starts=dev(np.int32(starts)), status=status)
             assert int(status) == 1 and (t == -9).all() and (n == -9).all()
+
+
+@pytest.mark.parametrize("v", [50257, 131071, 152064])
+@pytest.mark.parametrize("probs", [True, False, "ones"])
+def test_many_rows_tokens_at_the_ends_of_chunks(mq, v, probs):
+    """All of a row in one to three tokens beside the borders of 8192: rows that begin anywhere among 16 bytes; what is left of p,
+    p, and p itself where nothing is left."""
+    g = np.random.default_rng(v)
+    c = Case(v, [1, 0, 2, 1] * 5, probs is not False, key=("chunk ends", str(probs)))
+    c.logits[:] = -60.0
+    for r in range(c.rows):
+        at = 8192 * int(g.integers(1, v // 8192 + 1)) + np.arange(-2, 2)[r % 4] + np.array([0, 1, 5])[:1 + r // 4 % 3]
+        c.logits[r, at] = g.uniform(-2, 0, len(at))
+        c.drafts[r] = at[0] if r % 2 else 7
+    c.u[:] = np.float32(1 - 2.0 ** -24 if probs == "ones" else 0.5)
+    if probs:
+        c.q[:] = 1.0 if probs == "ones" else 0.0
+        c.q[np.arange(c.rows), c.drafts] = 1.0
+    c.u_draw = np.resize(np.float32([0.5, 0.0, 1 - 2.0 ** -24, 0.25, 0.9]), c.n)
+    t, n = (x.cpu().numpy() for x in c.run(mq))
+    for i in range(c.n):
+        borders(c, t, n, i)
