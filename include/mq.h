@@ -582,7 +582,7 @@ int mq_device_sms(void);
 #define MQ_KV_Q4 5
 
 typedef struct {
-    int type;              /* MQ_KV_F16, MQ_KV_BF16 or MQ_KV_Q8            */
+    int type;              /* MQ_KV_F16, MQ_KV_BF16, MQ_KV_Q8 or MQ_KV_Q4  */
     int n_pages, page_size, n_kv_heads, head_dim;
     void *k, *v;           /* the pages (device, 16-byte aligned)          */
     long long page_stride; /* bytes between pages; 0: back to back         */
@@ -857,7 +857,8 @@ int mq_add_rmsnorm_quant_q8(const mq_add_rmsnorm_args *args, void *stream);
  *   free_pages: n_list page numbers, *n_free of them on the list, the last on top.
  *   held_out, n_free_out: the same after the call; may be held and n_free.
  * Nothing else may overlap.  Rolling back (fewer cached tokens than before) keeps
- * the pages held.
+ * the pages held.  The launch is one cluster of up to 16 CTAs, which a whole GB300
+ * holds; where a partition does not, it is MQ_ERR_CUDA.
  * Shapes: 1 <= n_seqs <= MQ_ASSIGN_MAX_SEQS; 1 <= nt, pages_stride, n_list < 2^26;
  *   page_size a multiple of 16.  Pointers 4-byte aligned.
  * Errors: MQ_ERR_NULL, MQ_ERR_SHAPE, MQ_ERR_ALIGN, MQ_ERR_CUDA.

@@ -14,7 +14,7 @@
 // head, 8 query heads 28 us, 16 41 us (q8 25 and 37); one row of 32768, 40 and 8
 // heads, 28 us, 4 such rows of one sequence 64 us.
 //
-// Each warp streams its tokens, 16 at a time (a tile), through stages of its
+// Each warp streams its tokens, 16 at a time (a tile; q4: 32 or 64), through stages of its
 // own in shared memory, filled by 16-byte asynchronous copies: no warp waits for
 // another between a unit's first token and its last, and a warp's next tiles are
 // on their way, into the next unit too, while it works on one.  Rows are stored
@@ -38,7 +38,7 @@
 // scores; the scales of V multiply p, block by block, in units of the largest
 // power of two met so far, to stay in fp16's range.
 // q4: value = scale (code - 8), a code half a byte, two of them to fp16 by a mask and a subtraction.  (As
-//   subnormals, by the mask alone, with the 8s taken off the sums: 90.5 us where it takes 100 below, but the sums lose
+//   subnormals, by the mask alone, with the 8s taken off the sums: 90.5 us where it takes 101 below, but the sums lose
 //   bits where the 8s come off and in the products of subnormals, and outputs were off by 10^-5, now by 4 x 10^-7.)  K: a
 //   block's products end with the token's scale.  V: p takes the scales, block by block, as q8's does (its fp16 parts
 //   times the scale in half2: hi rounded, the product's rest exact in lo).  The page's order of half bytes is the
@@ -61,11 +61,12 @@
 // Measured (GB300, captured): 16 rows of 16384 tokens, 40 and 8 heads of 128:
 // f16 and bf16 159 us, 6.68 TB/s of the cache, the rate of a plain copy; q8 117
 // us, 4.9 TB/s, bound by 650 instructions a tile (f16: 360), a quarter of them
-// to turn codes into fp16; q4 100 us, 3.0 TB/s (its 299 MB take 44): some 400
-// instructions for 16 tokens, and two warps a scheduler, as a tile of 64 tokens fills
-// the registers, wait for each other's chains of conversions and products.  q4, 61 rows
-// of 0 to 8100 tokens, 28 and 4 heads: 26.7 us, of which the bytes take 5: units'
-// beginnings and ends.  One row of 32768 tokens, f16: 28.5 us, where the bytes
+// to turn codes into fp16; q4 101 us, 2.9 TB/s (its 299 MB take 44): 460 instructions
+// for 16 tokens with units' starts and ends, and two warps a scheduler, as a tile of 64
+// tokens fills the registers, wait for each other's chains of conversions and products
+// (half of the issue slots, 28% of the tensor pipe).  q4, heads of 256, 16 x 8192: 102
+// us, 36 bytes a thread spilled.  q4, 61 rows of 0 to 8100 tokens, 28 and 4 heads: 27.6
+// us, of which the bytes take 5: units' beginnings and ends.  One row of 32768 tokens, f16: 28.5 us, where the bytes
 // take 20; of the rest 3 us pass before the first copy (length, page, launch)
 // and 3 in the join.  One row of 117 tokens: 5.1 us, all of it latency.
 #include <cuda_bf16.h>

@@ -224,7 +224,8 @@ cudaError_t launch_rope_append(RopeAppendLaunch a, int sms, int pdl, cudaStream_
 constexpr int kAttnHeads = 8;        // query heads of a CTA (rows of its matrix products)
 // Tokens a warp takes at a time.  q4, whose tile has the same steps for a sum's rescaling, a block's scales and a unit of
 // queries however many tokens it has: as many as the registers hold.  16 rows of 16384 tokens, 40 and 8 heads: of 128, 32
-// tokens and 12 warps 102.6 us, 64 and 8 warps 99.7; of 96, 84.2 and 81.8; of 64, 32 and 16 warps 63.8, 64 and 12 warps 61.9 (now 60.6).
+// tokens and 12 warps 102.6 us, 64 and 8 warps 99.7 (now 101.4); of 96, 84.2 and 81.8 (83.5); of 64, 32 and 16 warps
+// 63.8, 64 and 12 warps 61.9 (62.5).
 __host__ __device__ constexpr int attn_tile(int type, int head_dim) { return type != 5 ? 16 : head_dim <= 128 ? 64 : 32; }
 constexpr int kAttnMaxRows = 1024;
 constexpr int kAttnMaxCtas = 256;    // CTAs that share out the work

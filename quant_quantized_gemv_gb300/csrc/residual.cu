@@ -12,8 +12,8 @@
 // What bounds it (captured): one row of 5120, the launch, one load and two exchanges, 3.5 us (with a norm behind the block
 // 4.6). 4096 rows of 5120, 360 MB: 55.5 us, 6.5 TB/s, the rate of a copy; with a norm behind the block and a gate for
 // each row, 444 MB: 72.8 us, 6.1 TB/s. 8000 rows of 1024: 26 us, 5.4 TB/s: the CTAs' beginnings (a row a warp,
-// without barriers, 34 us). 2000 rows of 13824: 106 us, 4.5 TB/s: one CTA of 864 threads an SM, whose loads wait for
-// its sums.
+// without barriers, 34 us). 2000 rows of 13824: 104 us, 4.5 TB/s: one CTA of 864 threads an SM, whose loads wait for
+// its sums. 1000 rows of 20480: 69.5 us, 5.1 TB/s, with gate and norm 101.5, 4.3 TB/s: x' once more from L2.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -39,9 +39,10 @@
 // one CTA, decide whether it stands. A row that does not stand, or is its sequence's last, draws at once from what is left of
 // the kept weights, whether or not a row before it has; the sequence's last row to arrive (an atomic count; nobody
 // waits) writes down which tokens count.  Many rows without a filter go by verify_stream.cu.  Captured, rows of
-// 152064: 5 rows 11.3 us, top-k 40 13.9, top-p 0.95 22.6, 29.7 where one is refused; 10 rows, top-k 40, 17; 21 of 50257, top-k 40, 15: the
-// barriers, as with a draw, and the last row's two dependent loads behind its count.  112 rows: top-k 40 80 us, top-p
-// 0.9 168: the passes of a draw and one over the draft's probabilities, in two waves of clusters.
+// 152064: 5 rows 11.3 us, top-k 40 13.8, top-p 0.95 22.7, 30 where one is refused; 10 rows, top-k 40, 17; 21 of 50257,
+// top-k 40, 15.4: the barriers, as with a draw, and the last row's two dependent loads behind its count.  112 rows: top-k 40
+// 80 us, top-p 0.9 171: the passes of a draw and one over the draft's probabilities, in two waves of clusters.  (The
+// verification's kernel keeps 16 bytes a thread outside its 64 registers, which hold two CTAs an SM.)
 //
 // What bounds it: with many rows the load, the count and step 4's pass one after
 // another (64 rows of 152064, flat, top-p 0.9: 63 us, of which loads 6, some 90
@@ -1368,7 +1369,7 @@ int cluster_for(int nt, int vocab, int sms)
 // Logits of a verification from which on the rows without a filter go by chunks, where there are arrays of filters (which
 // the host cannot look into) and where there are none.  Captured, us, rows of 152064 tokens by clusters / by chunks: without
 // arrays 5 rows 11.3 / 16, 10 rows 18.5 / 18, 20 rows 47 / 21, 40 rows 35 / 26; of 32000, 20 rows 13.9 / 16.1, 40
-// rows 27 / 19.  With arrays that filter nothing 10 rows 18.7 / 21, 20 rows 47 / 23, 40 rows 38 / 28; where all filter, the
+// rows 27 / 19.  With arrays that filter nothing 10 rows 18.7 / 21, 20 rows 47 / 22.5, 40 rows 38 / 27.6; where all filter, the
 // chunks' kernels find nothing to do: top-k 40, 10 rows 17 / 24, 20 rows 21 / 25, 112 rows 65 / 80.
 constexpr long long kStreamLeast = 2 << 20, kStreamLeastPlain = 1 << 20;
 

@@ -11,7 +11,7 @@
 // A temperature of 0 takes no second pass: a chunk leaves the first place of its largest logit in place of a sum.
 // Rows with a filter are left to the clusters.
 //
-// What bounds it: 112 rows of 152064, 69 MB of logits and 20 MB of probabilities, which take 13 us: 42 us captured. The
+// What bounds it: 112 rows of 152064, 69 MB of logits and 20 MB of probabilities, which take 13 us: 42.3 us captured. The
 // sums 20 of them (3.5 TB/s): a CTA's row ends, each with barriers, an atomic and the next row's sequence, and what a
 // launch begins and ends with (one warp left behind to finish a row: no faster); the rest 19 in one wave, its loads one
 // behind the other (the sequence's first row, the row, the logits; the last CTA the sums, then the chunk again); 3 in the
@@ -19,10 +19,12 @@
 //
 // Sums: a lane's 32 weights (of tokens 32 apart, wherever among 16 bytes the row begins) in f32, a weight of 2^-t of the
 // largest being off by (t 2^-23.5 + 2^-22) of itself at the most (the difference of two logits, its factor, ex2.approx);
-// everything above in integers of 2^-42 of the chunk's largest, times that one's weight in the row. In the second pass what is left of a token is rounded to units of 2^-42 of the row by itself,
-// so that the pass that finds the chunk and the one that finds the token in it add up the same integers; of tokens that have
-// more than 2^-10 of the row, whose errors would not vanish among the others', it is the draw's weight (32 x 5 rows of
-// 152064: 41.4 us; for every token 45.4).
+// everything above in integers of 2^-42 of the chunk's largest, times that one's weight in the row. In the second pass
+// what is left of a token is rounded to units of 2^-42 of the row by itself, so that the pass that finds the chunk and the one
+// that finds the token in it add up the same integers; of tokens that have more than 2^-10 of the row, whose errors would not
+// vanish among the others', it goes by the draw's weight (for every token: 3 us more). Where nothing is left of p (which
+// probabilities that are none leave), the draw goes by the first pass' sums, and in its chunk by the same part of the chunk's
+// weights: 32 x 2 rows 48 us instead of 35.
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <stdint.h>
