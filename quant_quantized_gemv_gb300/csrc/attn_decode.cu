@@ -293,11 +293,11 @@ constexpr int kQ4Group = D / 32 < 4 ? D / 32 : 4;
 // Scores: a block's products end with the token's scale. Output: p's two parts take V's scales, block by block.
 // The products of p and a scale are fp16 parts, which hold the bits of f32 where the largest are well above fp16's
 // subnormals. p is in units of 2^-unit: 2^-13, or, for scales of 2 and more, what brings the largest product that the group of
-// blocks has met below 2^14. While no scale of 2^-6 or more has been met (a V of small values; a warp's first tile), the
+// blocks has met below 2^14. While no scale of 2^-11 or more has been met (a V of small values; a warp's first tile), the
 // scales are taken times 2^more, which is exact, for a largest of 1 to 2 (of 2^-9, if all are fp16's least), and the sums are
-// in units of 2^-(unit + more). Without that, V of 10^-5 over 16384 tokens is off by 7 x 10^-5 of itself; it takes 1 to 3% of
-// the time (16 x 16384 tokens: 99.8 -> 101.4 us). The whole tile goes through the tensor core before a sum is rescaled and
-// added to.
+// in units of 2^-(unit + more): 16 x 16384 tokens are off by 2 x 10^-7 for V of 1 and of 10^-6, where V of 10^-5 was off by 9 x
+// 10^-6 and of 10^-6 by 8 x 10^-5. It takes 1 to 3% of the time, 8 to 10% where V is that small (so not from 2^-6 on, which
+// was no more exact). The whole tile goes through the tensor core before a sum is rescaled and added to.
 // lo, hi: the tokens that are seen; full: all.
 template <int D, int KC, int TILE>
 __device__ __forceinline__ void q4_tile(Two (&o)[D / 8], float &m, float &l, int (&unit)[KC / kQ4Group<D>], int (&more)[KC / kQ4Group<D>], const uint8_t *stage,
@@ -407,7 +407,7 @@ __device__ __forceinline__ void q4_tile(Two (&o)[D / 8], float &m, float &l, int
                 for (int b = 0; b < H; ++b) vs[i][b] = 0;
             }
         }
-        // Scales under 2, as bits, and one of 2^-6 has been met: no change. Else the largest, which is under 2^e.
+        // Scales under 2, as bits, and one of 2^-11 has been met: no change. Else the largest, which is under 2^e.
         unsigned any = 0;
 #pragma unroll
         for (int i = 0; i < 2 * J; ++i)
@@ -423,7 +423,7 @@ __device__ __forceinline__ void q4_tile(Two (&o)[D / 8], float &m, float &l, int
             big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
             big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
             const int e = min((int)(__float_as_uint(big) >> 23) - 126, 17);
-            const int now = min(unit[group], 14 - max(e, 1)), k = e < -5 ? min(more[group], 1 - e) : 0;
+            const int now = min(unit[group], 14 - max(e, 1)), k = e < -10 ? min(more[group], 1 - e) : 0;
             down *= __uint_as_float((unsigned)(127 + now + k - unit[group] - more[group]) << 23);
             unit[group] = now, more[group] = k;
             const __half2 by = half2_of((unsigned)(k + 15) * 0x04000400u);  // 2^k

@@ -514,10 +514,10 @@ def test_scales_that_change_along_a_sequence(mq, d, order):
 
 
 @pytest.mark.parametrize("d", [64, 96, 128, 256])
-@pytest.mark.parametrize("of,shift", [("queries", 0), ("weights", 0), ("weights", -9), ("weights", -20)])
+@pytest.mark.parametrize("of,shift", [("queries", 0), ("weights", 0), ("weights", -10), ("weights", -12), ("weights", -20)])
 def test_every_bit_shows_at_every_scale(mq, d, of, shift):
     """Two tokens alone matter (oracle.decode.TwoTokens) and nothing is allowed for but what its bound counts, under value
-    scales of 1, 2^-9 and 2^-20."""
+    scales of 1 to 2^-20."""
     g, hq, hkv, nt = synth.rng("q4 bits", d, of, shift), 10, 2, 24
     lens = g.integers(17, 200, nt)
     c = Q4(mq, d, hq, hkv, 16, lens)
